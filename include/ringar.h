@@ -449,6 +449,139 @@ ringar_result_t ringar_chunk_range(size_t count, ringar_dtype_t dtype, int nrank
                                    size_t chunk_elems, int c, size_t loop_off, int k,
                                    size_t* lo, size_t* hi, size_t* klo, size_t* khi);
 
+/*
+ * Block operators: what a tensor-parallel transformer block computes between
+ * two AllReduces.  Each rank's share runs through these calls and the
+ * AllReduce adds the partial products (one rank passes the bias and the
+ * residual) or averages the parameter gradients.
+ *
+ * All of them: dtype is RINGAR_FLOAT16, RINGAR_BFLOAT16 or RINGAR_FLOAT32,
+ * every sum is held in fp32 and every output is rounded once (dz, the
+ * activation's gradient that the backward products read, is rounded to dtype
+ * too).  Matrices are row-major with a row stride in elements (ld; at least
+ * the row's length, or 0 on an input to repeat one row), at any element
+ * alignment; rows starting at 16-byte boundaries with in_features a multiple
+ * of 16 bytes take the fast path.  Sizes lie in 0 .. 2^31 - 1; no rows is a
+ * successful call that writes zeros to the parameter gradients.  An output
+ * must not overlap another operand (RINGAR_ERR_INVALID_USAGE) except where
+ * said.  Results do not depend on scheduling (no atomic sums).
+ *
+ * Calls enqueue on `stream` and return; the caller keeps the operands until
+ * the work is done.  Workspaces are the library's, one per stream, grown as
+ * needed (growing waits for the stream) and freed by ringar_release; under
+ * stream capture nothing is allocated: the stream must have run a call of
+ * the same shape first, else RINGAR_ERR_INVALID_USAGE, and a graph must not
+ * be replayed after ringar_release, nor beside other work of its stream.
+ * Zero-initialise the structs, then set fields.
+ */
+typedef enum {
+  RINGAR_ACT_NONE = 0,
+  RINGAR_ACT_RELU = 1,
+  RINGAR_ACT_GELU = 2,      /* z/2 (1 + erf(z / sqrt 2)) */
+  RINGAR_ACT_GELU_TANH = 3, /* its tanh form */
+  RINGAR_ACT_SILU = 4,
+  RINGAR_ACT_SIGMOID = 5
+} ringar_act_t;
+
+/* Layer norm over the last dimension:
+ *   y = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(var + eps),
+ * var the mean square about the mean.  y may be x itself (same row stride). */
+typedef struct {
+  ringar_dtype_t dtype;        /* x, y */
+  ringar_dtype_t param_dtype;  /* weight, bias: dtype or RINGAR_FLOAT32 */
+  int64_t rows, cols;          /* cols >= 1 */
+  const void* x;
+  int64_t ldx;
+  const void* weight;          /* cols values, or NULL = ones */
+  const void* bias;            /* cols values, or NULL = zeros */
+  float eps;
+  void* y;
+  int64_t ldy;
+  float* mean;                 /* rows values each, or NULL */
+  float* rstd;
+} ringar_layer_norm_t;
+
+ringar_result_t ringar_layer_norm(const ringar_layer_norm_t* args, ringar_stream_t stream);
+
+/* Its gradients, from the forward pass's mean and rstd; with g = dy weight
+ * and h = (x - mean) rstd:
+ *   dx = rstd (g - mean(g) - h mean(g h)),
+ *   dweight = sum over rows of dy h,  dbias = sum over rows of dy.
+ * Any of dx, dweight, dbias may be NULL (not wanted). */
+typedef struct {
+  ringar_dtype_t dtype;        /* dy, x, dx */
+  ringar_dtype_t param_dtype;  /* weight, dweight, dbias */
+  int64_t rows, cols;
+  const void* dy;
+  int64_t lddy;
+  const void* x;
+  int64_t ldx;
+  const float* mean;
+  const float* rstd;
+  const void* weight;          /* or NULL = ones */
+  void* dx;
+  int64_t lddx;
+  void* dweight;
+  void* dbias;
+} ringar_layer_norm_backward_t;
+
+ringar_result_t ringar_layer_norm_backward(const ringar_layer_norm_backward_t* args, ringar_stream_t stream);
+
+/* Linear: z = x weight^T + bias, y = act(z) + residual.
+ *   x: rows x in_features; weight: out_features x in_features;
+ *   pre: where z is kept for the backward pass, or NULL;
+ *   residual: rows x out_features, or NULL; y may be the residual itself
+ *   (same row stride).
+ * Gated feed-forward (ringar_gated_ffn): weight and bias hold the gate's
+ * out_features rows, then the up projection's: [g u] = x weight^T + bias,
+ * y = act(g) u; pre (rows x 2 out_features) keeps [g u]; no residual. */
+typedef struct {
+  ringar_dtype_t dtype;
+  ringar_act_t act;
+  int64_t rows, in_features, out_features;
+  const void* x;
+  int64_t ldx;
+  const void* weight;
+  int64_t ldw;
+  const void* bias;            /* or NULL */
+  const void* residual;        /* or NULL */
+  int64_t ldr;
+  void* y;
+  int64_t ldy;
+  void* pre;                   /* or NULL */
+  int64_t ldp;
+} ringar_linear_t;
+
+ringar_result_t ringar_linear(const ringar_linear_t* args, ringar_stream_t stream);
+ringar_result_t ringar_gated_ffn(const ringar_linear_t* args, ringar_stream_t stream);
+
+/* Their gradients.  Linear: dz = dy act'(pre) (dy itself without an
+ * activation: pre is then not read).  Gated: dz = [dy u act'(g), dy act(g)].
+ *   dx = dz weight,  dweight = dz^T x,  dbias = sum over rows of dz.
+ * Any of dx, dweight, dbias may be NULL (not wanted; x is read for dweight
+ * only, weight for dx only). */
+typedef struct {
+  ringar_dtype_t dtype;
+  ringar_act_t act;
+  int64_t rows, in_features, out_features;
+  const void* dy;
+  int64_t lddy;
+  const void* pre;
+  int64_t ldp;
+  const void* x;
+  int64_t ldx;
+  const void* weight;
+  int64_t ldw;
+  void* dx;
+  int64_t lddx;
+  void* dweight;
+  int64_t lddw;
+  void* dbias;
+} ringar_linear_backward_t;
+
+ringar_result_t ringar_linear_backward(const ringar_linear_backward_t* args, ringar_stream_t stream);
+ringar_result_t ringar_gated_ffn_backward(const ringar_linear_backward_t* args, ringar_stream_t stream);
+
 /* Asynchronous errors ([BOOK] §1.4: ncclCommGetAsyncError reports what went
  * wrong after the call returned; [ARCH] §九.5: a kernel only leaves its wait
  * loops through the abort flag).  Waits for `stream`, then returns (and
@@ -469,7 +602,8 @@ ringar_result_t ringar_get_async_error(ringar_stream_t stream);
 /* Resource cleanup, the analogue of ncclCommDestroy ([BOOK] §1.4: free the
  * local resources once nothing uses them any more).  Synchronises every
  * device the library has used and frees every FIFO, counter and error word
- * it allocated (they are re-created on the next call).  Graphs captured
+ * it allocated, and the block operators' workspaces (they are re-created on
+ * the next call).  Graphs captured
  * before this call hold freed addresses: do not replay them.  Returns
  * RINGAR_ERR_DEVICE if a HIP call fails. */
 ringar_result_t ringar_release(void);

@@ -395,3 +395,8 @@ def all_gather(sends, recvs, nchannels=0, proto="auto", stream=None, **cfg_kwarg
     cfg = make_config(**cfg_kwargs) if cfg_kwargs else None
     _check(ringar_all_gather_ex([t.data_ptr() for t in sends], [t.data_ptr() for t in recvs], count,
                                 dtype, n, nchannels, proto, st.cuda_stream, cfg), "ringar_all_gather")
+
+
+# ------------------------------------------------------------------ block operators
+from .block import (gated_ffn, gated_ffn_backward, layer_norm, layer_norm_backward, linear,  # noqa: E402,F401
+                    linear_backward)

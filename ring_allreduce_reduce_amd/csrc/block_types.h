@@ -1,0 +1,183 @@
+// Element types, activations and kernel arguments of the block operators
+// (layer norm, linear, gated feed-forward), shared by their kernels and the
+// host side.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ringar {
+
+// activation codes of the public header
+enum : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4, kActSigmoid = 5 };
+
+// dtype codes of the public header that the block operators take
+enum : int { kF16 = 2, kBF16 = 3, kF32 = 4 };
+
+template <int DT> struct ElemOf;
+template <> struct ElemOf<kF16> { using type = _Float16; };
+template <> struct ElemOf<kBF16> { using type = __bf16; };
+template <> struct ElemOf<kF32> { using type = float; };
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// N elements moved as one access; rows may start at any element, so the
+// alignment promised is the element's own (the hardware takes unaligned
+// global accesses as single ones).
+template <typename T, int N> struct alignas(sizeof(T)) Pack {
+  T v[N];
+};
+template <typename T, int N> __device__ inline Pack<T, N> load_pack(const T* p) {
+  Pack<T, N> r;
+  __builtin_memcpy(&r, p, sizeof(r));
+  return r;
+}
+template <typename T, int N> __device__ inline void store_pack(T* p, const Pack<T, N>& v) {
+  __builtin_memcpy(p, &v, sizeof(v));
+}
+
+// exp and 1/x of the activations: the 16-bit types take the hardware's
+// exponential and reciprocal (relative error about 1e-6 against the 2e-3 of
+// their own rounding), fp32 the full-precision ones.
+template <bool FAST> __device__ inline float act_exp(float x) {
+  if constexpr (FAST) return __builtin_amdgcn_exp2f(x * 1.4426950408889634f);
+  return expf(x);
+}
+template <bool FAST> __device__ inline float act_rcp(float x) {
+  if constexpr (FAST) return __builtin_amdgcn_rcpf(x);
+  return 1.0f / x;
+}
+
+template <bool FAST> __device__ inline float sigmoid_of(float z) { return act_rcp<FAST>(1.0f + act_exp<FAST>(-z)); }
+
+// 2u of the tanh form: gelu_tanh(z) = z sigmoid(2u), u = sqrt(2/pi)(z + 0.044715 z^3)
+constexpr float kGeluA = 1.5957691216057308f;            // 2 sqrt(2/pi)
+constexpr float kGeluB = 0.044715f;
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+
+template <bool FAST> __device__ inline float activate(int act, float z) {
+  switch (act) {
+    case kActRelu: return z < 0.0f ? 0.0f : z;            // NaN stays NaN
+    case kActGelu: return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+    case kActGeluTanh: return z * sigmoid_of<FAST>(kGeluA * z * (1.0f + kGeluB * z * z));
+    case kActSilu: return z * sigmoid_of<FAST>(z);
+    case kActSigmoid: return sigmoid_of<FAST>(z);
+    default: return z;
+  }
+}
+
+// act(z) and act'(z) together: they share the exponential.
+template <bool FAST> __device__ inline void activate_grad(int act, float z, float* a, float* d) {
+  switch (act) {
+    case kActRelu:
+      *a = z < 0.0f ? 0.0f : z;
+      *d = z > 0.0f ? 1.0f : 0.0f;
+      return;
+    case kActGelu: {
+      const float cdf = 0.5f * (1.0f + erff(z * kSqrtHalf));
+      *a = z * cdf;
+      *d = cdf + z * (act_exp<FAST>(-0.5f * z * z) * kInvSqrt2Pi);
+      return;
+    }
+    case kActGeluTanh: {
+      const float zz = z * z;
+      const float s = sigmoid_of<FAST>(kGeluA * z * (1.0f + kGeluB * zz));
+      *a = z * s;
+      *d = s + z * (s * (1.0f - s)) * (kGeluA * (1.0f + 3.0f * kGeluB * zz));
+      return;
+    }
+    case kActSilu: {
+      const float s = sigmoid_of<FAST>(z);
+      *a = z * s;
+      *d = s * (1.0f + z * (1.0f - s));
+      return;
+    }
+    case kActSigmoid: {
+      const float s = sigmoid_of<FAST>(z);
+      *a = s;
+      *d = s * (1.0f - s);
+      return;
+    }
+    default:
+      *a = z;
+      *d = 1.0f;
+  }
+}
+
+// ------------------------------------------------------------- layer norm
+struct NormArgs {
+  const void* x;
+  const void* dy;        // backward
+  const void* weight;    // null: ones
+  const void* bias;      // null: zeros (forward)
+  void* y;               // forward: y; backward: dx (may be null)
+  float* mean;           // forward: may be null; backward: inputs
+  float* rstd;
+  float* part;           // backward: partial sums [2][groups][cols], or null
+  int64_t ldx, lddy, ldy;
+  int64_t rows;
+  int cols;
+  int groups;            // blocks of the backward grid
+  float eps;
+  float inv_cols;
+};
+
+// ------------------------------------------------- products and their epilogue
+// C[m][n] = sum_k A[m][k] B[n][k], the operands at any pair of strides.
+// Gated: n counts 2 * ceil16(F) logical columns in groups of 32, 16 gate
+// columns and then the same 16 up columns.
+enum : int { kEpiStore = 0, kEpiLinear = 1, kEpiGated = 2 };
+
+struct GemmArgs {
+  const void* a;
+  const void* b;
+  int64_t sam, sak;      // strides of A in elements
+  int64_t sbn, sbk;      // strides of B
+  int m, n, k;           // n: output columns (gated: F)
+  int splits;            // parts of k, each a multiple of the tile's k
+  int k_per_split;
+  float* part;           // splits > 1: [splits][m][logical n]
+  // epilogue
+  const void* bias;      // n (gated: 2F), or null
+  const void* residual;  // or null
+  void* c;
+  void* pre;             // or null
+  int64_t ldc, ldr, ldp;
+  int act;
+};
+
+__host__ __device__ inline int64_t logical_cols(int epi, int64_t n) { return epi == kEpiGated ? (n + 15) / 16 * 32 : n; }
+
+// activation's backward pass and column sums
+struct DzArgs {
+  const void* dy;        // [rows][n]
+  const void* pre;       // [rows][n], gated [rows][2n]
+  void* dz;              // [rows][n], gated [rows][2n]; null: not wanted
+  float* part;           // [groups][n or 2n] partial column sums, or null
+  int64_t lddy, ldp, lddz;
+  int64_t rows;
+  int n;
+  int groups;
+  int act;
+  int gated;
+};
+
+// out[c] = sum over p of part[p][c]
+struct ColSumArgs {
+  const float* part;
+  void* out;
+  int parts;
+  int64_t cols;
+};
+
+// the kernels' launchers (dtype codes of the public header)
+hipError_t launch_norm_forward(int dtype, int wdtype, const NormArgs& a, hipStream_t st);
+hipError_t launch_norm_backward(int dtype, int wdtype, const NormArgs& a, hipStream_t st);
+int norm_backward_groups(int dtype, int64_t rows, int cols);
+hipError_t launch_col_sum(int out_dtype, const ColSumArgs& a, hipStream_t st);
+hipError_t launch_dz(int dtype, const DzArgs& a, hipStream_t st);
+int dz_groups(int64_t rows, int64_t cols);
+hipError_t launch_gemm(int dtype, int epi, const GemmArgs& a, hipStream_t st);
+
+}  // namespace ringar

@@ -1,0 +1,116 @@
+// The activation's backward pass, with the column sums that become the bias
+// gradient:
+//   linear: dz = dy act'(z)
+//   gated:  dg = dh u act'(g), du = dh act(g)
+// dz is rounded to the operand type once, for the matrix products that read
+// it twice; the sums are taken of the unrounded values.  Memory bound: each
+// thread moves 16-byte packs of one column group down its block's rows.
+#include "block_types.h"
+
+namespace ringar {
+namespace {
+
+template <typename T, bool GATED> __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
+  constexpr int V = 16 / sizeof(T);
+  constexpr bool kFast = sizeof(T) == 2;
+  // a wave takes 64 packs of columns; the block's four waves take rows in turn
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = ((int64_t)blockIdx.x * 64 + lane) * V;
+  float s[V], su[V];
+#pragma unroll
+  for (int j = 0; j < V; j++) s[j] = su[j] = 0.0f;
+  if (c < a.n) {
+    const bool whole = c + V <= a.n;
+    for (int64_t row = (int64_t)blockIdx.y * 4 + wave; row < a.rows; row += (int64_t)a.groups * 4) {
+      Pack<T, V> dy, g, u;
+      const T* pdy = (const T*)a.dy + row * a.lddy + c;
+      const T* pre = (const T*)a.pre + row * a.ldp + c;
+      if (whole) {
+        dy = load_pack<T, V>(pdy);
+        if (a.pre) g = load_pack<T, V>(pre);
+        if constexpr (GATED) u = load_pack<T, V>(pre + a.n);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+          const bool in = c + j < a.n;
+          dy.v[j] = in ? pdy[j] : (T)0.0f;
+          g.v[j] = in && a.pre ? pre[j] : (T)0.0f;
+          if constexpr (GATED) u.v[j] = in ? pre[a.n + j] : (T)0.0f;
+        }
+      }
+      Pack<T, V> og, ou;
+#pragma unroll
+      for (int j = 0; j < V; j++) {
+        float act = 0.0f, d = 1.0f;
+        const float e = (float)dy.v[j];
+        if (GATED || a.pre) activate_grad<kFast>(a.act, (float)g.v[j], &act, &d);
+        if constexpr (GATED) {
+          const float dg = e * (float)u.v[j] * d, du = e * act;
+          s[j] += dg;
+          su[j] += du;
+          og.v[j] = (T)dg;
+          ou.v[j] = (T)du;
+        } else {
+          s[j] += e * d;
+          og.v[j] = (T)(e * d);
+        }
+      }
+      if (a.dz) {
+        T* o = (T*)a.dz + row * a.lddz + c;
+        if (whole) {
+          store_pack<T, V>(o, og);
+          if constexpr (GATED) store_pack<T, V>(o + a.n, ou);
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; j++)
+            if (c + j < a.n) {
+              o[j] = og.v[j];
+              if constexpr (GATED) o[a.n + j] = ou.v[j];
+            }
+        }
+      }
+    }
+  }
+  if (!a.part) return;
+  __shared__ float smem[4][64 * V];
+  const int64_t cols = GATED ? 2 * (int64_t)a.n : a.n;
+#pragma unroll
+  for (int which = 0; which < (GATED ? 2 : 1); which++) {
+    if (which) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < V; j++) smem[wave][lane * V + j] = which ? su[j] : s[j];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 64 * V; i += 256) {
+      const int64_t col = (int64_t)blockIdx.x * 64 * V + i;
+      if (col < a.n)
+        a.part[blockIdx.y * cols + (which ? a.n : 0) + col] = (smem[0][i] + smem[1][i]) + (smem[2][i] + smem[3][i]);
+    }
+  }
+}
+
+template <typename T> hipError_t launch(const DzArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)((a.n + 64 * (16 / sizeof(T)) - 1) / (64 * (16 / sizeof(T)))), a.groups);
+  if (a.gated) hipLaunchKernelGGL((dz_kernel<T, true>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((dz_kernel<T, false>), grid, dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// Row groups: enough blocks to fill the GPU (about 2048 with the column
+// groups), no more than the rows hold.
+int dz_groups(int64_t rows, int64_t n) {
+  const int64_t column_blocks = (n + 511) / 512;
+  int64_t g = 2048 / column_blocks;
+  const int64_t most = (rows + 3) / 4;
+  if (g > most) g = most;
+  return (int)(g < 1 ? 1 : g);
+}
+
+hipError_t launch_dz(int dtype, const DzArgs& a, hipStream_t st) {
+  if (dtype == kF32) return launch<float>(a, st);
+  if (dtype == kF16) return launch<_Float16>(a, st);
+  return launch<__bf16>(a, st);
+}
+
+}  // namespace ringar

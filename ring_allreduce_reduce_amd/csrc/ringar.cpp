@@ -21,6 +21,7 @@
 #include <utility>
 #include <vector>
 
+#include "op_host.h"
 #include "ringar.h"
 #include "ring_geometry.h"
 #include "ring_kernel.h"
@@ -850,6 +851,10 @@ ringar_result_t check_ring(const int* ring, int n) {
 
 }  // namespace
 
+namespace ringar {
+std::string& last_error_text() { return t_last_error; }
+}
+
 // ====================================================================== ABI
 extern "C" {
 
@@ -1449,6 +1454,7 @@ ringar_result_t ringar_release(void) {
   }
   g_res.clear();
   HIP_TRY(hipSetDevice(cur));
+  if (!release_workspaces()) return RINGAR_ERR_DEVICE;
   return RINGAR_SUCCESS;
 }
 
