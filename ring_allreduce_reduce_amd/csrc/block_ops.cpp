@@ -165,27 +165,9 @@ bool dims_ok(std::initializer_list<int64_t> d) {
 #define VEC(name, p, n, es, out) Mat{name, p, (p) ? 1 : 0, n, n, es, out}
 
 // --------------------------------------------------------------- products
-// Parts of k: enough blocks to fill the GPU where the output has few tiles.
-void choose_splits(GemmArgs& a, int epi, size_t es) {
-  const int64_t step = es == 4 ? 16 : 32;
-  const int64_t tiles = ((logical_cols(epi, a.n) + 63) / 64) * (((int64_t)a.m + 63) / 64);
-  const int64_t steps = (a.k + step - 1) / step;
-  int64_t splits = tiles >= 512 || steps < 16 ? 1 : 1024 / (tiles ? tiles : 1);
-  if (splits > steps / 8) splits = steps / 8;
-  if (splits < 1) splits = 1;
-  const int64_t per = (steps + splits - 1) / splits;
-  a.k_per_split = (int)(per * step);
-  a.splits = (int)(steps ? (steps + per - 1) / per : 1);
-}
-
-size_t part_bytes(const GemmArgs& a, int epi) {
-  return a.splits > 1 ? (size_t)a.splits * a.m * logical_cols(epi, a.n) * 4 : 0;
-}
-
 ringar_result_t run_gemm(int dtype, int epi, const GemmArgs& a, hipStream_t st) {
   if (a.m == 0 || a.n == 0) return RINGAR_SUCCESS;
-  const int64_t tiles = ((logical_cols(epi, a.n) + 63) / 64) * (((int64_t)a.m + 63) / 64);
-  if (tiles * a.splits > kMaxDim) return refuse(RINGAR_ERR_INVALID_USAGE, "the product has more tiles than one launch takes");
+  if (gemm_blocks(dtype, epi, a) > kMaxDim) return refuse(RINGAR_ERR_INVALID_USAGE, "the product has more tiles than one launch takes");
   HIP_TRY(launch_gemm(dtype, epi, a, st));
   return RINGAR_SUCCESS;
 }
@@ -338,10 +320,10 @@ static ringar_result_t product_forward(const ringar_linear_t* p, bool gated, hip
   a.ldr = p->ldr;
   a.ldp = p->ldp;
   a.act = p->act;
-  choose_splits(a, epi, es);
+  const size_t part = plan_gemm(p->dtype, epi, a);
   std::lock_guard<std::mutex> lock(g_ws_mu);
   char* ws = nullptr;
-  TRY(workspace(st, part_bytes(a, epi), &ws));
+  TRY(workspace(st, part, &ws));
   a.part = (float*)ws;
   return run_gemm(p->dtype, epi, a, st);
 }
@@ -394,12 +376,13 @@ static ringar_result_t product_backward(const ringar_linear_backward_t* p, bool 
   gw.k = (int)p->rows;
   gw.c = p->dweight;
   gw.ldc = p->lddw;
-  choose_splits(gx, kEpiStore, es);
-  choose_splits(gw, kEpiStore, es);
+  // a workspace starts at a 256-byte boundary, like this stand-in for it
+  gx.a = gw.a = need_dz ? (const void*)256 : p->dy;
+  gx.sam = gw.sak = need_dz ? z.lddz : p->lddy;
   Layout l;
   const size_t at_dz = l.add(need_dz ? (size_t)p->rows * z.lddz * es : 0);
   const size_t at_sum = l.add(p->dbias ? (size_t)z.groups * wide * 4 : 0);
-  const size_t bx = p->dx ? part_bytes(gx, kEpiStore) : 0, bw = p->dweight ? part_bytes(gw, kEpiStore) : 0;
+  const size_t bx = p->dx ? plan_gemm(p->dtype, kEpiStore, gx) : 0, bw = p->dweight ? plan_gemm(p->dtype, kEpiStore, gw) : 0;
   const size_t at_part = l.add(bx > bw ? bx : bw);
   std::lock_guard<std::mutex> lock(g_ws_mu);
   char* ws = nullptr;
@@ -408,8 +391,7 @@ static ringar_result_t product_backward(const ringar_linear_backward_t* p, bool 
   if (need_dz) z.dz = ws + at_dz;
   if (p->dbias) z.part = (float*)(ws + at_sum);
   if ((z.dz || z.part) && p->rows && p->out_features) HIP_TRY(launch_dz(p->dtype, z, st));
-  gx.a = gw.a = need_dz ? z.dz : p->dy;
-  gx.sam = gw.sak = need_dz ? z.lddz : p->lddy;
+  if (need_dz) gx.a = gw.a = z.dz;
   if (p->dbias && wide) HIP_TRY(launch_col_sum(p->dtype, {z.part, p->dbias, z.groups, wide}, st));
   if (p->dx) TRY(run_gemm(p->dtype, kEpiStore, gx, st));
   if (p->dweight) TRY(run_gemm(p->dtype, kEpiStore, gw, st));

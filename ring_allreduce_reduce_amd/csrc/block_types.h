@@ -129,15 +129,18 @@ struct NormArgs {
 // columns and then the same 16 up columns.
 enum : int { kEpiStore = 0, kEpiLinear = 1, kEpiGated = 2 };
 
+enum : int { kGeneral = 0, kTile256 = 1, kTile128 = 2, kTile64 = 3 };
+
 struct GemmArgs {
   const void* a;
   const void* b;
   int64_t sam, sak;      // strides of A in elements
   int64_t sbn, sbk;      // strides of B
   int m, n, k;           // n: output columns (gated: F)
+  int variant;           // kernel (kGeneral, ...), set with the split by plan_gemm
   int splits;            // parts of k, each a multiple of the tile's k
   int k_per_split;
-  float* part;           // splits > 1: [splits][m][logical n]
+  float* part;           // splits > 1: [splits][m][n, gated 2n]
   // epilogue
   const void* bias;      // n (gated: 2F), or null
   const void* residual;  // or null
@@ -178,6 +181,11 @@ int norm_backward_groups(int dtype, int64_t rows, int cols);
 hipError_t launch_col_sum(int out_dtype, const ColSumArgs& a, hipStream_t st);
 hipError_t launch_dz(int dtype, const DzArgs& a, hipStream_t st);
 int dz_groups(int64_t rows, int64_t cols);
+// Chooses the kernel and the split of k from sizes, strides and alignment
+// alone; returns the bytes of partial sums the launch needs.
+size_t plan_gemm(int dtype, int epi, GemmArgs& a);
+// Blocks of the planned launch.
+int64_t gemm_blocks(int dtype, int epi, const GemmArgs& a);
 hipError_t launch_gemm(int dtype, int epi, const GemmArgs& a, hipStream_t st);
 
 }  // namespace ringar

@@ -1,4 +1,4 @@
-// Products by element type.
+// Products by element type, and the rules that choose their kernel.
 #include "block_types.h"
 
 namespace ringar {
@@ -6,6 +6,63 @@ namespace ringar {
 hipError_t launch_gemm_f16(int epi, const GemmArgs& a, hipStream_t st);
 hipError_t launch_gemm_bf16(int epi, const GemmArgs& a, hipStream_t st);
 hipError_t launch_gemm_f32(int epi, const GemmArgs& a, hipStream_t st);
+
+namespace {
+
+struct Tile {
+  int m, n;
+};
+constexpr Tile kTiles[] = {{64, 64}, {256, 256}, {128, 128}, {64, 128}};
+
+// Operands the tiled kernels take: rows (or k lines) that start at 16-byte
+// boundaries, and offsets within a tile that fit the loads' 32 bits.
+bool operand_ok(const void* p, int64_t pitch, bool rows, int es, int64_t extra_rows) {
+  const int64_t bytes = pitch * es;
+  if ((uintptr_t)p % 16 || bytes % 16) return false;
+  return ((rows ? 256 : 64) + extra_rows) * bytes < (1ll << 32) - 4096;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int64_t tiles_of(int variant, int epi, const GemmArgs& a) {
+  const Tile t = kTiles[variant];
+  const int64_t cols = variant == kGeneral ? logical_cols(epi, a.n) : epi == kEpiGated ? 2 * (int64_t)a.n : a.n;
+  return ceil_div(a.m, t.m) * ceil_div(cols, t.n);
+}
+
+}  // namespace
+
+size_t plan_gemm(int dtype, int epi, GemmArgs& a) {
+  a.splits = 1;
+  a.k_per_split = a.k;
+  a.variant = kGeneral;
+  if (a.m == 0 || a.n == 0) return 0;
+  const int es = dtype == kF32 ? 4 : 2;
+  const bool arow = a.sak == 1, brow = a.sbk == 1;
+  const int64_t wide = epi == kEpiGated ? 2 * (int64_t)a.n : a.n;
+  const bool tiled = operand_ok(a.a, arow ? a.sam : a.sak, arow, es, 0) &&
+                     operand_ok(a.b, brow ? a.sbn : a.sbk, brow, es, epi == kEpiGated ? a.n : 0);
+  int step = es == 4 ? 16 : 32;
+  if (tiled) {
+    step = 128 / es;
+    a.variant = tiles_of(kTile256, epi, a) >= 192 && es == 2 ? kTile256 : arow && a.m <= 64 ? kTile64 : kTile128;
+  }
+  // parts of k: enough blocks to fill the GPU where the output has few tiles
+  const int64_t tiles = tiles_of(a.variant, epi, a), steps = ceil_div(a.k, step);
+  const int64_t want = a.variant == kTile256 ? 256 : 512;
+  int64_t splits = tiles >= want / 2 || steps < 8 ? 1 : ceil_div(want, tiles);
+  if (splits > steps / 4) splits = steps / 4;
+  if (splits < 1) splits = 1;
+  const int64_t per = ceil_div(steps, splits);
+  a.k_per_split = (int)(per * step < a.k ? per * step : a.k);
+  a.splits = (int)(steps ? ceil_div(steps, per) : 1);
+  return a.splits > 1 ? (size_t)a.splits * a.m * wide * 4 : 0;
+}
+
+int64_t gemm_blocks(int dtype, int epi, const GemmArgs& a) {
+  (void)dtype;
+  return tiles_of(a.variant, epi, a) * a.splits;
+}
 
 hipError_t launch_gemm(int dtype, int epi, const GemmArgs& a, hipStream_t st) {
   if (dtype == kF16) return launch_gemm_f16(epi, a, st);

@@ -84,6 +84,7 @@ template <typename T, int EPI> __global__ __launch_bounds__(256) void gemm_gener
   const int k_end = a.k - k_begin < a.k_per_split ? a.k : k_begin + a.k_per_split;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = (wave & 1) * 32, wn = (wave >> 1) * 32;
+  const int64_t part_cols = EPI == kEpiGated ? 2 * (int64_t)a.n : a.n;
   f32x4 acc[2][2] = {};
   for (int k0 = k_begin; k0 < k_end; k0 += kStep) {
     __syncthreads();
@@ -123,8 +124,8 @@ template <typename T, int EPI> __global__ __launch_bounds__(256) void gemm_gener
       if (a.splits > 1) {
 #pragma unroll
         for (int j = 0; j < 2; j++) {
-          const int64_t l = n0 + wn + j * 16 + (lane & 15);
-          if (l < cols) a.part[((int64_t)split * a.m + m) * cols + l] = acc[i][j][r];
+          const int64_t n = b_row<EPI>(a, n0 + wn + j * 16 + (lane & 15));
+          if (n >= 0) a.part[((int64_t)split * a.m + m) * part_cols + n] = acc[i][j][r];
         }
       } else if constexpr (EPI == kEpiGated) {
         const int64_t n = (n0 + wn) / 2 + (lane & 15);
@@ -143,30 +144,20 @@ template <typename T, int EPI> __global__ __launch_bounds__(256) void gemm_gener
 
 // Adds the parts of a split k in order and finishes the elements.
 template <typename T, int EPI> __global__ __launch_bounds__(256) void gemm_join(GemmArgs a) {
-  const int64_t cols = logical_cols(EPI, a.n);
+  const int64_t cols = EPI == kEpiGated ? 2 * (int64_t)a.n : a.n;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t m = i / a.n;
   const int n = (int)(i % a.n);
   if (m >= a.m) return;
-  const int64_t l = EPI == kEpiGated ? n / 16 * 32 + n % 16 : n;
-  const float* p = a.part + m * cols + l;
+  const float* p = a.part + m * cols + n;
   float s = 0.0f, u = 0.0f;
   for (int k = 0; k < a.splits; k++) {
     s += p[(int64_t)k * a.m * cols];
-    if constexpr (EPI == kEpiGated) u += p[(int64_t)k * a.m * cols + 16];
+    if constexpr (EPI == kEpiGated) u += p[(int64_t)k * a.m * cols + a.n];
   }
   if constexpr (EPI == kEpiGated) finish_gated<T>(a, m, n, s, u);
   else if constexpr (EPI == kEpiLinear) finish_linear<T>(a, m, n, s);
   else ((T*)a.c)[m * a.ldc + n] = (T)s;
-}
-
-template <typename T, int EPI> hipError_t launch_general(const GemmArgs& a, hipStream_t st) {
-  const int64_t tiles = ((logical_cols(EPI, a.n) + 63) / 64) * (((int64_t)a.m + 63) / 64);
-  hipLaunchKernelGGL((gemm_general<T, EPI>), dim3((unsigned)(tiles * a.splits)), dim3(256), 0, st, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL((gemm_join<T, EPI>), dim3((unsigned)(((int64_t)a.m * a.n + 255) / 256)), dim3(256), 0, st, a);
-  return hipGetLastError();
 }
 
 }  // namespace ringar

@@ -1,0 +1,382 @@
+// The tiled product kernel for operands whose rows start at 16-byte
+// boundaries.
+//
+// A block of WM x WN waves computes a BM x BN tile of C in steps of 128 bytes
+// of k.  Operand tiles go from memory straight into LDS (16 bytes a lane, no
+// registers), two buffers in turn: the loads of step t + 2 start as soon as
+// the last wave has read step t, and have a whole step of matrix instructions
+// to arrive.  Within a step the fragments of one half are read while the
+// other half's matrix instructions run, and the next step's first half is
+// read across the barrier, so the matrix units wait for LDS only where a
+// wave waits for the slowest one.
+//
+// LDS holds an operand as it lies in memory:
+//   ROW (k contiguous): one 128-byte line per row, its eight 16-byte chunks
+//     in the order c ^ (row & 7), so that eight rows read the same chunk from
+//     different banks.
+//   COL (rows contiguous): one line of the tile's rows per k, chunks in the
+//     order c ^ col_swizzle(k); 16-bit fragments come through the transposing
+//     LDS read, fp32 ones value by value.
+// The first matrix operand is B (columns of C), the second A: a lane then
+// holds four consecutive columns of one row of C.  The epilogue passes 32 rows
+// at a time through the wave's own part of LDS, after which eight lanes hold
+// 64 consecutive columns of a row and everything the epilogue reads or writes
+// moves in whole 128-byte lines.
+#pragma once
+
+#include "gemm_kernel.h"
+
+namespace ringar {
+
+#define RINGAR_LDS __attribute__((address_space(3)))
+
+// One operand's tile: R rows by 128 bytes of k, loaded by NW waves.
+template <typename T, bool ROW, int R, int NW> struct Operand {
+  static constexpr int kVec = 16 / sizeof(T);
+  static constexpr int kBK = 128 / sizeof(T);
+  static constexpr int kBytes = R * 128;
+  static constexpr int kLoads = kBytes / 1024 / NW;       // load instructions of a wave and step
+  static constexpr int kChunks = R * sizeof(T) / 16;      // COL: chunks of a line
+  static_assert(kLoads * 1024 * NW == kBytes, "every wave loads the same share");
+  static_assert(ROW || kChunks >= 16, "COL lines hold at least 16 chunks");
+
+  // COL: the four k lines that a transposing read (16-bit) or the four lane
+  // groups (fp32) touch together start 64 bytes apart in the banks.
+  static __device__ inline int col_swizzle(int k) { return (sizeof(T) == 2 ? k & 3 : (k >> 2) & 3) << 2; }
+
+  const char* base;        // of the current step, uniform
+  int64_t left;            // bytes from there to the operand's end
+  int64_t step;            // bytes of a step
+  uint32_t off[kLoads];
+
+  // `bytes`: the operand's size, up to the end of its last 16-byte chunk (a
+  // chunk that straddled the descriptor's end would read as zero entirely;
+  // what is past the operand in that chunk is cleared or not used).
+  __device__ inline void start(const void* p, int64_t at, int64_t bytes, int64_t step_bytes) {
+    base = (const char*)p + at;
+    left = ((bytes + 15) & ~15ll) - at;
+    step = step_bytes;
+  }
+
+  // lane's byte offset of load i, given where tile row r lies (ROW)
+  template <typename F> __device__ inline void offsets(int64_t pitch, int wave, int lane, F row_offset) {
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) {
+      const int idx = i * NW + wave;
+      if constexpr (ROW) {
+        const int r = idx * 8 + (lane >> 3);
+        off[i] = (uint32_t)row_offset(r) + (((lane & 7) ^ (r & 7)) << 4);
+      } else {
+        const int k = idx * (64 / kChunks) + lane / kChunks;
+        off[i] = (uint32_t)(k * pitch) + (((lane % kChunks) ^ col_swizzle(k)) << 4);
+      }
+    }
+  }
+
+  // Starts the loads of one step into `lds` and moves on.  Reads past the
+  // operand's end are stopped by the descriptor's size.  The loads are asm
+  // because the compiler would wait for them before every transposing LDS
+  // read that follows, which is what the second buffer is there to avoid;
+  // they have no register result, and wait_loads() waits for all of them
+  // before a barrier lets any wave read what they bring.
+  __device__ inline void load(char* lds, int wave) {
+    const uint32_t size = left <= 0 ? 0u : left > 0xffffffffll ? 0xffffffffu : (uint32_t)left;
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const u32x4 desc = {(uint32_t)(uintptr_t)base, (uint32_t)((uintptr_t)base >> 32), size, 0x00027000u};
+    const uint32_t to = (uint32_t)(uintptr_t)(RINGAR_LDS void*)lds + wave * 1024;
+#pragma unroll
+    for (int i = 0; i < kLoads; i++)
+      asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                   :: "s"(to + i * NW * 1024), "v"(off[i]), "s"(desc) : "memory");
+    base += step;
+    left -= step;
+  }
+
+  // Zeros every value of a step from k = `valid` on.
+  static __device__ inline void clear_tail(char* lds, int valid) {
+    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = threadIdx.x; i < R * 8; i += NW * 64) {
+      if constexpr (ROW) {
+        const int c = (i & 7) ^ ((i >> 3) & 7);
+        if (c * kVec >= valid) *(f32x4*)(lds + i * 16) = zero;
+        else if (c * kVec + kVec > valid)
+          for (int e = valid - c * kVec; e < kVec; e++) ((T*)(lds + i * 16))[e] = (T)0.0f;
+      } else {
+        if (i / kChunks >= valid) *(f32x4*)(lds + i * 16) = zero;
+      }
+    }
+  }
+
+  // Fragment of rows r0 .. r0 + 15 of half h of the step.
+  using Frag = typename Mma<T>::Frag;
+  static __device__ inline Frag read(const char* lds, int r0, int h, int lane) {
+    const int t = lane & 15, g = lane >> 4;
+    if constexpr (ROW) {
+      return *(const Frag*)(lds + (r0 + t) * 128 + (((h * 4 + g) ^ (t & 7)) << 4));
+    } else if constexpr (sizeof(T) == 2) {
+      // source lane t gives k line t / 4 and four columns; after the
+      // transposing read lane t holds column t of the four lines
+      const int col = r0 + (t & 3) * 4;
+      typedef short s16x4 __attribute__((ext_vector_type(4)));
+      typedef short s16x8 __attribute__((ext_vector_type(8)));
+      s16x4 v[2];
+#pragma unroll
+      for (int q = 0; q < 2; q++) {
+        const int k = h * 32 + g * 8 + q * 4 + (t >> 2);
+        const char* p = lds + k * (R * 2) + (((col >> 3) ^ col_swizzle(k)) << 4) + (col & 7) * 2;
+        v[q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((RINGAR_LDS s16x4*)(RINGAR_LDS void*)p);
+      }
+      const s16x8 w = {v[0][0], v[0][1], v[0][2], v[0][3], v[1][0], v[1][1], v[1][2], v[1][3]};
+      return __builtin_bit_cast(Frag, w);
+    } else {
+      const int col = r0 + t;
+      Frag f;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int k = h * 16 + g * 4 + i;
+        f[i] = *(const float*)(lds + k * (R * 4) + (((col >> 2) ^ col_swizzle(k)) << 4) + (col & 3) * 4);
+      }
+      return f;
+    }
+  }
+};
+
+// Eight consecutive output columns of one row, the first `valid` of them
+// real.
+template <typename T> __device__ inline void add8(const void* p, int64_t at, int valid, float* z) {
+  if (valid == 8) {
+    const Pack<T, 8> b = load_pack<T, 8>((const T*)p + at);
+#pragma unroll
+    for (int i = 0; i < 8; i++) z[i] += (float)b.v[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      if (i < valid) z[i] += (float)((const T*)p)[at + i];
+  }
+}
+
+template <typename T> __device__ inline void put8(void* p, int64_t at, int valid, const float* z) {
+  if (valid == 8) {
+    Pack<T, 8> o;
+#pragma unroll
+    for (int i = 0; i < 8; i++) o.v[i] = (T)z[i];
+    store_pack<T, 8>((T*)p + at, o);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      if (i < valid) ((T*)p)[at + i] = (T)z[i];
+  }
+}
+
+template <bool FAST> __device__ inline void activate8(int act, float* z) {
+  switch (act) {
+#define RINGAR_EACH(code)                                                       \
+  case code:                                                                    \
+    _Pragma("unroll") for (int i = 0; i < 8; i++) z[i] = activate<FAST>(code, z[i]); \
+    break;
+    RINGAR_EACH(kActRelu)
+    RINGAR_EACH(kActGelu)
+    RINGAR_EACH(kActGeluTanh)
+    RINGAR_EACH(kActSilu)
+    RINGAR_EACH(kActSigmoid)
+#undef RINGAR_EACH
+    default: break;
+  }
+}
+
+template <typename T> __device__ inline void finish8_linear(const GemmArgs& a, int64_t m, int64_t n, int valid, float* z) {
+  if (a.bias) add8<T>(a.bias, n, valid, z);
+  if (a.pre) put8<T>(a.pre, m * a.ldp + n, valid, z);
+  activate8<sizeof(T) == 2>(a.act, z);
+  if (a.residual) add8<T>(a.residual, m * a.ldr + n, valid, z);
+  put8<T>(a.c, m * a.ldc + n, valid, z);
+}
+
+template <typename T> __device__ inline void finish8_gated(const GemmArgs& a, int64_t m, int64_t n, int valid, float* g, float* u) {
+  if (a.bias) {
+    add8<T>(a.bias, n, valid, g);
+    add8<T>(a.bias, a.n + n, valid, u);
+  }
+  if (a.pre) {
+    put8<T>(a.pre, m * a.ldp + n, valid, g);
+    put8<T>(a.pre, m * a.ldp + a.n + n, valid, u);
+  }
+  activate8<sizeof(T) == 2>(a.act, g);
+#pragma unroll
+  for (int i = 0; i < 8; i++) g[i] *= u[i];
+  put8<T>(a.c, m * a.ldc + n, valid, g);
+}
+
+__device__ inline void wait_loads() {
+  // vmcnt(0): this wave's loads into LDS have landed; lgkmcnt(0): its
+  // fragment reads are done.  The empty asm keeps the compiler from moving
+  // memory accesses over the wait.
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);
+}
+__device__ inline void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <typename T, bool AROW, bool BROW, int EPI, int BM, int BN, int WM, int WN, int OCC>
+__global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_tile(GemmArgs a) {
+  constexpr int NW = WM * WN;
+  using OA = Operand<T, AROW, BM, NW>;
+  using OB = Operand<T, BROW, BN, NW>;
+  constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+  constexpr int kBK = OA::kBK;
+  static_assert(TN == 64, "eight lanes finish a wave's row");
+  static_assert(BROW || EPI == kEpiStore, "epilogues with columns of their own read weights by rows");
+  constexpr int kStage = OA::kBytes + OB::kBytes;
+  // epilogue: a wave's rows in fp32, shifted 16 bytes over the banks
+  constexpr int kPass = TM < 32 ? TM : 32, kRowF = TN + 4;
+  constexpr int kShared = 2 * kStage > NW * kPass * kRowF * 4 ? 2 * kStage : NW * kPass * kRowF * 4;
+  __shared__ __attribute__((aligned(1024))) char smem[kShared];
+  using Frag = typename Mma<T>::Frag;
+
+  // Blocks go round the 8 XCDs in turn: give each XCD a run of neighbouring
+  // tiles, 8 tiles of rows deep, so that its blocks share operands in its L2.
+  constexpr int kOut = EPI == kEpiGated ? BN / 2 : BN;    // output columns of a tile
+  const int tiles_m = (a.m + BM - 1) / BM, tiles_n = (a.n + kOut - 1) / kOut;
+  const int tiles = tiles_m * tiles_n;
+  const int total = tiles * a.splits;
+  const int q = total >> 3, rest = total & 7, xcd = blockIdx.x & 7;
+  const int id = xcd * q + (xcd < rest ? xcd : rest) + (blockIdx.x >> 3);
+  const int split = id / tiles, tile = id % tiles;
+  const int band = tile / (8 * tiles_n), in_band = tile % (8 * tiles_n);
+  const int deep = tiles_m - band * 8 < 8 ? tiles_m - band * 8 : 8;
+  const int64_t m0 = (int64_t)(band * 8 + in_band % deep) * BM, n0 = (int64_t)(in_band / deep) * kOut;
+  const int k_begin = split * a.k_per_split;
+  const int k_len = (a.k - k_begin < a.k_per_split ? a.k - k_begin : a.k_per_split);
+  const int steps = (k_len + kBK - 1) / kBK;
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = (wave % WM) * TM, wn = (wave / WM) * TN;
+
+  OA oa;
+  OB ob;
+  {
+    const int64_t pa = (AROW ? a.sam : a.sak) * (int64_t)sizeof(T), pb = (BROW ? a.sbn : a.sbk) * (int64_t)sizeof(T);
+    const int64_t rows_b = EPI == kEpiGated ? 2 * (int64_t)a.n : a.n;
+    const int64_t bytes_a = AROW ? (a.m - 1) * pa + (int64_t)a.k * sizeof(T) : (a.k - 1) * pa + (int64_t)a.m * sizeof(T);
+    const int64_t bytes_b = BROW ? (rows_b - 1) * pb + (int64_t)a.k * sizeof(T) : (a.k - 1) * pb + rows_b * (int64_t)sizeof(T);
+    oa.start(a.a, AROW ? m0 * pa + (int64_t)k_begin * sizeof(T) : k_begin * pa + m0 * (int64_t)sizeof(T), bytes_a, AROW ? 128 : kBK * pa);
+    ob.start(a.b, BROW ? n0 * pb + (int64_t)k_begin * sizeof(T) : k_begin * pb + n0 * (int64_t)sizeof(T), bytes_b, BROW ? 128 : kBK * pb);
+    // rows past the edge read the last one; their results are not stored
+    oa.offsets(pa, wave, lane, [&](int r) {
+      const int64_t m = m0 + r < a.m ? r : a.m - 1 - m0;
+      return m * pa;
+    });
+    ob.offsets(pb, wave, lane, [&](int r) {
+      if constexpr (EPI == kEpiGated) {
+        // 64 rows: 32 of the gate, then the same 32 of the up projection
+        const int64_t c = (r >> 6) * 32 + (r & 31);
+        return ((n0 + c < a.n ? c : a.n - 1 - n0) + (r & 32 ? a.n : 0)) * pb;
+      } else {
+        return (n0 + r < a.n ? r : a.n - 1 - n0) * pb;
+      }
+    });
+  }
+
+  f32x4 acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; i++)
+#pragma unroll
+    for (int j = 0; j < FM; j++) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  auto issue = [&](int buf) {
+    oa.load(smem + buf * kStage, wave);
+    ob.load(smem + buf * kStage + OA::kBytes, wave);
+  };
+  auto fix_tail = [&](int s) {        // the last step, where k ends inside it
+    if (s == steps - 1 && k_len % kBK != 0) {
+      OA::clear_tail(smem + (s & 1) * kStage, k_len % kBK);
+      OB::clear_tail(smem + (s & 1) * kStage + OA::kBytes, k_len % kBK);
+      wait_loads();
+      barrier();
+    }
+  };
+  auto read = [&](int buf, int h, Frag* fa, Frag* fb) {
+    const char* pa = smem + buf * kStage;
+    const char* pb = pa + OA::kBytes;
+#pragma unroll
+    for (int i = 0; i < FN; i++) fb[i] = OB::read(pb, wn + i * 16, h, lane);
+#pragma unroll
+    for (int i = 0; i < FM; i++) fa[i] = OA::read(pa, wm + i * 16, h, lane);
+  };
+  auto mma = [&](const Frag* fa, const Frag* fb) {
+#pragma unroll
+    for (int i = 0; i < FN; i++)
+#pragma unroll
+      for (int j = 0; j < FM; j++) acc[i][j] = Mma<T>::run(fb[i], fa[j], acc[i][j]);
+  };
+
+  if (steps > 0) {
+    Frag fa0[FM], fb0[FN], fa1[FM], fb1[FN];
+    issue(0);
+    wait_loads();
+    barrier();
+    fix_tail(0);
+    if (steps > 1) issue(1);
+    read(0, 0, fa0, fb0);
+    for (int s = 0; s < steps - 1; s++) {
+      read(s & 1, 1, fa1, fb1);
+      mma(fa0, fb0);
+      wait_loads();
+      barrier();
+      fix_tail(s + 1);
+      if (s + 2 < steps) issue(s & 1);
+      read((s + 1) & 1, 0, fa0, fb0);
+      mma(fa1, fb1);
+    }
+    read((steps - 1) & 1, 1, fa1, fb1);
+    mma(fa0, fb0);
+    mma(fa1, fb1);
+  }
+
+  wait_loads();
+  barrier();                                   // every wave is done with the operands
+  float* rows = (float*)smem + wave * kPass * kRowF;
+  constexpr int kLanes = EPI == kEpiGated ? 4 : 8;   // lanes of a row, eight columns each
+  const int64_t part_cols = EPI == kEpiGated ? 2 * (int64_t)a.n : a.n;
+#pragma unroll
+  for (int p = 0; p < TM / kPass; p++) {
+#pragma unroll
+    for (int j = 0; j < kPass / 16; j++)
+#pragma unroll
+      for (int i = 0; i < FN; i++)
+        *(f32x4*)(rows + (j * 16 + (lane & 15)) * kRowF + i * 16 + (lane >> 4) * 4) = acc[i][p * (kPass / 16) + j];
+    asm volatile("" ::: "memory");
+#pragma unroll 1
+    for (int r = lane / kLanes; r < kPass; r += 64 / kLanes) {
+      const int64_t m = m0 + wm + p * kPass + r;
+      const int64_t c = n0 + (EPI == kEpiGated ? wn >> 1 : wn) + (lane % kLanes) * 8;
+      if (m >= a.m || c >= a.n) continue;
+      const int valid = a.n - c < 8 ? (int)(a.n - c) : 8;
+      float v[8];
+      *(f32x4*)v = *(const f32x4*)(rows + r * kRowF + (lane % kLanes) * 8);
+      *(f32x4*)(v + 4) = *(const f32x4*)(rows + r * kRowF + (lane % kLanes) * 8 + 4);
+      float* part = a.part + ((int64_t)split * a.m + m) * part_cols;
+      if constexpr (EPI == kEpiGated) {
+        float u[8];
+        *(f32x4*)u = *(const f32x4*)(rows + r * kRowF + 32 + (lane % kLanes) * 8);
+        *(f32x4*)(u + 4) = *(const f32x4*)(rows + r * kRowF + 32 + (lane % kLanes) * 8 + 4);
+        if (a.splits > 1) {
+          put8<float>(part, c, valid, v);
+          put8<float>(part, a.n + c, valid, u);
+        } else {
+          finish8_gated<T>(a, m, c, valid, v, u);
+        }
+      } else {
+        if (a.splits > 1) put8<float>(part, c, valid, v);
+        else if constexpr (EPI == kEpiLinear) finish8_linear<T>(a, m, c, valid, v);
+        else put8<T>(a.c, m * a.ldc + c, valid, v);
+      }
+    }
+    asm volatile("" ::: "memory");
+  }
+}
+
+}  // namespace ringar

@@ -1,0 +1,6 @@
+// dweight = dz^T x: both operands with k as the row index (bf16).
+#include "gemm_launch.h"
+
+namespace ringar {
+hipError_t launch_tn_bf16(const GemmArgs& a, hipStream_t st) { return launch_tiled<__bf16, false, false, kEpiStore>(a, st); }
+}  // namespace ringar

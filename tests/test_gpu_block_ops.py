@@ -158,6 +158,60 @@ def test_products(rows, k, n, dtype, gated):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("rows,k,n", [(3601, 3608, 3624), (5000, 72, 5016)])
+def test_large_products(rows, k, n, gated, dtype):
+    """The largest tiles, with edges and a ragged last step in every product."""
+    g = torch.Generator(device="cuda")
+    print("case large", rows, k, n, gated, dtype, flush=True)
+    g.manual_seed(rows + k + n)
+    rand = lambda *s, scale=1.0: (torch.randn(*s, device="cuda", generator=g) * scale).to(dtype)  # noqa: E731
+    n = n // 2 if gated else n
+    wide = 2 * n if gated else n
+    x, w, b, dy = rand(rows, k), rand(wide, k, scale=k ** -0.5), rand(wide), rand(rows, n)
+    res = None if gated else rand(rows, n)
+    cuda64 = lambda *t: [None if v is None else _Cuda64(v) for v in t]  # noqa: E731
+    if gated:
+        got = ra.gated_ffn(x, w, b, act="silu", save_pre=True)
+        want, bound = R.gated_forward(*cuda64(x, w, b), "silu")
+    else:
+        got = ra.linear(x, w, b, act="gelu_tanh", residual=res, save_pre=True)
+        want, bound = R.linear_forward(*cuda64(x, w, b), "gelu_tanh", _Cuda64(res))
+    for a, c, e, what in zip(got, want, bound, ("y", "pre")):
+        _within_cuda(a, c, e, what)
+    back = ra.gated_ffn_backward if gated else ra.linear_backward
+    act = "silu" if gated else "gelu_tanh"
+    grads = back(dy, x, w, got[1], act=act)
+    want, bound = R.backward(*cuda64(dy, x, w, got[1]), act, gated)
+    for a, c, e, what in zip(grads, want, bound, ("dx", "dweight", "dbias")):
+        _within_cuda(a, c, e, what)
+
+
+class _Cuda64:
+    """A GPU tensor for the fp64 forms that stays on the GPU."""
+
+    def __init__(self, t):
+        self.t, self.dtype, self.shape = t, t.dtype, t.shape
+
+    def double(self):
+        return _Stay(self.t.double())
+
+
+class _Stay:
+    def __init__(self, t):
+        self.t = t
+
+    def cpu(self):
+        return self.t
+
+
+def _within_cuda(got, want, bound, what):
+    off = (got.double() - want).abs()
+    bad = ~(off <= bound)
+    assert not bad.any(), (what, int(bad.sum()), bad.numel(), bad.nonzero()[:4].tolist(), float((off / bound).max()))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,k,n", [(1, 520, 40), (20, 264, 72), (70, 135, 130), (300, 256, 264)])
 @pytest.mark.parametrize("gated", [False, True])
 def test_products_strided_in_nan(rows, k, n, dtype, gated):
