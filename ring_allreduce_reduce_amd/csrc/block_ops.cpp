@@ -272,7 +272,7 @@ static ringar_result_t norm_backward(const ringar_layer_norm_backward_t* p, ring
   a.rows = p->rows;
   a.cols = (int)p->cols;
   a.inv_cols = 1.0f / (float)p->cols;
-  a.groups = norm_backward_groups(p->dtype, p->rows, a.cols);
+  a.groups = norm_backward_groups(p->rows, a.cols);
   std::lock_guard<std::mutex> lock(g_ws_mu);
   if (params) {
     char* ws_p = nullptr;
@@ -280,9 +280,8 @@ static ringar_result_t norm_backward(const ringar_layer_norm_backward_t* p, ring
     a.part = (float*)ws_p;
   }
   if (p->rows) HIP_TRY(launch_norm_backward(p->dtype, p->param_dtype, a, st));
-  if (p->dweight) HIP_TRY(launch_col_sum(p->param_dtype, {a.part, p->dweight, a.groups, p->cols}, st));
-  if (p->dbias)
-    HIP_TRY(launch_col_sum(p->param_dtype, {a.part + (int64_t)a.groups * p->cols, p->dbias, a.groups, p->cols}, st));
+  if (params)
+    HIP_TRY(launch_col_sum(p->param_dtype, {a.part, a.groups, 2 * p->cols, p->cols, p->dweight, p->dbias}, st));
   return RINGAR_SUCCESS;
 }
 
@@ -392,7 +391,7 @@ static ringar_result_t product_backward(const ringar_linear_backward_t* p, bool 
   if (p->dbias) z.part = (float*)(ws + at_sum);
   if ((z.dz || z.part) && p->rows && p->out_features) HIP_TRY(launch_dz(p->dtype, z, st));
   if (need_dz) gx.a = gw.a = z.dz;
-  if (p->dbias && wide) HIP_TRY(launch_col_sum(p->dtype, {z.part, p->dbias, z.groups, wide}, st));
+  if (p->dbias && wide) HIP_TRY(launch_col_sum(p->dtype, {z.part, z.groups, wide, wide, p->dbias, nullptr}, st));
   if (p->dx) TRY(run_gemm(p->dtype, kEpiStore, gx, st));
   if (p->dweight) TRY(run_gemm(p->dtype, kEpiStore, gw, st));
   return RINGAR_SUCCESS;

@@ -105,6 +105,23 @@ template <bool FAST> __device__ inline void activate_grad(int act, float z, floa
   }
 }
 
+// The same for N values, the choice of activation outside the loop.
+template <bool FAST, int N> __device__ inline void activate_grad_n(int act, const float* z, float* a, float* d) {
+  switch (act) {
+#define RINGAR_EACH(code)                                                                              \
+  case code:                                                                                           \
+    _Pragma("unroll") for (int i = 0; i < N; i++) activate_grad<FAST>(code, z[i], a + i, d + i);       \
+    break;
+    RINGAR_EACH(kActRelu)
+    RINGAR_EACH(kActGelu)
+    RINGAR_EACH(kActGeluTanh)
+    RINGAR_EACH(kActSilu)
+    RINGAR_EACH(kActSigmoid)
+    RINGAR_EACH(kActNone)
+#undef RINGAR_EACH
+  }
+}
+
 // ------------------------------------------------------------- layer norm
 struct NormArgs {
   const void* x;
@@ -114,7 +131,7 @@ struct NormArgs {
   void* y;               // forward: y; backward: dx (may be null)
   float* mean;           // forward: may be null; backward: inputs
   float* rstd;
-  float* part;           // backward: partial sums [2][groups][cols], or null
+  float* part;           // backward: partial sums [groups][dweight, dbias], or null
   int64_t ldx, lddy, ldy;
   int64_t rows;
   int cols;
@@ -166,18 +183,21 @@ struct DzArgs {
   int gated;
 };
 
-// out[c] = sum over p of part[p][c]
+// sums over p of part[p][0 .. width): the first n0 columns to out0, the rest
+// to out1; a null output is not wanted
 struct ColSumArgs {
   const float* part;
-  void* out;
   int parts;
-  int64_t cols;
+  int64_t width;
+  int64_t n0;
+  void* out0;
+  void* out1;
 };
 
 // the kernels' launchers (dtype codes of the public header)
 hipError_t launch_norm_forward(int dtype, int wdtype, const NormArgs& a, hipStream_t st);
 hipError_t launch_norm_backward(int dtype, int wdtype, const NormArgs& a, hipStream_t st);
-int norm_backward_groups(int dtype, int64_t rows, int cols);
+int norm_backward_groups(int64_t rows, int cols);
 hipError_t launch_col_sum(int out_dtype, const ColSumArgs& a, hipStream_t st);
 hipError_t launch_dz(int dtype, const DzArgs& a, hipStream_t st);
 int dz_groups(int64_t rows, int64_t cols);

@@ -10,65 +10,52 @@
 namespace ringar {
 namespace {
 
-template <typename T, bool GATED> __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
-  constexpr int V = 16 / sizeof(T);
+// V columns a lane.  A lane whose pack would pass the last column takes the
+// last V columns instead; the `skip` first of them are another lane's too:
+// stored twice with the same value, counted once.
+template <typename T, bool GATED, int V> __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
   constexpr bool kFast = sizeof(T) == 2;
   // a wave takes 64 packs of columns; the block's four waves take rows in turn
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c = ((int64_t)blockIdx.x * 64 + lane) * V;
+  const int64_t nominal = ((int64_t)blockIdx.x * 64 + lane) * V;
+  const int64_t c = nominal < a.n - V ? nominal : a.n - V;
+  const int skip = (int)(nominal - c < V ? nominal - c : V);
   float s[V], su[V];
 #pragma unroll
   for (int j = 0; j < V; j++) s[j] = su[j] = 0.0f;
-  if (c < a.n) {
-    const bool whole = c + V <= a.n;
-    for (int64_t row = (int64_t)blockIdx.y * 4 + wave; row < a.rows; row += (int64_t)a.groups * 4) {
-      Pack<T, V> dy, g, u;
-      const T* pdy = (const T*)a.dy + row * a.lddy + c;
-      const T* pre = (const T*)a.pre + row * a.ldp + c;
-      if (whole) {
-        dy = load_pack<T, V>(pdy);
-        if (a.pre) g = load_pack<T, V>(pre);
-        if constexpr (GATED) u = load_pack<T, V>(pre + a.n);
+#pragma unroll 2
+  for (int64_t row = (int64_t)blockIdx.y * 4 + wave; row < a.rows; row += (int64_t)a.groups * 4) {
+    Pack<T, V> dy = load_pack<T, V>((const T*)a.dy + row * a.lddy + c), g, u;
+    const T* pre = (const T*)a.pre + row * a.ldp + c;
+    if (GATED || a.pre) g = load_pack<T, V>(pre);
+    if constexpr (GATED) u = load_pack<T, V>(pre + a.n);
+    float z[V], d[V], act[V];
+#pragma unroll
+    for (int j = 0; j < V; j++) {
+      z[j] = GATED || a.pre ? (float)g.v[j] : 0.0f;
+      act[j] = 0.0f;
+      d[j] = 1.0f;
+    }
+    if (GATED || a.pre) activate_grad_n<kFast, V>(a.act, z, act, d);
+    Pack<T, V> og, ou;
+#pragma unroll
+    for (int j = 0; j < V; j++) {
+      const float e = (float)dy.v[j];
+      if constexpr (GATED) {
+        const float dg = e * (float)u.v[j] * d[j], du = e * act[j];
+        s[j] += dg;
+        su[j] += du;
+        og.v[j] = (T)dg;
+        ou.v[j] = (T)du;
       } else {
-#pragma unroll
-        for (int j = 0; j < V; j++) {
-          const bool in = c + j < a.n;
-          dy.v[j] = in ? pdy[j] : (T)0.0f;
-          g.v[j] = in && a.pre ? pre[j] : (T)0.0f;
-          if constexpr (GATED) u.v[j] = in ? pre[a.n + j] : (T)0.0f;
-        }
+        s[j] += e * d[j];
+        og.v[j] = (T)(e * d[j]);
       }
-      Pack<T, V> og, ou;
-#pragma unroll
-      for (int j = 0; j < V; j++) {
-        float act = 0.0f, d = 1.0f;
-        const float e = (float)dy.v[j];
-        if (GATED || a.pre) activate_grad<kFast>(a.act, (float)g.v[j], &act, &d);
-        if constexpr (GATED) {
-          const float dg = e * (float)u.v[j] * d, du = e * act;
-          s[j] += dg;
-          su[j] += du;
-          og.v[j] = (T)dg;
-          ou.v[j] = (T)du;
-        } else {
-          s[j] += e * d;
-          og.v[j] = (T)(e * d);
-        }
-      }
-      if (a.dz) {
-        T* o = (T*)a.dz + row * a.lddz + c;
-        if (whole) {
-          store_pack<T, V>(o, og);
-          if constexpr (GATED) store_pack<T, V>(o + a.n, ou);
-        } else {
-#pragma unroll
-          for (int j = 0; j < V; j++)
-            if (c + j < a.n) {
-              o[j] = og.v[j];
-              if constexpr (GATED) o[a.n + j] = ou.v[j];
-            }
-        }
-      }
+    }
+    if (a.dz && skip < V) {
+      T* o = (T*)a.dz + row * a.lddz + c;
+      store_pack<T, V>(o, og);
+      if constexpr (GATED) store_pack<T, V>(o + a.n, ou);
     }
   }
   if (!a.part) return;
@@ -78,7 +65,8 @@ template <typename T, bool GATED> __global__ __launch_bounds__(256) void dz_kern
   for (int which = 0; which < (GATED ? 2 : 1); which++) {
     if (which) __syncthreads();
 #pragma unroll
-    for (int j = 0; j < V; j++) smem[wave][lane * V + j] = which ? su[j] : s[j];
+    for (int j = 0; j < V; j++)
+      if (j >= skip) smem[wave][c - (int64_t)blockIdx.x * 64 * V + j] = which ? su[j] : s[j];
     __syncthreads();
     for (int i = threadIdx.x; i < 64 * V; i += 256) {
       const int64_t col = (int64_t)blockIdx.x * 64 * V + i;
@@ -88,11 +76,16 @@ template <typename T, bool GATED> __global__ __launch_bounds__(256) void dz_kern
   }
 }
 
-template <typename T> hipError_t launch(const DzArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)((a.n + 64 * (16 / sizeof(T)) - 1) / (64 * (16 / sizeof(T)))), a.groups);
-  if (a.gated) hipLaunchKernelGGL((dz_kernel<T, true>), grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((dz_kernel<T, false>), grid, dim3(256), 0, st, a);
+template <typename T, int V> hipError_t launch(const DzArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)(((int64_t)a.n + 64 * V - 1) / (64 * V)), a.groups);
+  if (a.gated) hipLaunchKernelGGL((dz_kernel<T, true, V>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((dz_kernel<T, false, V>), grid, dim3(256), 0, st, a);
   return hipGetLastError();
+}
+
+template <typename T> hipError_t launch(const DzArgs& a, hipStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  return a.n < V ? launch<T, 1>(a, st) : launch<T, V>(a, st);
 }
 
 }  // namespace

@@ -141,31 +141,18 @@ template <typename T, bool ROW, int R, int NW> struct Operand {
   }
 };
 
-// Eight consecutive output columns of one row, the first `valid` of them
-// real.
-template <typename T> __device__ inline void add8(const void* p, int64_t at, int valid, float* z) {
-  if (valid == 8) {
-    const Pack<T, 8> b = load_pack<T, 8>((const T*)p + at);
+// Eight consecutive output columns of one row.
+template <typename T> __device__ inline void add8(const void* p, int64_t at, float* z) {
+  const Pack<T, 8> b = load_pack<T, 8>((const T*)p + at);
 #pragma unroll
-    for (int i = 0; i < 8; i++) z[i] += (float)b.v[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; i++)
-      if (i < valid) z[i] += (float)((const T*)p)[at + i];
-  }
+  for (int i = 0; i < 8; i++) z[i] += (float)b.v[i];
 }
 
-template <typename T> __device__ inline void put8(void* p, int64_t at, int valid, const float* z) {
-  if (valid == 8) {
-    Pack<T, 8> o;
+template <typename T> __device__ inline void put8(void* p, int64_t at, const float* z) {
+  Pack<T, 8> o;
 #pragma unroll
-    for (int i = 0; i < 8; i++) o.v[i] = (T)z[i];
-    store_pack<T, 8>((T*)p + at, o);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; i++)
-      if (i < valid) ((T*)p)[at + i] = (T)z[i];
-  }
+  for (int i = 0; i < 8; i++) o.v[i] = (T)z[i];
+  store_pack<T, 8>((T*)p + at, o);
 }
 
 template <bool FAST> __device__ inline void activate8(int act, float* z) {
@@ -184,27 +171,27 @@ template <bool FAST> __device__ inline void activate8(int act, float* z) {
   }
 }
 
-template <typename T> __device__ inline void finish8_linear(const GemmArgs& a, int64_t m, int64_t n, int valid, float* z) {
-  if (a.bias) add8<T>(a.bias, n, valid, z);
-  if (a.pre) put8<T>(a.pre, m * a.ldp + n, valid, z);
+template <typename T> __device__ inline void finish8_linear(const GemmArgs& a, int64_t m, int64_t n, float* z) {
+  if (a.bias) add8<T>(a.bias, n, z);
+  if (a.pre) put8<T>(a.pre, m * a.ldp + n, z);
   activate8<sizeof(T) == 2>(a.act, z);
-  if (a.residual) add8<T>(a.residual, m * a.ldr + n, valid, z);
-  put8<T>(a.c, m * a.ldc + n, valid, z);
+  if (a.residual) add8<T>(a.residual, m * a.ldr + n, z);
+  put8<T>(a.c, m * a.ldc + n, z);
 }
 
-template <typename T> __device__ inline void finish8_gated(const GemmArgs& a, int64_t m, int64_t n, int valid, float* g, float* u) {
+template <typename T> __device__ inline void finish8_gated(const GemmArgs& a, int64_t m, int64_t n, float* g, float* u) {
   if (a.bias) {
-    add8<T>(a.bias, n, valid, g);
-    add8<T>(a.bias, a.n + n, valid, u);
+    add8<T>(a.bias, n, g);
+    add8<T>(a.bias, a.n + n, u);
   }
   if (a.pre) {
-    put8<T>(a.pre, m * a.ldp + n, valid, g);
-    put8<T>(a.pre, m * a.ldp + a.n + n, valid, u);
+    put8<T>(a.pre, m * a.ldp + n, g);
+    put8<T>(a.pre, m * a.ldp + a.n + n, u);
   }
   activate8<sizeof(T) == 2>(a.act, g);
 #pragma unroll
   for (int i = 0; i < 8; i++) g[i] *= u[i];
-  put8<T>(a.c, m * a.ldc + n, valid, g);
+  put8<T>(a.c, m * a.ldc + n, g);
 }
 
 __device__ inline void wait_loads() {
@@ -354,25 +341,43 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_tile(GemmArgs a) {
       const int64_t m = m0 + wm + p * kPass + r;
       const int64_t c = n0 + (EPI == kEpiGated ? wn >> 1 : wn) + (lane % kLanes) * 8;
       if (m >= a.m || c >= a.n) continue;
-      const int valid = a.n - c < 8 ? (int)(a.n - c) : 8;
-      float v[8];
-      *(f32x4*)v = *(const f32x4*)(rows + r * kRowF + (lane % kLanes) * 8);
-      *(f32x4*)(v + 4) = *(const f32x4*)(rows + r * kRowF + (lane % kLanes) * 8 + 4);
+      const float* from = rows + r * kRowF + (lane % kLanes) * 8;
       float* part = a.part + ((int64_t)split * a.m + m) * part_cols;
-      if constexpr (EPI == kEpiGated) {
-        float u[8];
-        *(f32x4*)u = *(const f32x4*)(rows + r * kRowF + 32 + (lane % kLanes) * 8);
-        *(f32x4*)(u + 4) = *(const f32x4*)(rows + r * kRowF + 32 + (lane % kLanes) * 8 + 4);
-        if (a.splits > 1) {
-          put8<float>(part, c, valid, v);
-          put8<float>(part, a.n + c, valid, u);
+      if (c + 8 <= a.n) {
+        float v[8];
+        *(f32x4*)v = *(const f32x4*)from;
+        *(f32x4*)(v + 4) = *(const f32x4*)(from + 4);
+        if constexpr (EPI == kEpiGated) {
+          float u[8];
+          *(f32x4*)u = *(const f32x4*)(from + 32);
+          *(f32x4*)(u + 4) = *(const f32x4*)(from + 36);
+          if (a.splits > 1) {
+            put8<float>(part, c, v);
+            put8<float>(part, a.n + c, u);
+          } else {
+            finish8_gated<T>(a, m, c, v, u);
+          }
         } else {
-          finish8_gated<T>(a, m, c, valid, v, u);
+          if (a.splits > 1) put8<float>(part, c, v);
+          else if constexpr (EPI == kEpiLinear) finish8_linear<T>(a, m, c, v);
+          else put8<T>(a.c, m * a.ldc + c, v);
         }
       } else {
-        if (a.splits > 1) put8<float>(part, c, valid, v);
-        else if constexpr (EPI == kEpiLinear) finish8_linear<T>(a, m, c, valid, v);
-        else put8<T>(a.c, m * a.ldc + c, valid, v);
+#pragma unroll 1
+        for (int i = 0; c + i < a.n; i++) {
+          if constexpr (EPI == kEpiGated) {
+            if (a.splits > 1) {
+              part[c + i] = from[i];
+              part[a.n + c + i] = from[32 + i];
+            } else {
+              finish_gated<T>(a, m, (int)(c + i), from[i], from[32 + i]);
+            }
+          } else {
+            if (a.splits > 1) part[c + i] = from[i];
+            else if constexpr (EPI == kEpiLinear) finish_linear<T>(a, m, (int)(c + i), from[i]);
+            else ((T*)a.c)[m * a.ldc + c + i] = (T)from[i];
+          }
+        }
       }
     }
     asm volatile("" ::: "memory");

@@ -26,9 +26,10 @@ template <int TPR> __device__ inline float row_sum(float v, float* smem) {
     const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) smem[wave] = v;
     __syncthreads();
+    const float* row = smem + wave / (TPR / 64) * (TPR / 64);
     v = 0.0f;
 #pragma unroll
-    for (int i = 0; i < TPR / 64; i++) v += smem[i];
+    for (int i = 0; i < TPR / 64; i++) v += row[i];
     __syncthreads();
   }
   return v;
@@ -47,105 +48,128 @@ template <int TPR> __device__ inline void row_sum2(float& u, float& v, float* sm
       smem[2 * wave + 1] = v;
     }
     __syncthreads();
+    const float* row = smem + wave / (TPR / 64) * (TPR / 64) * 2;
     u = v = 0.0f;
 #pragma unroll
     for (int i = 0; i < TPR / 64; i++) {
-      u += smem[2 * i];
-      v += smem[2 * i + 1];
+      u += row[2 * i];
+      v += row[2 * i + 1];
     }
     __syncthreads();
   }
 }
 
-// E elements of a row as floats: thread t of TPR holds the packs of V
-// elements that start at (i * TPR + t) * V.  Elements past the row read 0.
-template <typename T, int TPR, int E>
-struct Row {
-  static constexpr int V = 16 / sizeof(T) < E ? 16 / sizeof(T) : E;
+// E elements of a row: thread t of TPR holds the packs of V elements that
+// start at (i * TPR + t) * V.  A pack that would pass the row's end starts V
+// before the end instead, and its first `skip` elements, which belong to
+// other packs, are held as zeros and not stored: loads never branch, so all
+// of them are in flight together, at any width of at least V.
+template <typename T, int TPR, int E, int V> struct Row {
   static constexpr int P = E / V;
-  static __device__ inline int col(int i, int t) { return (i * TPR + t) * V; }
-  static __device__ inline void load(const T* p, int cols, int t, float* out, float fill = 0.0f) {
+  int col[P], skip[P];
+
+  __device__ inline Row(int cols, int t) {
 #pragma unroll
     for (int i = 0; i < P; i++) {
-      const int c = col(i, t);
-      if (c + V <= cols) {
-        const Pack<T, V> q = load_pack<T, V>(p + c);
-#pragma unroll
-        for (int j = 0; j < V; j++) out[i * V + j] = (float)q.v[j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; j++) out[i * V + j] = c + j < cols ? (float)p[c + j] : fill;
-      }
+      const int c = (i * TPR + t) * V;
+      col[i] = c < cols - V ? c : cols - V;
+      skip[i] = c - col[i];
     }
   }
-  // a row of another element type at the same columns
-  template <typename W> static __device__ inline void load_as(const W* p, int cols, int t, float* out, float fill) {
+  // the row as it lies in memory
+  template <typename U> struct Raw {
+    Pack<U, V> q[P];
+  };
+  template <typename U> __device__ inline void load(const U* p, Raw<U>& r) const {
 #pragma unroll
-    for (int i = 0; i < P; i++) {
-      const int c = col(i, t);
-      if (p != nullptr && c + V <= cols) {
-        const Pack<W, V> q = load_pack<W, V>(p + c);
-#pragma unroll
-        for (int j = 0; j < V; j++) out[i * V + j] = (float)q.v[j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; j++) out[i * V + j] = p != nullptr && c + j < cols ? (float)p[c + j] : fill;
-      }
-    }
+    for (int i = 0; i < P; i++) r.q[i] = load_pack<U, V>(p + col[i]);
   }
-  static __device__ inline void store(T* p, int cols, int t, const float* in) {
+  template <typename U> __device__ inline void widen(const Raw<U>& r, float* out) const {
+#pragma unroll
+    for (int i = 0; i < P; i++)
+#pragma unroll
+      for (int j = 0; j < V; j++) out[i * V + j] = (float)r.q[i].v[j];
+    clear(out);
+  }
+  __device__ inline void clear(float* v) const {
+#pragma unroll
+    for (int i = 0; i < P; i++)
+      if (skip[i] > 0)
+#pragma unroll
+        for (int j = 0; j < V; j++)
+          if (j < skip[i]) v[i * V + j] = 0.0f;
+  }
+  template <typename F> __device__ inline void each(F f) const {
+#pragma unroll
+    for (int i = 0; i < P; i++)
+#pragma unroll
+      for (int j = 0; j < V; j++)
+        if (j >= skip[i]) f(i * V + j, col[i] + j);
+  }
+  __device__ inline void store(T* p, const float* in) const {
 #pragma unroll
     for (int i = 0; i < P; i++) {
-      const int c = col(i, t);
-      if (c + V <= cols) {
+      if (skip[i] == 0) {
         Pack<T, V> q;
 #pragma unroll
         for (int j = 0; j < V; j++) q.v[j] = (T)in[i * V + j];
-        store_pack<T, V>(p + c, q);
+        store_pack<T, V>(p + col[i], q);
       } else {
 #pragma unroll
         for (int j = 0; j < V; j++)
-          if (c + j < cols) p[c + j] = (T)in[i * V + j];
+          if (j >= skip[i]) p[col[i] + j] = (T)in[i * V + j];
       }
     }
   }
 };
 
-template <typename T, typename W, int TPR, int E>
+template <typename T, typename W, int TPR, int E, int V>
 __global__ __launch_bounds__(TPR < kBlock ? kBlock : TPR) void norm_forward(NormArgs a) {
-  using R = Row<T, TPR, E>;
+  using R = Row<T, TPR, E, V>;
   constexpr int kThreads = TPR < kBlock ? kBlock : TPR;
   constexpr int kRows = kThreads / TPR;
   __shared__ float smem[kThreads / 64];
   const int t = threadIdx.x % TPR;
-  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
-  if (row >= a.rows) return;   // whole blocks where TPR > 64: a block then holds one row
-  float v[E];
-  R::load((const T*)a.x + row * a.ldx, a.cols, t, v);
-  float s = 0.0f;
+  const R r(a.cols, t);
+  // A block takes rows in turn: the parameters stay in its registers (as they
+  // lie in memory), and the next row is on its way while this one is worked
+  // on.  Every thread runs the same number of turns; a row past the end is
+  // the last one again and not stored.
+  const int64_t stride = (int64_t)gridDim.x * kRows;
+  int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+  typename R::template Raw<T> next;
+  typename R::template Raw<W> w, b;
+  auto fetch = [&](int64_t i) { r.template load<T>((const T*)a.x + (i < a.rows ? i : a.rows - 1) * a.ldx, next); };
+  fetch(row);
+  if (a.weight) r.template load<W>((const W*)a.weight, w);
+  if (a.bias) r.template load<W>((const W*)a.bias, b);
+  for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.rows; base += stride, row += stride) {
+    float v[E];
+    r.template widen<T>(next, v);
+    fetch(row + stride);
+    float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < E; i++) s += v[i];
-  const float mean = row_sum<TPR>(s, smem) * a.inv_cols;
-  s = 0.0f;
+    for (int i = 0; i < E; i++) s += v[i];
+    const float mean = row_sum<TPR>(s, smem) * a.inv_cols;
 #pragma unroll
-  for (int i = 0; i < R::P; i++)
+    for (int i = 0; i < E; i++) v[i] -= mean;
+    r.clear(v);
+    s = 0.0f;
 #pragma unroll
-    for (int j = 0; j < R::V; j++) {
-      float& e = v[i * R::V + j];
-      e = R::col(i, t) + j < a.cols ? e - mean : 0.0f;
-      s = fmaf(e, e, s);
+    for (int i = 0; i < E; i++) s = fmaf(v[i], v[i], s);
+    const float rstd = 1.0f / sqrtf(row_sum<TPR>(s, smem) * a.inv_cols + a.eps);
+    if (row >= a.rows) continue;
+    if (t == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
     }
-  const float rstd = 1.0f / sqrtf(row_sum<TPR>(s, smem) * a.inv_cols + a.eps);
-  if (t == 0) {
-    if (a.mean) a.mean[row] = mean;
-    if (a.rstd) a.rstd[row] = rstd;
-  }
-  float w[E], b[E];
-  R::template load_as<W>((const W*)a.weight, a.cols, t, w, 1.0f);
-  R::template load_as<W>((const W*)a.bias, a.cols, t, b, 0.0f);
 #pragma unroll
-  for (int i = 0; i < E; i++) v[i] = fmaf(v[i] * rstd, w[i], b[i]);
-  R::store((T*)a.y + row * a.ldy, a.cols, t, v);
+    for (int i = 0; i < E; i++) {
+      const float scale = a.weight ? (float)w.q[i / V].v[i % V] : 1.0f, shift = a.bias ? (float)b.q[i / V].v[i % V] : 0.0f;
+      v[i] = fmaf(v[i] * rstd, scale, shift);
+    }
+    r.store((T*)a.y + row * a.ldy, v);
+  }
 }
 
 // Rows too long for the registers: three passes, the later two from cache.
@@ -174,88 +198,84 @@ template <typename T, typename W> __global__ __launch_bounds__(1024) void norm_f
   }
 }
 
-template <typename T, typename W, int TPR, int E>
-__global__ __launch_bounds__(TPR < kBlock ? kBlock : TPR) void norm_backward(NormArgs a) {
-  using R = Row<T, TPR, E>;
-  constexpr int kThreads = TPR < kBlock ? kBlock : TPR;
-  constexpr int kRows = kThreads / TPR;
+template <typename T, typename W, int TPR, int E, int V, int kRows>
+__global__ __launch_bounds__(TPR * kRows) void norm_backward(NormArgs a) {
+  using R = Row<T, TPR, E, V>;
+  constexpr int kThreads = TPR * kRows;
   __shared__ float smem[kThreads / 64 * 2];
   const int t = threadIdx.x % TPR;
   const int lane_row = threadIdx.x / TPR;
-  float w[E], dw[E], db[E];
-  R::template load_as<W>((const W*)a.weight, a.cols, t, w, 1.0f);
+  const R r(a.cols, t);
+  // The next row is loaded while this one is worked on.  Every thread of a
+  // block runs the same number of turns; a row past the end is the last one
+  // again, not counted and not stored.
+  const int64_t stride = (int64_t)a.groups * kRows;
+  int64_t row = (int64_t)blockIdx.x * kRows + lane_row;
+  typename R::template Raw<T> rx, rdy;
+  float next_mean, next_rstd;
+  auto fetch = [&](int64_t i) {
+    i = i < a.rows ? i : a.rows - 1;
+    r.template load<T>((const T*)a.x + i * a.ldx, rx);
+    r.template load<T>((const T*)a.dy + i * a.lddy, rdy);
+    next_mean = a.mean[i];
+    next_rstd = a.rstd[i];
+  };
+  fetch(row);
+  float dw[E], db[E];
+  typename R::template Raw<W> wt;
+  if (a.weight) r.template load<W>((const W*)a.weight, wt);
+  auto weight = [&](int i) { return a.weight ? (float)wt.q[i / V].v[i % V] : 1.0f; };
 #pragma unroll
   for (int i = 0; i < E; i++) dw[i] = db[i] = 0.0f;
-  // every thread of a block runs the same number of turns; a row past the
-  // end is computed on zeros and not stored
-  for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.rows; base += (int64_t)a.groups * kRows) {
-    const int64_t row = base + lane_row;
+  for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.rows; base += stride, row += stride) {
     const bool live = row < a.rows;
     float h[E], dy[E];
-    float mean = 0.0f, rstd = 0.0f;
-    if (live) {
-      R::load((const T*)a.x + row * a.ldx, a.cols, t, h);
-      R::load((const T*)a.dy + row * a.lddy, a.cols, t, dy);
-      mean = a.mean[row];
-      rstd = a.rstd[row];
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; i++) h[i] = dy[i] = 0.0f;
-    }
+    r.template widen<T>(rx, h);
+    r.template widen<T>(rdy, dy);
+    const float mean = next_mean, rstd = next_rstd;
+    fetch(row + stride);
     float sg = 0.0f, sgh = 0.0f;
 #pragma unroll
-    for (int i = 0; i < R::P; i++)
-#pragma unroll
-      for (int j = 0; j < R::V; j++) {
-        const int e = i * R::V + j;
-        h[e] = R::col(i, t) + j < a.cols ? (h[e] - mean) * rstd : 0.0f;
-        dw[e] = fmaf(dy[e], h[e], dw[e]);
-        db[e] += dy[e];
-        dy[e] *= w[e];
-        sg += dy[e];
-        sgh = fmaf(dy[e], h[e], sgh);
-      }
+    for (int i = 0; i < E; i++) {
+      dy[i] = live ? dy[i] : 0.0f;
+      h[i] = (h[i] - mean) * rstd;
+      dw[i] = fmaf(dy[i], h[i], dw[i]);      // dy is 0 where a pack holds no element
+      db[i] += dy[i];
+      dy[i] *= weight(i);
+      sg += dy[i];
+      sgh = fmaf(dy[i], h[i], sgh);
+    }
     if (a.y) {
       row_sum2<TPR>(sg, sgh, smem);
       sg *= a.inv_cols;
       sgh *= a.inv_cols;
 #pragma unroll
       for (int i = 0; i < E; i++) dy[i] = rstd * (dy[i] - sg - h[i] * sgh);
-      if (live) R::store((T*)a.y + row * a.ldy, a.cols, t, dy);
+      if (live) r.store((T*)a.y + row * a.ldy, dy);
     }
   }
   if (!a.part) return;
   // the block's rows into one partial row
+  float* out = a.part + (int64_t)blockIdx.x * 2 * a.cols;
   if constexpr (kRows > 1) {
     __shared__ float rows[kRows][TPR * E];
 #pragma unroll
     for (int which = 0; which < 2; which++) {
       if (which) __syncthreads();
-#pragma unroll
-      for (int i = 0; i < R::P; i++)
-#pragma unroll
-        for (int j = 0; j < R::V; j++) rows[lane_row][R::col(i, t) + j] = which ? db[i * R::V + j] : dw[i * R::V + j];
+      r.each([&](int i, int c) { rows[lane_row][c] = which ? db[i] : dw[i]; });
       __syncthreads();
-      float* out = a.part + ((int64_t)which * a.groups + blockIdx.x) * a.cols;
-      for (int c = threadIdx.x; c < TPR * E && c < a.cols; c += kThreads) {
+      for (int c = threadIdx.x; c < a.cols; c += kThreads) {
         float s = 0.0f;
 #pragma unroll 4
-        for (int r = 0; r < kRows; r++) s += rows[r][c];
-        out[c] = s;
+        for (int i = 0; i < kRows; i++) s += rows[i][c];
+        out[which * a.cols + c] = s;
       }
     }
   } else {
-    float* out = a.part + (int64_t)blockIdx.x * a.cols;
-#pragma unroll
-    for (int i = 0; i < R::P; i++)
-#pragma unroll
-      for (int j = 0; j < R::V; j++) {
-        const int c = R::col(i, t) + j;
-        if (c < a.cols) {
-          out[c] = dw[i * R::V + j];
-          out[(int64_t)a.groups * a.cols + c] = db[i * R::V + j];
-        }
-      }
+    r.each([&](int i, int c) {
+      out[c] = dw[i];
+      out[a.cols + c] = db[i];
+    });
   }
 }
 
@@ -293,21 +313,32 @@ template <typename T> __global__ __launch_bounds__(256) void norm_params_long(No
     dw = fmaf(g, ((float)((const T*)a.x)[row * a.ldx + c] - a.mean[row]) * a.rstd[row], dw);
     db += g;
   }
-  a.part[(int64_t)blockIdx.y * a.cols + c] = dw;
-  a.part[((int64_t)a.groups + blockIdx.y) * a.cols + c] = db;
+  a.part[(int64_t)blockIdx.y * 2 * a.cols + c] = dw;
+  a.part[((int64_t)blockIdx.y * 2 + 1) * a.cols + c] = db;
 }
 
-template <typename O> __global__ __launch_bounds__(256) void col_sum(ColSumArgs a) {
-  __shared__ float smem[4][64];
-  const int64_t c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
-  const int w = threadIdx.x >> 6;
+// Column sums of the partial rows: a block takes 64 columns, its 16 waves
+// every 16th row, eight loads in flight each; then the waves' sums in order.
+template <typename O> __global__ __launch_bounds__(1024) void col_sum(ColSumArgs a) {
+  constexpr int kStrips = 16;
+  __shared__ float smem[kStrips][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
   float s = 0.0f;
-  if (c < a.cols)
-    for (int p = w; p < a.parts; p += 4) s += a.part[p * a.cols + c];
-  smem[w][threadIdx.x & 63] = s;
+  if (c < a.width) {
+    const float* p = a.part + c;
+#pragma unroll 8
+    for (int i = w; i < a.parts; i += kStrips) s += p[i * a.width];
+  }
+  smem[w][lane] = s;
   __syncthreads();
-  if (w == 0 && c < a.cols)
-    ((O*)a.out)[c] = (O)((smem[0][threadIdx.x] + smem[1][threadIdx.x]) + (smem[2][threadIdx.x] + smem[3][threadIdx.x]));
+  if (w == 0 && c < a.width) {
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kStrips; i++) s += smem[i][lane];
+    O* out = c < a.n0 ? (O*)a.out0 : (O*)a.out1;
+    if (out) out[c < a.n0 ? c : c - a.n0] = (O)s;
+  }
 }
 
 // Threads and elements per thread of a row: the smallest shape that holds it.
@@ -315,32 +346,38 @@ constexpr int kLongest = 1024 * 16;
 template <typename T, typename W> hipError_t forward(const NormArgs& a, hipStream_t st) {
   auto go = [&](auto kernel, int tpr) {
     const int threads = tpr < kBlock ? kBlock : tpr, rows = threads / tpr;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((a.rows + rows - 1) / rows)), dim3(threads), 0, st, a);
+    // 16 waves a CU, which the kernels' registers allow
+    const int64_t blocks = (a.rows + rows - 1) / rows, most = 256 * 1024 / threads;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(threads), 0, st, a);
     return hipGetLastError();
   };
-  if (a.cols <= 16 * 8) return go(norm_forward<T, W, 16, 8>, 16);
-  if (a.cols <= 64 * 8) return go(norm_forward<T, W, 64, 8>, 64);
-  if (a.cols <= 64 * 16) return go(norm_forward<T, W, 64, 16>, 64);
-  if (a.cols <= 256 * 8) return go(norm_forward<T, W, 256, 8>, 256);
-  if (a.cols <= 256 * 16) return go(norm_forward<T, W, 256, 16>, 256);
-  if (a.cols <= 512 * 16) return go(norm_forward<T, W, 512, 16>, 512);
-  if (a.cols <= kLongest) return go(norm_forward<T, W, 1024, 16>, 1024);
+  constexpr int V = 16 / sizeof(T);
+  if (a.cols < V) return go(norm_forward<T, W, 16, 1, 1>, 16);
+  if (a.cols <= 16 * 8) return go(norm_forward<T, W, 16, 8, V>, 16);
+  if (a.cols <= 64 * 8) return go(norm_forward<T, W, 64, 8, V>, 64);
+  if (a.cols <= 64 * 16) return go(norm_forward<T, W, 64, 16, V>, 64);
+  if (a.cols <= 256 * 8) return go(norm_forward<T, W, 256, 8, V>, 256);
+  if (a.cols <= 256 * 16) return go(norm_forward<T, W, 256, 16, V>, 256);
+  if (a.cols <= 512 * 16) return go(norm_forward<T, W, 512, 16, V>, 512);
+  if (a.cols <= kLongest) return go(norm_forward<T, W, 1024, 16, V>, 1024);
   hipLaunchKernelGGL((norm_forward_long<T, W>), dim3((unsigned)a.rows), dim3(1024), 0, st, a);
   return hipGetLastError();
 }
 
 template <typename T, typename W> hipError_t backward(const NormArgs& a, hipStream_t st) {
-  auto go = [&](auto kernel, int tpr) {
-    hipLaunchKernelGGL(kernel, dim3(a.groups), dim3(tpr < kBlock ? kBlock : tpr), 0, st, a);
+  auto go = [&](auto kernel, int threads) {
+    hipLaunchKernelGGL(kernel, dim3(a.groups), dim3(threads), 0, st, a);
     return hipGetLastError();
   };
-  if (a.cols <= 16 * 8) return go(norm_backward<T, W, 16, 8>, 16);
-  if (a.cols <= 64 * 8) return go(norm_backward<T, W, 64, 8>, 64);
-  if (a.cols <= 64 * 16) return go(norm_backward<T, W, 64, 16>, 64);
-  if (a.cols <= 256 * 8) return go(norm_backward<T, W, 256, 8>, 256);
-  if (a.cols <= 256 * 16) return go(norm_backward<T, W, 256, 16>, 256);
-  if (a.cols <= 512 * 16) return go(norm_backward<T, W, 512, 16>, 512);
-  if (a.cols <= kLongest) return go(norm_backward<T, W, 1024, 16>, 1024);
+  constexpr int V = 16 / sizeof(T);
+  if (a.cols < V) return go(norm_backward<T, W, 16, 1, 1, 16>, 256);
+  if (a.cols <= 16 * 8) return go(norm_backward<T, W, 16, 8, V, 16>, 256);
+  if (a.cols <= 64 * 8) return go(norm_backward<T, W, 64, 8, V, 8>, 512);
+  if (a.cols <= 64 * 16) return go(norm_backward<T, W, 64, 16, V, 8>, 512);
+  if (a.cols <= 256 * 8) return go(norm_backward<T, W, 256, 8, V, 2>, 512);
+  if (a.cols <= 256 * 16) return go(norm_backward<T, W, 256, 16, V, 2>, 512);
+  if (a.cols <= 512 * 16) return go(norm_backward<T, W, 512, 16, V, 1>, 512);
+  if (a.cols <= kLongest) return go(norm_backward<T, W, 512, 32, V, 1>, 512);
   if (a.y) {
     hipLaunchKernelGGL((norm_backward_long<T, W>), dim3((unsigned)a.rows), dim3(1024), 0, st, a);
     const hipError_t e = hipGetLastError();
@@ -352,11 +389,14 @@ template <typename T, typename W> hipError_t backward(const NormArgs& a, hipStre
 
 }  // namespace
 
-int norm_backward_groups(int dtype, int64_t rows, int cols) {
-  (void)dtype;
-  const int per = cols <= 128 ? 16 : cols <= 1024 ? 4 : 1;   // rows of a block at a time
+// Blocks of the backward grid, each of which leaves one partial row: enough
+// to fill the GPU (8 waves a CU), few enough that the partial rows stay small beside
+// the rows themselves.
+int norm_backward_groups(int64_t rows, int cols) {
+  if (cols > kLongest) return (int)(rows < 64 ? rows : 64);
+  const int per = cols <= 128 ? 16 : cols <= 1024 ? 8 : cols <= 4096 ? 2 : 1;   // rows of a block at a time
   const int64_t blocks = (rows + per - 1) / per;
-  const int most = cols <= kLongest ? 512 : 64;
+  const int64_t most = cols <= 128 ? 512 : 256;
   return (int)(blocks < most ? blocks : most);
 }
 
@@ -373,10 +413,10 @@ hipError_t launch_norm_backward(int dtype, int wdtype, const NormArgs& a, hipStr
 }
 
 hipError_t launch_col_sum(int out_dtype, const ColSumArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)((a.cols + 63) / 64));
-  if (out_dtype == kF32) hipLaunchKernelGGL(col_sum<float>, grid, dim3(256), 0, st, a);
-  else if (out_dtype == kF16) hipLaunchKernelGGL(col_sum<_Float16>, grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL(col_sum<__bf16>, grid, dim3(256), 0, st, a);
+  const dim3 grid((unsigned)((a.width + 63) / 64)), block(1024);
+  if (out_dtype == kF32) hipLaunchKernelGGL(col_sum<float>, grid, block, 0, st, a);
+  else if (out_dtype == kF16) hipLaunchKernelGGL(col_sum<_Float16>, grid, block, 0, st, a);
+  else hipLaunchKernelGGL(col_sum<__bf16>, grid, block, 0, st, a);
   return hipGetLastError();
 }
 
