@@ -461,7 +461,7 @@ ringar_result_t ringar_chunk_range(size_t count, ringar_dtype_t dtype, int nrank
  * too).  Matrices are row-major with a row stride in elements (ld; at least
  * the row's length, or 0 on an input to repeat one row), at any element
  * alignment; rows starting at 16-byte boundaries with in_features a multiple
- * of 16 bytes take the fast path.  Sizes lie in 0 .. 2^31 - 1; no rows is a
+ * of 16 bytes take the fast path.  Sizes lie in 0 .. 2^31 - 1025; no rows is a
  * successful call that writes zeros to the parameter gradients.  An output
  * must not overlap another operand (RINGAR_ERR_INVALID_USAGE) except where
  * said.  Results do not depend on scheduling (no atomic sums).

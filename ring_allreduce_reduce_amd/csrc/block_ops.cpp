@@ -99,7 +99,8 @@ struct Layout {
 // ---------------------------------------------------------------- checks
 size_t size_of(int dtype) { return dtype == kF32 ? 4 : 2; }
 bool type_ok(int dtype) { return dtype == kF16 || dtype == kBF16 || dtype == kF32; }
-constexpr int64_t kMaxDim = 0x7fffffff;
+constexpr int64_t kMaxPitch = 0x7fffffff;
+constexpr int64_t kMaxDim = kMaxPitch - 1024;   // sizes rounded up to tiles stay 32-bit
 
 // A matrix operand: rows x cols elements, row i at p + i * ld elements.
 struct Mat {
@@ -118,7 +119,7 @@ ringar_result_t check_mat(const Mat& m) {
   if ((uintptr_t)m.p % m.es) return refuse(RINGAR_ERR_INVALID_ARGUMENT, std::string(m.name) + " is not aligned to its element size");
   if (m.rows > 1 && m.ld < m.cols && !(m.ld == 0 && !m.output))
     return refuse(RINGAR_ERR_INVALID_ARGUMENT, std::string(m.name) + ": row stride below the row's length");
-  if (m.ld > kMaxDim) return refuse(RINGAR_ERR_INVALID_ARGUMENT, std::string(m.name) + ": row stride beyond 2^31 - 1 elements");
+  if (m.ld > kMaxPitch) return refuse(RINGAR_ERR_INVALID_ARGUMENT, std::string(m.name) + ": row stride beyond 2^31 - 1 elements");
   return RINGAR_SUCCESS;
 }
 

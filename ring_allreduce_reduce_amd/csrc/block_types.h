@@ -141,12 +141,14 @@ struct NormArgs {
 };
 
 // ------------------------------------------------- products and their epilogue
-// C[m][n] = sum_k A[m][k] B[n][k], the operands at any pair of strides.
-// Gated: n counts 2 * ceil16(F) logical columns in groups of 32, 16 gate
-// columns and then the same 16 up columns.
+// C[m][n] = sum_k A[m][k] B[n][k]; one of each operand's two strides is 1.
+// Gated: n counts the outputs; B has 2 n rows, the gate's and then the up
+// projection's.
 enum : int { kEpiStore = 0, kEpiLinear = 1, kEpiGated = 2 };
 
-enum : int { kGeneral = 0, kTile256 = 1, kTile128 = 2, kTile64 = 3 };
+// kernels of a product: tiles of 256 x 256, 128 x 128, 64 x 128 with direct
+// loads, 128 x 128 with loads through registers (any alignment)
+enum : int { kTile256 = 0, kTile128 = 1, kTile64 = 2, kStaged128 = 3 };
 
 struct GemmArgs {
   const void* a;
@@ -154,7 +156,7 @@ struct GemmArgs {
   int64_t sam, sak;      // strides of A in elements
   int64_t sbn, sbk;      // strides of B
   int m, n, k;           // n: output columns (gated: F)
-  int variant;           // kernel (kGeneral, ...), set with the split by plan_gemm
+  int variant;           // kernel, set with the split by plan_gemm
   int splits;            // parts of k, each a multiple of the tile's k
   int k_per_split;
   float* part;           // splits > 1: [splits][m][n, gated 2n]
@@ -166,8 +168,6 @@ struct GemmArgs {
   int64_t ldc, ldr, ldp;
   int act;
 };
-
-__host__ __device__ inline int64_t logical_cols(int epi, int64_t n) { return epi == kEpiGated ? (n + 15) / 16 * 32 : n; }
 
 // activation's backward pass and column sums
 struct DzArgs {

@@ -12,9 +12,9 @@ namespace {
 struct Tile {
   int m, n;
 };
-constexpr Tile kTiles[] = {{64, 64}, {256, 256}, {128, 128}, {64, 128}};
+constexpr Tile kTiles[] = {{256, 256}, {128, 128}, {64, 128}, {128, 128}};
 
-// Operands the tiled kernels take: rows (or k lines) that start at 16-byte
+// Operands the direct loads take: rows (or k lines) that start at 16-byte
 // boundaries, and offsets within a tile that fit the loads' 32 bits.
 bool operand_ok(const void* p, int64_t pitch, bool rows, int es, int64_t extra_rows) {
   const int64_t bytes = pitch * es;
@@ -26,7 +26,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 int64_t tiles_of(int variant, int epi, const GemmArgs& a) {
   const Tile t = kTiles[variant];
-  const int64_t cols = variant == kGeneral ? logical_cols(epi, a.n) : epi == kEpiGated ? 2 * (int64_t)a.n : a.n;
+  const int64_t cols = epi == kEpiGated ? 2 * (int64_t)a.n : a.n;
   return ceil_div(a.m, t.m) * ceil_div(cols, t.n);
 }
 
@@ -35,18 +35,15 @@ int64_t tiles_of(int variant, int epi, const GemmArgs& a) {
 size_t plan_gemm(int dtype, int epi, GemmArgs& a) {
   a.splits = 1;
   a.k_per_split = a.k;
-  a.variant = kGeneral;
+  a.variant = kStaged128;
   if (a.m == 0 || a.n == 0) return 0;
   const int es = dtype == kF32 ? 4 : 2;
   const bool arow = a.sak == 1, brow = a.sbk == 1;
   const int64_t wide = epi == kEpiGated ? 2 * (int64_t)a.n : a.n;
-  const bool tiled = operand_ok(a.a, arow ? a.sam : a.sak, arow, es, 0) &&
+  const bool direct = operand_ok(a.a, arow ? a.sam : a.sak, arow, es, 0) &&
                      operand_ok(a.b, brow ? a.sbn : a.sbk, brow, es, epi == kEpiGated ? a.n : 0);
-  int step = es == 4 ? 16 : 32;
-  if (tiled) {
-    step = 128 / es;
-    a.variant = tiles_of(kTile256, epi, a) >= 192 && es == 2 ? kTile256 : arow && a.m <= 64 ? kTile64 : kTile128;
-  }
+  const int step = 128 / es;
+  a.variant = !direct ? kStaged128 : tiles_of(kTile256, epi, a) >= 192 && es == 2 ? kTile256 : arow && a.m <= 64 ? kTile64 : kTile128;
   // parts of k: enough blocks to fill the GPU where the output has few tiles
   const int64_t tiles = tiles_of(a.variant, epi, a), steps = ceil_div(a.k, step);
   const int64_t want = a.variant == kTile256 ? 256 : 512;

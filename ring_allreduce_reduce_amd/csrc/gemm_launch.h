@@ -10,23 +10,22 @@ inline unsigned blocks_of(const GemmArgs& a, int cols_of_tile, int rows_of_tile,
   return (unsigned)((cols + cols_of_tile - 1) / cols_of_tile * (((int64_t)a.m + rows_of_tile - 1) / rows_of_tile) * a.splits);
 }
 
-template <typename T, int EPI> hipError_t launch_general(const GemmArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((gemm_general<T, EPI>), dim3(blocks_of(a, 64, 64, logical_cols(EPI, a.n))), dim3(256), 0, st, a);
-  return hipGetLastError();
-}
-
 template <typename T, bool AROW, bool BROW, int EPI> hipError_t launch_tiled(const GemmArgs& a, hipStream_t st) {
   const int64_t cols = EPI == kEpiGated ? 2 * (int64_t)a.n : a.n;
-  if (a.variant == kTile256) {
-    if constexpr (sizeof(T) == 2)
-      hipLaunchKernelGGL((gemm_tile<T, AROW, BROW, EPI, 256, 256, 2, 4, 2>), dim3(blocks_of(a, 256, 256, cols)), dim3(512), 0, st, a);
-  } else if (a.variant == kTile128) {
-    hipLaunchKernelGGL((gemm_tile<T, AROW, BROW, EPI, 128, 128, 2, 2, 2>), dim3(blocks_of(a, 128, 128, cols)), dim3(256), 0, st, a);
-  } else {
-    if constexpr (AROW)
-      hipLaunchKernelGGL((gemm_tile<T, AROW, BROW, EPI, 64, 128, 1, 2, 1>), dim3(blocks_of(a, 128, 64, cols)), dim3(128), 0, st, a);
+  auto go = [&](auto kernel, int bm, int bn, int threads) {
+    hipLaunchKernelGGL(kernel, dim3(blocks_of(a, bn, bm, cols)), dim3(threads), 0, st, a);
+    return hipGetLastError();
+  };
+  switch (a.variant) {
+    case kTile256:
+      if constexpr (sizeof(T) == 2) return go(gemm_tile<T, AROW, BROW, EPI, 256, 256, 2, 4, 2, true>, 256, 256, 512);
+      return hipErrorInvalidValue;
+    case kTile64:
+      if constexpr (AROW) return go(gemm_tile<T, AROW, BROW, EPI, 64, 128, 1, 2, 1, true>, 64, 128, 128);
+      return hipErrorInvalidValue;
+    case kTile128: return go(gemm_tile<T, AROW, BROW, EPI, 128, 128, 2, 2, 2, true>, 128, 128, 256);
+    default: return go(gemm_tile<T, AROW, BROW, EPI, 128, 128, 2, 2, 2, false>, 128, 128, 256);
   }
-  return hipGetLastError();
 }
 
 template <typename T, int EPI> hipError_t join(const GemmArgs& a, hipStream_t st) {

@@ -7,16 +7,14 @@ hipError_t launch_nn_f32(const GemmArgs& a, hipStream_t st);
 hipError_t launch_tn_f32(const GemmArgs& a, hipStream_t st);
 
 template <int EPI> static hipError_t forward(const GemmArgs& a, hipStream_t st) {
-  const hipError_t e = a.variant == kGeneral ? launch_general<float, EPI>(a, st) : launch_tiled<float, true, true, EPI>(a, st);
+  const hipError_t e = launch_tiled<float, true, true, EPI>(a, st);
   return e == hipSuccess ? join<float, EPI>(a, st) : e;
 }
 
 hipError_t launch_gemm_f32(int epi, const GemmArgs& a, hipStream_t st) {
   if (epi == kEpiLinear) return forward<kEpiLinear>(a, st);
   if (epi == kEpiGated) return forward<kEpiGated>(a, st);
-  const hipError_t e = a.variant == kGeneral ? launch_general<float, kEpiStore>(a, st)
-                       : a.sak == 1         ? launch_nn_f32(a, st)
-                                            : launch_tn_f32(a, st);
+  const hipError_t e = a.sak == 1 ? launch_nn_f32(a, st) : launch_tn_f32(a, st);
   return e == hipSuccess ? join<float, kEpiStore>(a, st) : e;
 }
 

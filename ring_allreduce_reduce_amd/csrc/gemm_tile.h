@@ -1,5 +1,4 @@
-// The tiled product kernel for operands whose rows start at 16-byte
-// boundaries.
+// The tiled product kernel.
 //
 // A block of WM x WN waves computes a BM x BN tile of C in steps of 128 bytes
 // of k.  Operand tiles go from memory straight into LDS (16 bytes a lane, no
@@ -23,6 +22,8 @@
 // 64 consecutive columns of a row and everything the epilogue reads or writes
 // moves in whole 128-byte lines.
 #pragma once
+
+#include <type_traits>
 
 #include "gemm_kernel.h"
 
@@ -141,6 +142,70 @@ template <typename T, bool ROW, int R, int NW> struct Operand {
   }
 };
 
+// An operand at any alignment: the same tile in LDS, its chunks loaded to
+// registers a step ahead and written from there.  Chunks that pass the end
+// of a row (ROW: k, COL: columns) are put together value by value, zeros
+// past the end, so nothing beyond the operand is read.
+template <typename T, bool ROW, int R, int NW> struct StagedOperand : Operand<T, ROW, R, NW> {
+  using Base = Operand<T, ROW, R, NW>;
+  static constexpr int kVec = Base::kVec, kLoads = Base::kLoads, kChunks = Base::kChunks;
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const T* from[kLoads];
+  int at[kLoads];          // ROW: first k of the chunk; COL: k line
+  int columns[kLoads];     // COL: columns left from the chunk's first
+  u32x4 data[kLoads];
+  int64_t step_elems;
+  int k_end;
+
+  template <typename F>
+  __device__ inline void offsets(const T* p, int64_t pitch, int k_begin, int k_stop, int64_t cols_left, int wave, int lane, F row_offset) {
+    k_end = k_stop;
+    step_elems = ROW ? Base::kBK : Base::kBK * pitch;
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) {
+      const int idx = i * NW + wave;
+      if constexpr (ROW) {
+        const int r = idx * 8 + (lane >> 3), c = (lane & 7) ^ (r & 7);
+        at[i] = k_begin + c * kVec;
+        from[i] = p + row_offset(r) + c * kVec;
+      } else {
+        const int k = idx * (64 / kChunks) + lane / kChunks, q = (lane % kChunks) ^ Base::col_swizzle(k);
+        at[i] = k_begin + k;
+        from[i] = p + k * pitch + q * kVec;
+        const int64_t left = cols_left - q * kVec;
+        columns[i] = (int)(left < 0 ? 0 : left > kVec ? kVec : left);
+      }
+    }
+  }
+
+  __device__ inline void load() {
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) {
+      const int n = ROW ? k_end - at[i] : at[i] < k_end ? columns[i] : 0;
+      if (n >= kVec) {
+        __builtin_memcpy(&data[i], from[i], 16);
+      } else {
+        u32x4 v = {0, 0, 0, 0};
+        const T* p = from[i];
+#pragma unroll
+        for (int e = 0; e < kVec; e++)
+          if (e < n) {
+            if constexpr (sizeof(T) == 2) v[e / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[e]) << (e % 2 * 16);
+            else v[e] = __builtin_bit_cast(uint32_t, p[e]);
+          }
+        data[i] = v;
+      }
+      from[i] += step_elems;
+      at[i] += Base::kBK;
+    }
+  }
+
+  __device__ inline void commit(char* lds, int wave, int lane) {
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) *(u32x4*)(lds + (i * NW + wave) * 1024 + lane * 16) = data[i];
+  }
+};
+
 // Eight consecutive output columns of one row.
 template <typename T> __device__ inline void add8(const void* p, int64_t at, float* z) {
   const Pack<T, 8> b = load_pack<T, 8>((const T*)p + at);
@@ -207,11 +272,11 @@ __device__ inline void barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <typename T, bool AROW, bool BROW, int EPI, int BM, int BN, int WM, int WN, int OCC>
+template <typename T, bool AROW, bool BROW, int EPI, int BM, int BN, int WM, int WN, int OCC, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_tile(GemmArgs a) {
   constexpr int NW = WM * WN;
-  using OA = Operand<T, AROW, BM, NW>;
-  using OB = Operand<T, BROW, BN, NW>;
+  using OA = std::conditional_t<DIRECT, Operand<T, AROW, BM, NW>, StagedOperand<T, AROW, BM, NW>>;
+  using OB = std::conditional_t<DIRECT, Operand<T, BROW, BN, NW>, StagedOperand<T, BROW, BN, NW>>;
   constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr int kBK = OA::kBK;
   static_assert(TN == 64, "eight lanes finish a wave's row");
@@ -245,26 +310,34 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_tile(GemmArgs a) {
   OA oa;
   OB ob;
   {
-    const int64_t pa = (AROW ? a.sam : a.sak) * (int64_t)sizeof(T), pb = (BROW ? a.sbn : a.sbk) * (int64_t)sizeof(T);
-    const int64_t rows_b = EPI == kEpiGated ? 2 * (int64_t)a.n : a.n;
-    const int64_t bytes_a = AROW ? (a.m - 1) * pa + (int64_t)a.k * sizeof(T) : (a.k - 1) * pa + (int64_t)a.m * sizeof(T);
-    const int64_t bytes_b = BROW ? (rows_b - 1) * pb + (int64_t)a.k * sizeof(T) : (a.k - 1) * pb + rows_b * (int64_t)sizeof(T);
-    oa.start(a.a, AROW ? m0 * pa + (int64_t)k_begin * sizeof(T) : k_begin * pa + m0 * (int64_t)sizeof(T), bytes_a, AROW ? 128 : kBK * pa);
-    ob.start(a.b, BROW ? n0 * pb + (int64_t)k_begin * sizeof(T) : k_begin * pb + n0 * (int64_t)sizeof(T), bytes_b, BROW ? 128 : kBK * pb);
+    const int64_t pitch_a = AROW ? a.sam : a.sak, pitch_b = BROW ? a.sbn : a.sbk;
     // rows past the edge read the last one; their results are not stored
-    oa.offsets(pa, wave, lane, [&](int r) {
-      const int64_t m = m0 + r < a.m ? r : a.m - 1 - m0;
-      return m * pa;
-    });
-    ob.offsets(pb, wave, lane, [&](int r) {
+    auto row_a = [&](int r) { return m0 + r < a.m ? (int64_t)r : a.m - 1 - m0; };
+    auto row_b = [&](int r) -> int64_t {
       if constexpr (EPI == kEpiGated) {
         // 64 rows: 32 of the gate, then the same 32 of the up projection
         const int64_t c = (r >> 6) * 32 + (r & 31);
-        return ((n0 + c < a.n ? c : a.n - 1 - n0) + (r & 32 ? a.n : 0)) * pb;
+        return (n0 + c < a.n ? c : a.n - 1 - n0) + (r & 32 ? a.n : 0);
       } else {
-        return (n0 + r < a.n ? r : a.n - 1 - n0) * pb;
+        return n0 + r < a.n ? r : a.n - 1 - n0;
       }
-    });
+    };
+    const int64_t first_a = AROW ? m0 * pitch_a + k_begin : k_begin * pitch_a + m0;
+    const int64_t first_b = BROW ? n0 * pitch_b + k_begin : k_begin * pitch_b + n0;
+    if constexpr (DIRECT) {
+      constexpr int64_t es = sizeof(T);
+      const int64_t rows_b = EPI == kEpiGated ? 2 * (int64_t)a.n : a.n;
+      const int64_t size_a = AROW ? (a.m - 1) * pitch_a + a.k : (a.k - 1) * pitch_a + a.m;
+      const int64_t size_b = BROW ? (rows_b - 1) * pitch_b + a.k : (a.k - 1) * pitch_b + rows_b;
+      oa.start(a.a, first_a * es, size_a * es, AROW ? 128 : kBK * pitch_a * es);
+      ob.start(a.b, first_b * es, size_b * es, BROW ? 128 : kBK * pitch_b * es);
+      oa.offsets(pitch_a * es, wave, lane, [&](int r) { return row_a(r) * pitch_a * es; });
+      ob.offsets(pitch_b * es, wave, lane, [&](int r) { return row_b(r) * pitch_b * es; });
+    } else {
+      const int k_stop = k_begin + k_len;
+      oa.offsets((const T*)a.a + first_a, pitch_a, k_begin, k_stop, a.m - m0, wave, lane, [&](int r) { return row_a(r) * pitch_a; });
+      ob.offsets((const T*)a.b + first_b, pitch_b, k_begin, k_stop, a.n - n0, wave, lane, [&](int r) { return row_b(r) * pitch_b; });
+    }
   }
 
   f32x4 acc[FN][FM];
@@ -273,12 +346,25 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_tile(GemmArgs a) {
 #pragma unroll
     for (int j = 0; j < FM; j++) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
+  // DIRECT: starts the loads of the next step into buffer `buf`.  Otherwise
+  // they go to registers here and to LDS in commit().
   auto issue = [&](int buf) {
-    oa.load(smem + buf * kStage, wave);
-    ob.load(smem + buf * kStage + OA::kBytes, wave);
+    if constexpr (DIRECT) {
+      oa.load(smem + buf * kStage, wave);
+      ob.load(smem + buf * kStage + OA::kBytes, wave);
+    } else {
+      oa.load();
+      ob.load();
+    }
+  };
+  auto commit = [&](int buf) {
+    if constexpr (!DIRECT) {
+      oa.commit(smem + buf * kStage, wave, lane);
+      ob.commit(smem + buf * kStage + OA::kBytes, wave, lane);
+    }
   };
   auto fix_tail = [&](int s) {        // the last step, where k ends inside it
-    if (s == steps - 1 && k_len % kBK != 0) {
+    if (DIRECT && s == steps - 1 && k_len % kBK != 0) {
       OA::clear_tail(smem + (s & 1) * kStage, k_len % kBK);
       OB::clear_tail(smem + (s & 1) * kStage + OA::kBytes, k_len % kBK);
       wait_loads();
@@ -303,6 +389,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_tile(GemmArgs a) {
   if (steps > 0) {
     Frag fa0[FM], fb0[FN], fa1[FM], fb1[FN];
     issue(0);
+    commit(0);
     wait_loads();
     barrier();
     fix_tail(0);
@@ -311,6 +398,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_tile(GemmArgs a) {
     for (int s = 0; s < steps - 1; s++) {
       read(s & 1, 1, fa1, fb1);
       mma(fa0, fb0);
+      commit((s + 1) & 1);      // its readers of step s - 1 passed the last barrier
       wait_loads();
       barrier();
       fix_tail(s + 1);
