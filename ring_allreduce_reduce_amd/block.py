@@ -42,8 +42,8 @@ ringar_linear_backward_t = _struct(
     ("weight", _vp), ("ldw", _i64), ("dx", _vp), ("lddx", _i64), ("dweight", _vp), ("lddw", _i64), ("dbias", _vp))
 
 _fns = {}
-_torch = None
 _types = {}
+_torch = _device_now = _stream_now = None
 
 
 def _fn(name):
@@ -57,9 +57,11 @@ def _fn(name):
 
 
 def _setup():
-    global _torch
+    global _torch, _device_now, _stream_now
     import torch
+    torch.cuda.init()
     _types.update({torch.float16: 2, torch.bfloat16: 3, torch.float32: 4})
+    _device_now, _stream_now = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     _torch = torch
 
 
@@ -67,31 +69,36 @@ def _bad(why):
     raise RingarError(INVALID_ARGUMENT, why)
 
 
-def _type(t):
+def _begin(x):
+    """(dtype, its code, device index) of the operand that the others go by."""
+    device = x.get_device()
+    if device < 0:
+        _bad("the operands must be CUDA tensors")
     if _torch is None:
         _setup()
-    code = _types.get(t.dtype)
+    dtype = x.dtype
+    code = _types.get(dtype)
     if code is None:
-        _bad(f"unsupported dtype {t.dtype}: float16, bfloat16 or float32")
-    return code
+        _bad(f"unsupported dtype {dtype}: float16, bfloat16 or float32")
+    return dtype, code, device
 
 
-def _rows(t, what, like=None):
+def _rows(t, what, dtype, device):
     """(rows, columns, row stride) of a tensor whose last dimension is contiguous."""
-    if not t.is_cuda:
-        _bad(f"{what} must be a CUDA tensor")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+    if t.dtype is not dtype or t.get_device() != device:
         _bad(f"{what} must have the dtype and device of the other operands")
     shape, stride = t.shape, t.stride()
     n = len(shape)
+    if n == 2:
+        rows, cols = shape
+        if stride[1] != 1 and cols > 1:
+            _bad(f"{what}: the last dimension must be contiguous")
+        return rows, cols, stride[0] if rows > 1 else cols
     if n == 0:
         _bad(f"{what} needs at least one dimension")
     cols = shape[-1]
     if cols > 1 and stride[-1] != 1:
         _bad(f"{what}: the last dimension must be contiguous")
-    if n == 2:
-        rows = shape[0]
-        return rows, cols, stride[0] if rows > 1 else cols
     rows, ld = 1, None
     for size, step in zip(reversed(shape[:-1]), reversed(stride[:-1])):
         if size == 0:
@@ -109,55 +116,42 @@ def _rows(t, what, like=None):
 def _vector(t, n, what, dtype, device):
     if t is None:
         return None
-    if t.dtype != dtype or t.device != device or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.dtype is not dtype or t.get_device() != device or t.shape != (n,) or not t.is_contiguous():
         _bad(f"{what} must be a contiguous vector of {n} values of {dtype} on the operands' GPU")
     return t.data_ptr()
 
 
-class _On:
-    """The stream a call runs on; tensors made inside belong to it, and
-    ``uses`` keeps the caller's tensors alive until its work is done where it
-    is not their own."""
+def _call(name, args, device):
+    code = _fn(name)(ctypes.byref(args), _stream_now(device))
+    if code != SUCCESS:
+        raise RingarError(code, f"{name} ({ringar_last_error()})")
 
-    def __init__(self, x, stream):
-        self.device = x.device.index
-        self.other = None
-        if stream is not None and stream.cuda_stream != _torch._C._cuda_getCurrentRawStream(self.device):
-            self.other = _torch.cuda.stream(stream)
-            self.stream = stream
-        elif self.device != _torch.cuda.current_device():
-            self.other = _torch.cuda.device(self.device)
-            self.stream = None
+
+class _Elsewhere:
+    """Runs a call on another stream or GPU than the current one: outputs are
+    made there, and the caller's tensors are kept until its work is done."""
+
+    def __init__(self, device, stream, *tensors):
+        self.device, self.stream, self.tensors = _torch.cuda.device(device), stream, tensors
+        if stream is not None and stream.device_index != device:
+            _bad("the stream belongs to another GPU than the operands")
+        self.on = _torch.cuda.stream(stream)
 
     def __enter__(self):
-        if self.other is not None:
-            self.other.__enter__()
-        return self
+        self.device.__enter__()
+        self.on.__enter__()
 
     def __exit__(self, *exc):
-        if self.other is not None:
-            self.other.__exit__(*exc)
-
-    def call(self, name, args, *tensors):
-        code = _fn(name)(ctypes.byref(args), _torch._C._cuda_getCurrentRawStream(self.device))
-        if code != SUCCESS:
-            raise RingarError(code, f"{name} ({ringar_last_error()})")
-        if self.other is not None and self.stream is not None:
-            for t in tensors:
+        if exc[0] is None and self.stream is not None:
+            for t in self.tensors:
                 if t is not None:
                     t.record_stream(self.stream)
+        self.on.__exit__(*exc)
+        self.device.__exit__(*exc)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
-
-
-def _out(out, like, shape, what):
-    if out is None:
-        return _torch.empty(shape, dtype=like.dtype, device=like.device)
-    if tuple(out.shape) != tuple(shape):
-        _bad(f"{what} must have shape {tuple(shape)}")
-    return out
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, *, stats=False, out=None, stream=None):
@@ -166,22 +160,28 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, *, stats=False, out=None, st
     ``weight`` and ``bias``: vectors of x's dtype or both float32.  ``stats``:
     return ``(y, mean, rstd)``, the float32 row statistics that
     ``layer_norm_backward`` takes.  ``out``: where y goes (it may be x)."""
-    code = _type(x)
-    rows, cols, ldx = _rows(x, "x")
+    dtype, code, device = _begin(x)
+    if stream is not None or device != _device_now():
+        with _Elsewhere(device, stream, x, weight, bias, out):
+            return layer_norm(x, weight, bias, eps, stats=stats, out=out)
+    rows, cols, ldx = _rows(x, "x", dtype, device)
     p = weight if weight is not None else bias
-    pdtype = x.dtype if p is None else p.dtype
-    w = _vector(weight, cols, "weight", pdtype, x.device)
-    b = _vector(bias, cols, "bias", pdtype, x.device)
-    with _On(x, stream) as on:
-        y = _out(out, x, x.shape, "out")
-        ldy = _rows(y, "out", x)[2]
-        mean = rstd = None
-        if stats:
-            mean = _torch.empty(x.shape[:-1], dtype=_torch.float32, device=x.device)
-            rstd = _torch.empty_like(mean)
-        on.call("ringar_layer_norm",
-                ringar_layer_norm_t(code, code if p is None else _type(p), rows, cols, x.data_ptr(), ldx, w, b, eps,
-                                    y.data_ptr(), ldy, _ptr(mean), _ptr(rstd)), x, weight, bias, out)
+    pdtype = dtype if p is None else p.dtype
+    w = _vector(weight, cols, "weight", pdtype, device)
+    b = _vector(bias, cols, "bias", pdtype, device)
+    if out is None:
+        y, ldy = x.new_empty(x.shape), cols
+    else:
+        y, ldy = out, _rows(out, "out", dtype, device)[2]
+        if out.shape != x.shape:
+            _bad("out must have x's shape")
+    mean = rstd = None
+    if stats:
+        mean = _torch.empty(x.shape[:-1], dtype=_torch.float32, device=x.device)
+        rstd = _torch.empty_like(mean)
+    _call("ringar_layer_norm",
+          ringar_layer_norm_t(code, _types.get(pdtype, -1), rows, cols, x.data_ptr(), ldx, w, b, eps, y.data_ptr(), ldy,
+                              _ptr(mean), _ptr(rstd)), device)
     return (y, mean, rstd) if stats else y
 
 
@@ -189,53 +189,58 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, dx=True, dweight=True
     """``(dx, dweight, dbias)`` of ``layer_norm``; one whose flag is False is
     not computed and None.  The parameter gradients have the weight's dtype
     (x's without a weight)."""
-    code = _type(x)
-    rows, cols, ldx = _rows(x, "x")
-    r2, c2, lddy = _rows(dy, "dy", x)
-    if (r2, c2) != (rows, cols):
+    dtype, code, device = _begin(x)
+    if stream is not None or device != _device_now():
+        with _Elsewhere(device, stream, dy, x, mean, rstd, weight):
+            return layer_norm_backward(dy, x, mean, rstd, weight, dx=dx, dweight=dweight, dbias=dbias)
+    rows, cols, ldx = _rows(x, "x", dtype, device)
+    r2, c2, lddy = _rows(dy, "dy", dtype, device)
+    if r2 != rows or c2 != cols:
         _bad("dy must have x's shape")
     for t, what in ((mean, "mean"), (rstd, "rstd")):
-        if t.dtype != _torch.float32 or t.numel() != rows or not t.is_contiguous() or t.device != x.device:
+        if t.dtype is not _torch.float32 or t.numel() != rows or not t.is_contiguous() or t.get_device() != device:
             _bad(f"{what} must be {rows} contiguous float32 values on x's GPU")
-    pdtype = x.dtype if weight is None else weight.dtype
-    w = _vector(weight, cols, "weight", pdtype, x.device)
-    with _On(x, stream) as on:
-        gx = _torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx else None
-        gw = _torch.empty(cols, dtype=pdtype, device=x.device) if dweight else None
-        gb = _torch.empty(cols, dtype=pdtype, device=x.device) if dbias else None
-        on.call("ringar_layer_norm_backward",
-                ringar_layer_norm_backward_t(code, code if weight is None else _type(weight), rows, cols,
-                                             dy.data_ptr(), lddy, x.data_ptr(), ldx, mean.data_ptr(),
-                                             rstd.data_ptr(), w, _ptr(gx), cols, _ptr(gw), _ptr(gb)),
-                dy, x, mean, rstd, weight)
+    pdtype = dtype if weight is None else weight.dtype
+    w = _vector(weight, cols, "weight", pdtype, device)
+    gx = x.new_empty(x.shape) if dx else None
+    gw = x.new_empty(cols, dtype=pdtype) if dweight else None
+    gb = x.new_empty(cols, dtype=pdtype) if dbias else None
+    _call("ringar_layer_norm_backward",
+          ringar_layer_norm_backward_t(code, _types.get(pdtype, -1), rows, cols, dy.data_ptr(), lddy, x.data_ptr(), ldx,
+                                       mean.data_ptr(), rstd.data_ptr(), w, _ptr(gx), cols, _ptr(gw), _ptr(gb)), device)
     return gx, gw, gb
 
 
 def _forward(name, gated, x, weight, bias, act, residual, save_pre, out, stream):
-    code = _type(x)
-    if act not in ACTS:
+    dtype, code, device = _begin(x)
+    if stream is not None or device != _device_now():
+        with _Elsewhere(device, stream, x, weight, bias, residual, out):
+            return _forward(name, gated, x, weight, bias, act, residual, save_pre, out, None)
+    a = ACTS.get(act)
+    if a is None:
         _bad(f"unknown activation {act!r}: one of {', '.join(ACTS)}")
-    rows, k, ldx = _rows(x, "x")
-    if weight.dim() != 2:
-        _bad("weight must have two dimensions")
-    wide, k2, ldw = _rows(weight, "weight", x)
-    if k2 != k or (gated and wide % 2):
+    rows, k, ldx = _rows(x, "x", dtype, device)
+    wide, k2, ldw = _rows(weight, "weight", dtype, device)
+    if k2 != k or weight.dim() != 2 or (gated and wide % 2):
         _bad("weight must be out_features x in_features" if not gated else "weight must be 2 out_features x in_features")
     n = wide // 2 if gated else wide
-    b = _vector(bias, wide, "bias", x.dtype, x.device)
-    ldr = 0
+    b = _vector(bias, wide, "bias", dtype, device)
+    r, ldr = None, 0
     if residual is not None:
-        rr, rc, ldr = _rows(residual, "residual", x)
-        if (rr, rc) != (rows, n):
+        rr, rc, ldr = _rows(residual, "residual", dtype, device)
+        if rr != rows or rc != n:
             _bad("residual must have the output's shape")
+        r = residual.data_ptr()
     lead = x.shape[:-1]
-    with _On(x, stream) as on:
-        y = _out(out, x, (*lead, n), "out")
-        ldy = _rows(y, "out", x)[2]
-        pre = _torch.empty((*lead, wide), dtype=x.dtype, device=x.device) if save_pre else None
-        on.call(name, ringar_linear_t(code, ACTS[act], rows, k, n, x.data_ptr(), ldx, weight.data_ptr(), ldw, b,
-                                      _ptr(residual), ldr, y.data_ptr(), ldy, _ptr(pre), wide),
-                x, weight, bias, residual, out)
+    if out is None:
+        y, ldy = x.new_empty((*lead, n)), n
+    else:
+        y, ldy = out, _rows(out, "out", dtype, device)[2]
+        if out.shape != (*lead, n):
+            _bad(f"out must have shape {(*lead, n)}")
+    pre = x.new_empty((*lead, wide)) if save_pre else None
+    _call(name, ringar_linear_t(code, a, rows, k, n, x.data_ptr(), ldx, weight.data_ptr(), ldw, b, r, ldr, y.data_ptr(),
+                                ldy, _ptr(pre), wide), device)
     return (y, pre) if save_pre else y
 
 
@@ -255,22 +260,26 @@ def gated_ffn(x, weight, bias=None, *, act="silu", save_pre=False, out=None, str
 
 
 def _backward(name, gated, dy, x, weight, pre, act, dx, dweight, dbias, stream):
-    code = _type(dy)
-    if act not in ACTS:
+    dtype, code, device = _begin(dy)
+    if stream is not None or device != _device_now():
+        with _Elsewhere(device, stream, dy, x, weight, pre):
+            return _backward(name, gated, dy, x, weight, pre, act, dx, dweight, dbias, None)
+    a = ACTS.get(act)
+    if a is None:
         _bad(f"unknown activation {act!r}: one of {', '.join(ACTS)}")
-    rows, n, lddy = _rows(dy, "dy")
+    rows, n, lddy = _rows(dy, "dy", dtype, device)
     wide = 2 * n if gated else n
     px = pw = pp = None
     ldx = ldw = ldp = k = 0
     if x is not None:
-        rx, k, ldx = _rows(x, "x", dy)
+        rx, k, ldx = _rows(x, "x", dtype, device)
         px = x.data_ptr()
         if rx != rows:
             _bad("x and dy must have the same rows")
     elif dweight:
         _bad("the weight's gradient needs x")
     if weight is not None:
-        rw, kw, ldw = _rows(weight, "weight", dy)
+        rw, kw, ldw = _rows(weight, "weight", dtype, device)
         pw = weight.data_ptr()
         if rw != wide or weight.dim() != 2 or (x is not None and kw != k):
             _bad("weight does not fit dy and x")
@@ -278,19 +287,17 @@ def _backward(name, gated, dy, x, weight, pre, act, dx, dweight, dbias, stream):
     elif dx:
         _bad("x's gradient needs the weight")
     if pre is not None:
-        rp, cp, ldp = _rows(pre, "pre", dy)
+        rp, cp, ldp = _rows(pre, "pre", dtype, device)
         pp = pre.data_ptr()
-        if (rp, cp) != (rows, wide):
+        if rp != rows or cp != wide:
             _bad(f"pre must have {wide} columns and dy's rows")
-    elif gated or act != "none":
+    elif gated or a:
         _bad("pre, kept by the forward pass, is needed")
-    with _On(dy, stream) as on:
-        kw = dict(dtype=dy.dtype, device=dy.device)
-        gx = _torch.empty((*dy.shape[:-1], k), **kw) if dx else None
-        gw = _torch.empty((wide, k), **kw) if dweight else None
-        gb = _torch.empty(wide, **kw) if dbias else None
-        on.call(name, ringar_linear_backward_t(code, ACTS[act], rows, k, n, dy.data_ptr(), lddy, pp, ldp, px, ldx,
-                                               pw, ldw, _ptr(gx), k, _ptr(gw), k, _ptr(gb)), dy, x, weight, pre)
+    gx = dy.new_empty((*dy.shape[:-1], k)) if dx else None
+    gw = dy.new_empty((wide, k)) if dweight else None
+    gb = dy.new_empty(wide) if dbias else None
+    _call(name, ringar_linear_backward_t(code, a, rows, k, n, dy.data_ptr(), lddy, pp, ldp, px, ldx, pw, ldw, _ptr(gx), k,
+                                         _ptr(gw), k, _ptr(gb)), device)
     return gx, gw, gb
 
 

@@ -14,6 +14,7 @@
 
 #include "block_types.h"
 #include "op_host.h"
+#include "ring_kernel.h"
 #include "ringar.h"
 
 using namespace ringar;
@@ -57,9 +58,14 @@ struct Workspace {
 std::mutex g_ws_mu;
 std::map<std::pair<int, hipStream_t>, Workspace> g_ws;
 
+// The buffer starts with kCounters zeroed words, which every kernel that uses
+// one leaves at zero; *out is what follows them.
+constexpr size_t kCounterBytes = kCounters * sizeof(uint32_t);
+
 ringar_result_t workspace(hipStream_t st, size_t bytes, char** out) {
   *out = nullptr;
   if (bytes == 0) return RINGAR_SUCCESS;
+  bytes += kCounterBytes;
   int dev = 0;
   HIP_TRY(hipGetDevice(&dev));
   hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
@@ -81,8 +87,9 @@ ringar_result_t workspace(hipStream_t st, size_t bytes, char** out) {
     const size_t want = (bytes + (4u << 20) - 1) / (4u << 20) * (4u << 20);
     HIP_TRY(hipMalloc((void**)&w.p, want));
     w.bytes = want;
+    HIP_TRY(launch_fill((uint64_t*)w.p, kCounterBytes / 8, 0, st));
   }
-  *out = w.p;
+  *out = w.p + kCounterBytes;
   return RINGAR_SUCCESS;
 }
 
@@ -325,6 +332,7 @@ static ringar_result_t product_forward(const ringar_linear_t* p, bool gated, hip
   char* ws = nullptr;
   TRY(workspace(st, part, &ws));
   a.part = (float*)ws;
+  if (ws) a.arrived = (uint32_t*)(ws - kCounterBytes);
   return run_gemm(p->dtype, epi, a, st);
 }
 

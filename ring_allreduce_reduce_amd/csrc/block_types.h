@@ -147,8 +147,12 @@ struct NormArgs {
 enum : int { kEpiStore = 0, kEpiLinear = 1, kEpiGated = 2 };
 
 // kernels of a product: tiles of 256 x 256, 128 x 128, 64 x 128 with direct
-// loads, 128 x 128 with loads through registers (any alignment)
-enum : int { kTile256 = 0, kTile128 = 1, kTile64 = 2, kStaged128 = 3 };
+// loads, 128 x 128 with loads through registers (any alignment),
+// and the forward product of up to 16 rows
+enum : int { kTile256 = 0, kTile128 = 1, kTile64 = 2, kStaged128 = 3, kRows = 4 };
+
+// kRows: blocks of columns
+inline int64_t rows_tiles(int epi, int64_t n) { return epi == kEpiGated ? (n + 7) / 8 : (n + 15) / 16; }
 
 struct GemmArgs {
   const void* a;
@@ -160,6 +164,7 @@ struct GemmArgs {
   int splits;            // parts of k, each a multiple of the tile's k
   int k_per_split;
   float* part;           // splits > 1: [splits][m][n, gated 2n]
+  uint32_t* arrived;     // kRows with splits > 1: a zero for every tile
   // epilogue
   const void* bias;      // n (gated: 2F), or null
   const void* residual;  // or null
@@ -204,6 +209,8 @@ int dz_groups(int64_t rows, int64_t cols);
 // Chooses the kernel and the split of k from sizes, strides and alignment
 // alone; returns the bytes of partial sums the launch needs.
 size_t plan_gemm(int dtype, int epi, GemmArgs& a);
+// Counters at the start of every workspace, zero between calls.
+constexpr int kCounters = 4096;
 // Blocks of the planned launch.
 int64_t gemm_blocks(int dtype, int epi, const GemmArgs& a);
 hipError_t launch_gemm(int dtype, int epi, const GemmArgs& a, hipStream_t st);

@@ -12,7 +12,7 @@ namespace {
 struct Tile {
   int m, n;
 };
-constexpr Tile kTiles[] = {{256, 256}, {128, 128}, {64, 128}, {128, 128}};
+constexpr Tile kTiles[] = {{256, 256}, {128, 128}, {64, 128}, {128, 128}, {16, 16}};
 
 // Operands the direct loads take: rows (or k lines) that start at 16-byte
 // boundaries, and offsets within a tile that fit the loads' 32 bits.
@@ -26,6 +26,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 int64_t tiles_of(int variant, int epi, const GemmArgs& a) {
   const Tile t = kTiles[variant];
+  if (variant == kRows) return rows_tiles(epi, a.n);
   const int64_t cols = epi == kEpiGated ? 2 * (int64_t)a.n : a.n;
   return ceil_div(a.m, t.m) * ceil_div(cols, t.n);
 }
@@ -44,6 +45,19 @@ size_t plan_gemm(int dtype, int epi, GemmArgs& a) {
                      operand_ok(a.b, brow ? a.sbn : a.sbk, brow, es, epi == kEpiGated ? a.n : 0);
   const int step = 128 / es;
   a.variant = !direct ? kStaged128 : tiles_of(kTile256, epi, a) >= 192 && es == 2 ? kTile256 : arow && a.m <= 64 ? kTile64 : kTile128;
+  if (epi != kEpiStore && a.m <= 16) {
+    a.variant = kRows;
+    // k over several blocks until there are two for every CU, each with
+    // two steps for each of its 8 waves or more
+    const int64_t tiles = rows_tiles(epi, a.n), turns = ceil_div(a.k, 8 * 256 / es);
+    int64_t splits = tiles >= 256 ? 1 : ceil_div(512, tiles);
+    if (splits > turns / 2) splits = turns / 2;
+    if (splits < 1 || tiles > kCounters) splits = 1;
+    const int64_t per = ceil_div(turns, splits) * (8 * 256 / es);
+    a.k_per_split = (int)(per < a.k ? per : a.k);
+    a.splits = a.k ? (int)ceil_div(a.k, per) : 1;
+    return a.splits > 1 ? (size_t)tiles * a.splits * a.m * 16 * 4 : 0;
+  }
   // parts of k: enough blocks to fill the GPU where the output has few tiles
   const int64_t tiles = tiles_of(a.variant, epi, a), steps = ceil_div(a.k, step);
   const int64_t want = a.variant == kTile256 ? 256 : 512;

@@ -2,6 +2,7 @@
 // operand layout.
 #pragma once
 
+#include "gemm_rows.h"
 #include "gemm_tile.h"
 
 namespace ringar {
@@ -20,6 +21,12 @@ template <typename T, bool AROW, bool BROW, int EPI> hipError_t launch_tiled(con
     case kTile256:
       if constexpr (sizeof(T) == 2) return go(gemm_tile<T, AROW, BROW, EPI, 256, 256, 2, 4, 2, true>, 256, 256, 512);
       return hipErrorInvalidValue;
+    case kRows:
+      if constexpr (EPI != kEpiStore) {
+        hipLaunchKernelGGL((gemm_rows<T, EPI, 8>), dim3((unsigned)(rows_tiles(EPI, a.n) * a.splits)), dim3(512), 0, st, a);
+        return hipGetLastError();
+      }
+      return hipErrorInvalidValue;
     case kTile64:
       if constexpr (AROW) return go(gemm_tile<T, AROW, BROW, EPI, 64, 128, 1, 2, 1, true>, 64, 128, 128);
       return hipErrorInvalidValue;
@@ -29,7 +36,7 @@ template <typename T, bool AROW, bool BROW, int EPI> hipError_t launch_tiled(con
 }
 
 template <typename T, int EPI> hipError_t join(const GemmArgs& a, hipStream_t st) {
-  if (a.splits == 1) return hipSuccess;
+  if (a.splits == 1 || a.variant == kRows) return hipSuccess;
   hipLaunchKernelGGL((gemm_join<T, EPI>), dim3((unsigned)(((int64_t)a.m * a.n + 255) / 256)), dim3(256), 0, st, a);
   return hipGetLastError();
 }
