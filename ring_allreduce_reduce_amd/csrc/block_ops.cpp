@@ -173,10 +173,15 @@ bool dims_ok(std::initializer_list<int64_t> d) {
 #define VEC(name, p, n, es, out) Mat{name, p, (p) ? 1 : 0, n, n, es, out}
 
 // --------------------------------------------------------------- products
-ringar_result_t run_gemm(int dtype, int epi, const GemmArgs& a, hipStream_t st) {
-  if (a.m == 0 || a.n == 0) return RINGAR_SUCCESS;
-  if (gemm_blocks(dtype, epi, a) > kMaxDim) return refuse(RINGAR_ERR_INVALID_USAGE, "the product has more tiles than one launch takes");
-  HIP_TRY(launch_gemm(dtype, epi, a, st));
+// `ws`: p.bytes at `at` in the stream's workspace (null where nothing of it
+// is needed).
+ringar_result_t run_gemm(int dtype, const GemmPlan& p, char* ws, size_t at, hipStream_t st) {
+  HIP_TRY(launch_gemm(dtype, p, ws ? ws + at : nullptr, ws ? (uint32_t*)(ws - kCounterBytes) : nullptr, st));
+  return RINGAR_SUCCESS;
+}
+
+ringar_result_t check_plan(const GemmPlan& p) {
+  if (gemm_blocks(p) > kMaxDim) return refuse(RINGAR_ERR_INVALID_USAGE, "the product has more tiles than one launch takes");
   return RINGAR_SUCCESS;
 }
 
@@ -327,13 +332,12 @@ static ringar_result_t product_forward(const ringar_linear_t* p, bool gated, hip
   a.ldr = p->ldr;
   a.ldp = p->ldp;
   a.act = p->act;
-  const size_t part = plan_gemm(p->dtype, epi, a);
+  const GemmPlan plan = plan_gemm(p->dtype, epi, a);
+  TRY(check_plan(plan));
   std::lock_guard<std::mutex> lock(g_ws_mu);
   char* ws = nullptr;
-  TRY(workspace(st, part, &ws));
-  a.part = (float*)ws;
-  if (ws) a.arrived = (uint32_t*)(ws - kCounterBytes);
-  return run_gemm(p->dtype, epi, a, st);
+  TRY(workspace(st, plan.bytes, &ws));
+  return run_gemm(p->dtype, plan, ws, 0, st);
 }
 
 static ringar_result_t product_backward(const ringar_linear_backward_t* p, bool gated, hipStream_t st) {
@@ -387,22 +391,24 @@ static ringar_result_t product_backward(const ringar_linear_backward_t* p, bool 
   // a workspace starts at a 256-byte boundary, like this stand-in for it
   gx.a = gw.a = need_dz ? (const void*)256 : p->dy;
   gx.sam = gw.sak = need_dz ? z.lddz : p->lddy;
+  GemmPlan px = {}, pw = {};
+  if (p->dx) px = plan_gemm(p->dtype, kEpiStore, gx);
+  if (p->dweight) pw = plan_gemm(p->dtype, kEpiStore, gw);
+  TRY(check_plan(px));
+  TRY(check_plan(pw));
   Layout l;
   const size_t at_dz = l.add(need_dz ? (size_t)p->rows * z.lddz * es : 0);
   const size_t at_sum = l.add(p->dbias ? (size_t)z.groups * wide * 4 : 0);
-  const size_t bx = p->dx ? plan_gemm(p->dtype, kEpiStore, gx) : 0, bw = p->dweight ? plan_gemm(p->dtype, kEpiStore, gw) : 0;
-  const size_t at_part = l.add(bx > bw ? bx : bw);
+  const size_t at_gemm = l.add(px.bytes > pw.bytes ? px.bytes : pw.bytes);
   std::lock_guard<std::mutex> lock(g_ws_mu);
   char* ws = nullptr;
   TRY(workspace(st, l.bytes, &ws));
-  gx.part = gw.part = (float*)(ws + at_part);
-  if (need_dz) z.dz = ws + at_dz;
+  if (need_dz) px.args.a = pw.args.a = z.dz = ws + at_dz;
   if (p->dbias) z.part = (float*)(ws + at_sum);
   if ((z.dz || z.part) && p->rows && p->out_features) HIP_TRY(launch_dz(p->dtype, z, st));
-  if (need_dz) gx.a = gw.a = z.dz;
   if (p->dbias && wide) HIP_TRY(launch_col_sum(p->dtype, {z.part, z.groups, wide, wide, p->dbias, nullptr}, st));
-  if (p->dx) TRY(run_gemm(p->dtype, kEpiStore, gx, st));
-  if (p->dweight) TRY(run_gemm(p->dtype, kEpiStore, gw, st));
+  if (p->dx) TRY(run_gemm(p->dtype, px, ws, at_gemm, st));
+  if (p->dweight) TRY(run_gemm(p->dtype, pw, ws, at_gemm, st));
   return RINGAR_SUCCESS;
 }
 

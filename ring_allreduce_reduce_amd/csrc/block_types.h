@@ -146,10 +146,10 @@ struct NormArgs {
 // projection's.
 enum : int { kEpiStore = 0, kEpiLinear = 1, kEpiGated = 2 };
 
-// kernels of a product: tiles of 256 x 256, 128 x 128, 64 x 128 with direct
-// loads, 128 x 128 with loads through registers (any alignment),
-// and the forward product of up to 16 rows
-enum : int { kTile256 = 0, kTile128 = 1, kTile64 = 2, kStaged128 = 3, kRows = 4 };
+// kernels of a product: tiles of 256 x 256, 128 x 128 and 64 x 64 (gated:
+// 64 x 128) with direct loads, 64 x 64 with loads through registers (any
+// alignment), and the forward product of up to 16 rows
+enum : int { kTile256 = 0, kTile128 = 1, kTile64 = 2, kStaged64 = 3, kRows = 4 };
 
 // kRows: blocks of columns
 inline int64_t rows_tiles(int epi, int64_t n) { return epi == kEpiGated ? (n + 7) / 8 : (n + 15) / 16; }
@@ -172,6 +172,24 @@ struct GemmArgs {
   void* pre;             // or null
   int64_t ldc, ldr, ldp;
   int act;
+};
+
+// A product as planned: its arguments, and the copies of operands whose rows
+// do not start at 16-byte boundaries that are made first, where the direct
+// loads win back what a copy costs.
+struct GemmPlan {
+  GemmArgs args;
+  int epi;
+  bool pack_a, pack_b;
+  int64_t packed_a, packed_b;   // the copies' row strides
+  size_t bytes;                 // workspace
+};
+struct PackArgs {
+  const void* from;
+  void* to;
+  int64_t ld_from, ld_to;
+  int64_t rows;
+  int cols;
 };
 
 // activation's backward pass and column sums
@@ -206,13 +224,15 @@ int norm_backward_groups(int64_t rows, int cols);
 hipError_t launch_col_sum(int out_dtype, const ColSumArgs& a, hipStream_t st);
 hipError_t launch_dz(int dtype, const DzArgs& a, hipStream_t st);
 int dz_groups(int64_t rows, int64_t cols);
-// Chooses the kernel and the split of k from sizes, strides and alignment
-// alone; returns the bytes of partial sums the launch needs.
-size_t plan_gemm(int dtype, int epi, GemmArgs& a);
 // Counters at the start of every workspace, zero between calls.
 constexpr int kCounters = 4096;
+// Chooses the kernel, the split of k and the copies from sizes, strides and
+// alignment alone.
+GemmPlan plan_gemm(int dtype, int epi, const GemmArgs& a);
 // Blocks of the planned launch.
-int64_t gemm_blocks(int dtype, int epi, const GemmArgs& a);
-hipError_t launch_gemm(int dtype, int epi, const GemmArgs& a, hipStream_t st);
+int64_t gemm_blocks(const GemmPlan& p);
+// `ws`: p.bytes of workspace; `counters`: kCounters zeros.
+hipError_t launch_gemm(int dtype, const GemmPlan& p, char* ws, uint32_t* counters, hipStream_t st);
+hipError_t launch_pack(int dtype, const PackArgs& a, hipStream_t st);
 
 }  // namespace ringar

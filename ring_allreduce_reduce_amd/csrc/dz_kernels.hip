@@ -88,6 +88,33 @@ template <typename T> hipError_t launch(const DzArgs& a, hipStream_t st) {
   return a.n < V ? launch<T, 1>(a, st) : launch<T, V>(a, st);
 }
 
+// A copy with rows padded to 128 bytes (zeros), for loads that need them to
+// start at 16-byte boundaries.
+template <typename T, int V> __global__ __launch_bounds__(256) void pack_rows(PackArgs a) {
+  const int64_t per_row = a.ld_to / V;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = i / per_row;
+  if (row >= a.rows) return;
+  const int64_t c = i % per_row * V;
+  const T* from = (const T*)a.from + row * a.ld_from + c;
+  Pack<T, V> v;
+  if (c + V <= a.cols) {
+    v = load_pack<T, V>(from);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j++) v.v[j] = c + j < a.cols ? from[j] : (T)0.0f;
+  }
+  store_pack<T, V>((T*)a.to + row * a.ld_to + c, v);
+}
+
+template <typename T> hipError_t pack(const PackArgs& a, hipStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  const int64_t blocks = (a.rows * (a.ld_to / V) + 255) / 256;
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  if (blocks) hipLaunchKernelGGL((pack_rows<T, V>), dim3((unsigned)blocks), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 // Row groups: enough blocks to fill the GPU (about 2048 with the column
@@ -98,6 +125,12 @@ int dz_groups(int64_t rows, int64_t n) {
   const int64_t most = (rows + 3) / 4;
   if (g > most) g = most;
   return (int)(g < 1 ? 1 : g);
+}
+
+hipError_t launch_pack(int dtype, const PackArgs& a, hipStream_t st) {
+  if (dtype == kF32) return pack<float>(a, st);
+  if (dtype == kF16) return pack<_Float16>(a, st);
+  return pack<__bf16>(a, st);
 }
 
 hipError_t launch_dz(int dtype, const DzArgs& a, hipStream_t st) {

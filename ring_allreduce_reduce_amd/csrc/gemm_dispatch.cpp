@@ -9,10 +9,7 @@ hipError_t launch_gemm_f32(int epi, const GemmArgs& a, hipStream_t st);
 
 namespace {
 
-struct Tile {
-  int m, n;
-};
-constexpr Tile kTiles[] = {{256, 256}, {128, 128}, {64, 128}, {128, 128}, {16, 16}};
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Operands the direct loads take: rows (or k lines) that start at 16-byte
 // boundaries, and offsets within a tile that fit the loads' 32 bits.
@@ -22,63 +19,167 @@ bool operand_ok(const void* p, int64_t pitch, bool rows, int es, int64_t extra_r
   return ((rows ? 256 : 64) + extra_rows) * bytes < (1ll << 32) - 4096;
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+struct Tile {
+  int m, n;
+};
+Tile tile_of(int variant, int epi) {
+  switch (variant) {
+    case kTile256: return {256, 256};
+    case kTile128: return {128, 128};
+    default: return {64, epi == kEpiGated ? 128 : 64};
+  }
+}
 
 int64_t tiles_of(int variant, int epi, const GemmArgs& a) {
-  const Tile t = kTiles[variant];
   if (variant == kRows) return rows_tiles(epi, a.n);
-  const int64_t cols = epi == kEpiGated ? 2 * (int64_t)a.n : a.n;
-  return ceil_div(a.m, t.m) * ceil_div(cols, t.n);
+  const Tile t = tile_of(variant, epi);
+  return ceil_div(a.m, t.m) * ceil_div(epi == kEpiGated ? 2 * (int64_t)a.n : a.n, t.n);
+}
+
+// Microseconds of a tiled launch: a start, and for every step of 128 bytes of
+// k (and one and a half more, to fill the buffers and to finish) either a lone
+// block's latency or the CU's throughput, whichever is more.
+// Measured on MI355X over 32 .. 2500 rows, widths of 1024 .. 4096 and splits
+// of 1 .. 16 (bf16 and fp32, the fastest choice of this table within 10% of
+// the fastest measured): a 64 x 64 tile wins until its blocks are about four
+// to a CU (512 x 4096 x 4096 bf16: 26 us, 128 x 128 34 us), 256 x 256 from
+// about 200 tiles on (8192 x 8192 x 8192: 0.87 ms).
+struct Cost {
+  double start, alone, shared;
+};
+Cost cost_of(int variant, int epi, int es, bool arow, bool brow) {
+  if (es == 4) {
+    if (variant == kTile128) return {1, 1.95, 1.95};
+    if (variant == kTile64) return epi == kEpiGated ? Cost{2, 1.06, 1.0} : Cost{2, 0.6, 0.51};
+    return epi == kEpiGated ? Cost{2, 1.4, 1.3} : Cost{2, 0.8, 0.7};
+  }
+  switch (variant) {
+    case kTile256: return {6, 1.43, 1.43};
+    case kTile128: return {2.6, 0.6, 0.55};
+    case kTile64: return epi == kEpiGated ? Cost{2.6, 0.31, 0.29} : arow ? Cost{2.6, 0.24, 0.18} : Cost{2.6, 0.25, 0.23};
+    default: return epi == kEpiGated ? Cost{2, 0.7, 0.5} : brow ? Cost{2, 0.5, 0.3} : Cost{2, 0.7, 0.5};
+  }
+}
+
+struct Choice {
+  int variant, splits;
+  double us;
+};
+
+// The cheapest split of one kernel: parts of k fill the GPU where the output
+// has few tiles, and cost a pass over the parts.
+Choice cheapest(int variant, int epi, int es, const GemmArgs& a) {
+  const Cost c = cost_of(variant, epi, es, a.sak == 1, a.sbk == 1);
+  const int64_t tiles = tiles_of(variant, epi, a), steps = ceil_div(a.k, 128 / es);
+  const double outputs = (double)a.m * a.n * (epi == kEpiGated ? 2 : 1);
+  Choice best = {variant, 1, 0};
+  for (int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
+    if (s > 1 && steps < 2 * s) break;
+    const int64_t per = ceil_div(steps, s);
+    const double at_once = c.shared * (double)ceil_div(tiles * s, 256);
+    const double us = c.start + (per + 1.5) * (at_once > c.alone ? at_once : c.alone) + (s > 1 ? 4.5 + outputs * s * 8 / 8e6 : 0);
+    if (s == 1 || us < best.us) best = {variant, s, us};
+  }
+  return best;
 }
 
 }  // namespace
 
-size_t plan_gemm(int dtype, int epi, GemmArgs& a) {
+GemmPlan plan_gemm(int dtype, int epi, const GemmArgs& given) {
+  GemmPlan p = {};
+  p.epi = epi;
+  p.args = given;
+  GemmArgs& a = p.args;
   a.splits = 1;
   a.k_per_split = a.k;
-  a.variant = kStaged128;
-  if (a.m == 0 || a.n == 0) return 0;
+  a.variant = kStaged64;
+  if (a.m == 0 || a.n == 0) return p;
   const int es = dtype == kF32 ? 4 : 2;
-  const bool arow = a.sak == 1, brow = a.sbk == 1;
   const int64_t wide = epi == kEpiGated ? 2 * (int64_t)a.n : a.n;
-  const bool direct = operand_ok(a.a, arow ? a.sam : a.sak, arow, es, 0) &&
-                     operand_ok(a.b, brow ? a.sbn : a.sbk, brow, es, epi == kEpiGated ? a.n : 0);
-  const int step = 128 / es;
-  a.variant = !direct ? kStaged128 : tiles_of(kTile256, epi, a) >= 192 && es == 2 ? kTile256 : arow && a.m <= 64 ? kTile64 : kTile128;
-  if (epi != kEpiStore && a.m <= 16) {
+  // Up to 16 rows; where the weight is large the tiles, which read the rows
+  // once for 128 columns, win from 9 on (16 x 4096 x 20480 bf16: 36 us, not
+  // 43; 16 x 4096 x 4096: 16 us, not 10).
+  if (epi != kEpiStore && a.m <= (wide >= 16384 ? 8 : 16)) {
     a.variant = kRows;
     // k over several blocks until there are two for every CU, each with
     // two steps for each of its 8 waves or more
-    const int64_t tiles = rows_tiles(epi, a.n), turns = ceil_div(a.k, 8 * 256 / es);
+    const int64_t turn = 8 * 256 / es, tiles = rows_tiles(epi, a.n), turns = ceil_div(a.k, turn);
     int64_t splits = tiles >= 256 ? 1 : ceil_div(512, tiles);
     if (splits > turns / 2) splits = turns / 2;
     if (splits < 1 || tiles > kCounters) splits = 1;
-    const int64_t per = ceil_div(turns, splits) * (8 * 256 / es);
+    const int64_t per = ceil_div(turns, splits) * turn;
     a.k_per_split = (int)(per < a.k ? per : a.k);
     a.splits = a.k ? (int)ceil_div(a.k, per) : 1;
-    return a.splits > 1 ? (size_t)tiles * a.splits * a.m * 16 * 4 : 0;
+    p.bytes = a.splits > 1 ? (size_t)tiles * a.splits * a.m * 16 * 4 : 0;
+    return p;
   }
-  // parts of k: enough blocks to fill the GPU where the output has few tiles
-  const int64_t tiles = tiles_of(a.variant, epi, a), steps = ceil_div(a.k, step);
-  const int64_t want = a.variant == kTile256 ? 256 : 512;
-  int64_t splits = tiles >= want / 2 || steps < 8 ? 1 : ceil_div(want, tiles);
-  if (splits > steps / 4) splits = steps / 4;
-  if (splits < 1) splits = 1;
-  const int64_t per = ceil_div(steps, splits);
+  const bool arow = a.sak == 1, brow = a.sbk == 1;
+  const bool ok_a = operand_ok(a.a, arow ? a.sam : a.sak, arow, es, 0);
+  const bool ok_b = operand_ok(a.b, brow ? a.sbn : a.sbk, brow, es, epi == kEpiGated ? a.n : 0);
+  // the operands as stored, and copies with padded rows
+  const int64_t rows_a = arow ? a.m : a.k, cols_a = arow ? a.k : a.m, rows_b = brow ? wide : a.k, cols_b = brow ? a.k : wide;
+  const int64_t pad = 128 / es;
+  p.packed_a = ceil_div(cols_a, pad) * pad;
+  p.packed_b = ceil_div(cols_b, pad) * pad;
+  auto copy_us = [&](int64_t rows, int64_t pitch) { return 3 + (double)rows * pitch * es * 2 / 4.5e6; };
+  Choice best = cheapest(kTile64, epi, es, a);
+  for (int v : {kTile128, kTile256}) {
+    if (v == kTile256 && es == 4) continue;
+    const Choice c = cheapest(v, epi, es, a);
+    if (c.us < best.us) best = c;
+  }
+  if (!ok_a || !ok_b) {
+    const double copies = (ok_a ? 0 : copy_us(rows_a, p.packed_a)) + (ok_b ? 0 : copy_us(rows_b, p.packed_b));
+    const bool fits = ((arow ? 256 : 64) * p.packed_a + 64) * es < (1ll << 32) - 4096 &&
+                      ((brow ? 256 + (epi == kEpiGated ? a.n : 0) : 64) * p.packed_b + 64) * es < (1ll << 32) - 4096;
+    const Choice staged = cheapest(kStaged64, epi, es, a);
+    if (fits && best.us + copies < staged.us) {
+      p.pack_a = !ok_a;
+      p.pack_b = !ok_b;
+    } else {
+      best = staged;
+    }
+  }
+  a.variant = best.variant;
+  const int64_t step = 128 / es, steps = ceil_div(a.k, step), per = ceil_div(steps, best.splits);
   a.k_per_split = (int)(per * step < a.k ? per * step : a.k);
   a.splits = (int)(steps ? ceil_div(steps, per) : 1);
-  return a.splits > 1 ? (size_t)a.splits * a.m * wide * 4 : 0;
+  auto part = [&](size_t n) { p.bytes += (n + 255) / 256 * 256; };
+  if (a.splits > 1) part((size_t)a.splits * a.m * wide * 4);
+  if (p.pack_a) part((size_t)rows_a * p.packed_a * es);
+  if (p.pack_b) part((size_t)rows_b * p.packed_b * es);
+  return p;
 }
 
-int64_t gemm_blocks(int dtype, int epi, const GemmArgs& a) {
-  (void)dtype;
-  return tiles_of(a.variant, epi, a) * a.splits;
-}
+int64_t gemm_blocks(const GemmPlan& p) { return p.args.m && p.args.n ? tiles_of(p.args.variant, p.epi, p.args) * p.args.splits : 0; }
 
-hipError_t launch_gemm(int dtype, int epi, const GemmArgs& a, hipStream_t st) {
-  if (dtype == kF16) return launch_gemm_f16(epi, a, st);
-  if (dtype == kBF16) return launch_gemm_bf16(epi, a, st);
-  return launch_gemm_f32(epi, a, st);
+hipError_t launch_gemm(int dtype, const GemmPlan& p, char* ws, uint32_t* counters, hipStream_t st) {
+  GemmArgs a = p.args;
+  if (a.m == 0 || a.n == 0) return hipSuccess;
+  const int es = dtype == kF32 ? 4 : 2;
+  const int64_t wide = p.epi == kEpiGated ? 2 * (int64_t)a.n : a.n;
+  auto part = [&](size_t n) {
+    char* at = ws;
+    ws += (n + 255) / 256 * 256;
+    return at;
+  };
+  a.part = (float*)ws;
+  a.arrived = counters;
+  if (a.variant != kRows && a.splits > 1) a.part = (float*)part((size_t)a.splits * a.m * wide * 4);
+  auto pack = [&](const void** from, int64_t* pitch, int64_t packed, int64_t rows, int64_t cols) {
+    void* to = part((size_t)rows * packed * es);
+    const hipError_t e = launch_pack(dtype, {*from, to, *pitch, packed, rows, (int)cols}, st);
+    *from = to;
+    *pitch = packed;
+    return e;
+  };
+  hipError_t e = hipSuccess;
+  if (p.pack_a) e = a.sak == 1 ? pack(&a.a, &a.sam, p.packed_a, a.m, a.k) : pack(&a.a, &a.sak, p.packed_a, a.k, a.m);
+  if (e == hipSuccess && p.pack_b) e = a.sbk == 1 ? pack(&a.b, &a.sbn, p.packed_b, wide, a.k) : pack(&a.b, &a.sbk, p.packed_b, a.k, wide);
+  if (e != hipSuccess) return e;
+  if (dtype == kF16) return launch_gemm_f16(p.epi, a, st);
+  if (dtype == kBF16) return launch_gemm_bf16(p.epi, a, st);
+  return launch_gemm_f32(p.epi, a, st);
 }
 
 }  // namespace ringar

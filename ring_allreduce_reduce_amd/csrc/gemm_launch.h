@@ -27,11 +27,13 @@ template <typename T, bool AROW, bool BROW, int EPI> hipError_t launch_tiled(con
         return hipGetLastError();
       }
       return hipErrorInvalidValue;
+    case kTile128: return go(gemm_tile<T, AROW, BROW, EPI, 128, 128, 4, 2, 4, true>, 128, 128, 512);
     case kTile64:
-      if constexpr (AROW) return go(gemm_tile<T, AROW, BROW, EPI, 64, 128, 1, 2, 1, true>, 64, 128, 128);
-      return hipErrorInvalidValue;
-    case kTile128: return go(gemm_tile<T, AROW, BROW, EPI, 128, 128, 2, 2, 2, true>, 128, 128, 256);
-    default: return go(gemm_tile<T, AROW, BROW, EPI, 128, 128, 2, 2, 2, false>, 128, 128, 256);
+      if constexpr (EPI == kEpiGated) return go(gemm_tile<T, AROW, BROW, EPI, 64, 128, 2, 2, 2, true, 3>, 64, 128, 256);
+      else return go(gemm_tile<T, AROW, BROW, EPI, 64, 64, 2, 2, 2, true, 3>, 64, 64, 256);
+    default:
+      if constexpr (EPI == kEpiGated) return go(gemm_tile<T, AROW, BROW, EPI, 64, 128, 2, 2, 2, false>, 64, 128, 256);
+      else return go(gemm_tile<T, AROW, BROW, EPI, 64, 64, 2, 2, 2, false>, 64, 64, 256);
   }
 }
 

@@ -39,11 +39,17 @@ template <typename T, bool ROW, int R, int NW> struct Operand {
   static constexpr int kLoads = kBytes / 1024 / NW;       // load instructions of a wave and step
   static constexpr int kChunks = R * sizeof(T) / 16;      // COL: chunks of a line
   static_assert(kLoads * 1024 * NW == kBytes, "every wave loads the same share");
-  static_assert(ROW || kChunks >= 16, "COL lines hold at least 16 chunks");
+  static_assert(ROW || kChunks >= (sizeof(T) == 4 ? 16 : 8), "COL lines hold the swizzle's chunks");
 
-  // COL: the four k lines that a transposing read (16-bit) or the four lane
-  // groups (fp32) touch together start 64 bytes apart in the banks.
-  static __device__ inline int col_swizzle(int k) { return (sizeof(T) == 2 ? k & 3 : (k >> 2) & 3) << 2; }
+  // COL: the k lines that the lanes of one LDS cycle read (32 lanes of the
+  // transposing read: lines k .. k + 3 and k + 8 .. k + 11; all four lane
+  // groups of fp32) lie in different 32 (64) bytes of the 256 that the banks
+  // span.  A line of 8 chunks spans half of them, odd lines the other half.
+  static __device__ inline int col_swizzle(int k) {
+    if constexpr (sizeof(T) == 4) return ((k >> 2) & 3) << 2;
+    if constexpr (kChunks == 8) return ((k >> 1) & 1) << 2 | ((k >> 3) & 1) << 1;
+    return (k & 3) << 2 | ((k >> 3) & 1) << 1;
+  }
 
   const char* base;        // of the current step, uniform
   int64_t left;            // bytes from there to the operand's end
@@ -74,23 +80,25 @@ template <typename T, bool ROW, int R, int NW> struct Operand {
     }
   }
 
-  // Starts the loads of one step into `lds` and moves on.  Reads past the
-  // operand's end are stopped by the descriptor's size.  The loads are asm
+  // next_step() moves on to a step, load(i) starts its i-th load into `lds`.
+  // Reads past the operand's end are stopped by the descriptor's size.  The
+  // loads are asm
   // because the compiler would wait for them before every transposing LDS
   // read that follows, which is what the second buffer is there to avoid;
   // they have no register result, and wait_loads() waits for all of them
   // before a barrier lets any wave read what they bring.
-  __device__ inline void load(char* lds, int wave) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  u32x4 desc;
+  __device__ inline void next_step() {
     const uint32_t size = left <= 0 ? 0u : left > 0xffffffffll ? 0xffffffffu : (uint32_t)left;
-    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    const u32x4 desc = {(uint32_t)(uintptr_t)base, (uint32_t)((uintptr_t)base >> 32), size, 0x00027000u};
-    const uint32_t to = (uint32_t)(uintptr_t)(RINGAR_LDS void*)lds + wave * 1024;
-#pragma unroll
-    for (int i = 0; i < kLoads; i++)
-      asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                   :: "s"(to + i * NW * 1024), "v"(off[i]), "s"(desc) : "memory");
+    desc = u32x4{(uint32_t)(uintptr_t)base, (uint32_t)((uintptr_t)base >> 32), size, 0x00027000u};
     base += step;
     left -= step;
+  }
+  __device__ inline void load(int i, char* lds, int wave) {
+    const uint32_t to = (uint32_t)(uintptr_t)(RINGAR_LDS void*)lds + (i * NW + wave) * 1024;
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :: "s"(to), "v"(off[i]), "s"(desc) : "memory");
   }
 
   // Zeros every value of a step from k = `valid` on.
@@ -149,9 +157,9 @@ template <typename T, bool ROW, int R, int NW> struct Operand {
 template <typename T, bool ROW, int R, int NW> struct StagedOperand : Operand<T, ROW, R, NW> {
   using Base = Operand<T, ROW, R, NW>;
   static constexpr int kVec = Base::kVec, kLoads = Base::kLoads, kChunks = Base::kChunks;
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  using typename Base::u32x4;
   const T* from[kLoads];
-  int at[kLoads];          // ROW: first k of the chunk; COL: k line
+  int at[kLoads];          // within the step: ROW: first k of the chunk; COL: k line
   int columns[kLoads];     // COL: columns left from the chunk's first
   u32x4 data[kLoads];
   int64_t step_elems;
@@ -160,17 +168,19 @@ template <typename T, bool ROW, int R, int NW> struct StagedOperand : Operand<T,
   template <typename F>
   __device__ inline void offsets(const T* p, int64_t pitch, int k_begin, int k_stop, int64_t cols_left, int wave, int lane, F row_offset) {
     k_end = k_stop;
+    k_now = k_begin;
+    all_columns = cols_left >= R;
     step_elems = ROW ? Base::kBK : Base::kBK * pitch;
 #pragma unroll
     for (int i = 0; i < kLoads; i++) {
       const int idx = i * NW + wave;
       if constexpr (ROW) {
         const int r = idx * 8 + (lane >> 3), c = (lane & 7) ^ (r & 7);
-        at[i] = k_begin + c * kVec;
+        at[i] = c * kVec;
         from[i] = p + row_offset(r) + c * kVec;
       } else {
         const int k = idx * (64 / kChunks) + lane / kChunks, q = (lane % kChunks) ^ Base::col_swizzle(k);
-        at[i] = k_begin + k;
+        at[i] = k;
         from[i] = p + k * pitch + q * kVec;
         const int64_t left = cols_left - q * kVec;
         columns[i] = (int)(left < 0 ? 0 : left > kVec ? kVec : left);
@@ -178,13 +188,18 @@ template <typename T, bool ROW, int R, int NW> struct StagedOperand : Operand<T,
     }
   }
 
-  __device__ inline void load() {
+  // The loads of the next step; `inside`: no chunk of the tile passes an edge
+  // (then none branches, and all are in flight together).
+  int k_now;               // first k of the step
+  bool all_columns;        // COL: the tile's columns all exist
+  __device__ inline void load_step() {
+    if (k_now + Base::kBK <= k_end && (ROW || all_columns)) {
 #pragma unroll
-    for (int i = 0; i < kLoads; i++) {
-      const int n = ROW ? k_end - at[i] : at[i] < k_end ? columns[i] : 0;
-      if (n >= kVec) {
-        __builtin_memcpy(&data[i], from[i], 16);
-      } else {
+      for (int i = 0; i < kLoads; i++) __builtin_memcpy(&data[i], from[i], 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; i++) {
+        const int n = ROW ? k_end - at[i] - k_now : at[i] + k_now < k_end ? columns[i] : 0;
         u32x4 v = {0, 0, 0, 0};
         const T* p = from[i];
 #pragma unroll
@@ -195,9 +210,10 @@ template <typename T, bool ROW, int R, int NW> struct StagedOperand : Operand<T,
           }
         data[i] = v;
       }
-      from[i] += step_elems;
-      at[i] += Base::kBK;
     }
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) from[i] += step_elems;
+    k_now += Base::kBK;
   }
 
   __device__ inline void commit(char* lds, int wave, int lane) {
@@ -259,12 +275,13 @@ template <typename T> __device__ inline void finish8_gated(const GemmArgs& a, in
   put8<T>(a.c, m * a.ldc + n, g);
 }
 
-__device__ inline void wait_loads() {
-  // vmcnt(0): this wave's loads into LDS have landed; lgkmcnt(0): its
-  // fragment reads are done.  The empty asm keeps the compiler from moving
-  // memory accesses over the wait.
+// Waits until all but the wave's last N loads into LDS have landed, and all
+// its fragment reads are done.  The empty asm keeps the compiler from moving
+// memory accesses over the wait.
+template <int N = 0> __device__ inline void wait_loads() {
+  static_assert(N < 64, "the counter has six bits");
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070);
+  __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | (N >> 4 << 14));
 }
 __device__ inline void barrier() {
   asm volatile("" ::: "memory");
@@ -272,19 +289,19 @@ __device__ inline void barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <typename T, bool AROW, bool BROW, int EPI, int BM, int BN, int WM, int WN, int OCC, bool DIRECT>
+template <typename T, bool AROW, bool BROW, int EPI, int BM, int BN, int WM, int WN, int OCC, bool DIRECT, int STAGES = 2>
 __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_tile(GemmArgs a) {
   constexpr int NW = WM * WN;
   using OA = std::conditional_t<DIRECT, Operand<T, AROW, BM, NW>, StagedOperand<T, AROW, BM, NW>>;
   using OB = std::conditional_t<DIRECT, Operand<T, BROW, BN, NW>, StagedOperand<T, BROW, BN, NW>>;
   constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr int kBK = OA::kBK;
-  static_assert(TN == 64, "eight lanes finish a wave's row");
+  static_assert(TN == 64 || (TN == 32 && EPI != kEpiGated), "eight or four lanes finish a wave's row");
   static_assert(BROW || EPI == kEpiStore, "epilogues with columns of their own read weights by rows");
   constexpr int kStage = OA::kBytes + OB::kBytes;
   // epilogue: a wave's rows in fp32, shifted 16 bytes over the banks
   constexpr int kPass = TM < 32 ? TM : 32, kRowF = TN + 4;
-  constexpr int kShared = 2 * kStage > NW * kPass * kRowF * 4 ? 2 * kStage : NW * kPass * kRowF * 4;
+  constexpr int kShared = STAGES * kStage > NW * kPass * kRowF * 4 ? STAGES * kStage : NW * kPass * kRowF * 4;
   __shared__ __attribute__((aligned(1024))) char smem[kShared];
   using Frag = typename Mma<T>::Frag;
 
@@ -346,15 +363,25 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_tile(GemmArgs a) {
 #pragma unroll
     for (int j = 0; j < FM; j++) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // DIRECT: starts the loads of the next step into buffer `buf`.  Otherwise
-  // they go to registers here and to LDS in commit().
+  // Load l of the next step into buffer `buf`.  (Not DIRECT: issue() loads to
+  // registers, from which commit() writes to the buffer.)
+  constexpr int kStepLoads = DIRECT ? OA::kLoads + OB::kLoads : 0;
+  auto load = [&](int l, int buf) {
+    if constexpr (DIRECT) {
+      char* lds = smem + buf * kStage;
+      if (l < OA::kLoads) oa.load(l, lds, wave);
+      else ob.load(l - OA::kLoads, lds + OA::kBytes, wave);
+    }
+  };
   auto issue = [&](int buf) {
     if constexpr (DIRECT) {
-      oa.load(smem + buf * kStage, wave);
-      ob.load(smem + buf * kStage + OA::kBytes, wave);
+      oa.next_step();
+      ob.next_step();
+#pragma unroll
+      for (int l = 0; l < kStepLoads; l++) load(l, buf);
     } else {
-      oa.load();
-      ob.load();
+      oa.load_step();
+      ob.load_step();
     }
   };
   auto commit = [&](int buf) {
@@ -365,56 +392,103 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_tile(GemmArgs a) {
   };
   auto fix_tail = [&](int s) {        // the last step, where k ends inside it
     if (DIRECT && s == steps - 1 && k_len % kBK != 0) {
-      OA::clear_tail(smem + (s & 1) * kStage, k_len % kBK);
-      OB::clear_tail(smem + (s & 1) * kStage + OA::kBytes, k_len % kBK);
-      wait_loads();
+      OA::clear_tail(smem + s % STAGES * kStage, k_len % kBK);
+      OB::clear_tail(smem + s % STAGES * kStage + OA::kBytes, k_len % kBK);
+      wait_loads<>();
       barrier();
     }
   };
-  auto read = [&](int buf, int h, Frag* fa, Frag* fb) {
+  // Fragment r of half h: B's first.
+  auto read = [&](int r, int buf, int h, Frag* fa, Frag* fb) {
     const char* pa = smem + buf * kStage;
-    const char* pb = pa + OA::kBytes;
+    if (r < FN) fb[r] = OB::read(pa + OA::kBytes, wn + r * 16, h, lane);
+    else fa[r - FN] = OA::read(pa, wm + (r - FN) * 16, h, lane);
+  };
+  // The matrix instructions of one half, and between them, evenly, the reads
+  // of the next half's fragments (buffer `from`) and, LOADS, the loads of a
+  // step to come (buffer `to`).  A wave issues in order: a burst of loads
+  // would hold its matrix instructions back until the last is accepted.
+  auto half = [&](auto loads, const Frag* fa, const Frag* fb, int from, int h, Frag* na, Frag* nb, int to) {
+    constexpr int kMma = FN * FM, kReads = FN + FM;
+    if constexpr (loads.value) {
+      oa.next_step();
+      ob.next_step();
+    }
 #pragma unroll
-    for (int i = 0; i < FN; i++) fb[i] = OB::read(pb, wn + i * 16, h, lane);
+    for (int t = 0; t < kMma; t++) {
+      // reads in the first three quarters, so that they are back at the end
 #pragma unroll
-    for (int i = 0; i < FM; i++) fa[i] = OA::read(pa, wm + i * 16, h, lane);
+      for (int r = 0; r < kReads; r++)
+        if (r * kMma * 3 / (kReads * 4) == t) read(r, from, h, na, nb);
+      if constexpr (loads.value) {
+#pragma unroll
+        for (int l = 0; l < kStepLoads; l++)
+          if (l * kMma / kStepLoads == t) load(l, to);
+      }
+      acc[t / FM][t % FM] = Mma<T>::run(fb[t / FM], fa[t % FM], acc[t / FM][t % FM]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
   auto mma = [&](const Frag* fa, const Frag* fb) {
 #pragma unroll
-    for (int i = 0; i < FN; i++)
-#pragma unroll
-      for (int j = 0; j < FM; j++) acc[i][j] = Mma<T>::run(fb[i], fa[j], acc[i][j]);
+    for (int t = 0; t < FN * FM; t++) acc[t / FM][t % FM] = Mma<T>::run(fb[t / FM], fa[t % FM], acc[t / FM][t % FM]);
   };
 
   if (steps > 0) {
+    static_assert(STAGES == 2 || (STAGES == 3 && DIRECT), "registers hold one step");
+    constexpr std::false_type kNoLoads;
+    constexpr std::true_type kLoads;
     Frag fa0[FM], fb0[FN], fa1[FM], fb1[FN];
+    // STAGES - 1 steps are on their way before the first is used
     issue(0);
     commit(0);
-    wait_loads();
+    if (STAGES == 3 && steps > 1) {
+      issue(1);
+      wait_loads<STAGES == 3 ? kStepLoads : 0>();
+    } else {
+      wait_loads<>();
+    }
     barrier();
     fix_tail(0);
-    if (steps > 1) issue(1);
-    read(0, 0, fa0, fb0);
-    for (int s = 0; s < steps - 1; s++) {
-      read(s & 1, 1, fa1, fb1);
-      mma(fa0, fb0);
-      commit((s + 1) & 1);      // its readers of step s - 1 passed the last barrier
-      wait_loads();
+    if (STAGES - 1 < steps) issue(STAGES - 1);
+#pragma unroll
+    for (int r = 0; r < FN + FM; r++) read(r, 0, 0, fa0, fb0);
+    int now = 0, next = 1;            // buffers of steps s and s + 1
+    auto first_half = [&](int s) {
+      half(kNoLoads, fa0, fb0, now, 1, fa1, fb1, 0);
+      commit(next);                   // its readers of step s - 1 passed the last barrier
+      // step s + 1 has landed; with three buffers step s + 2 may still be on its way
+      if (STAGES == 3 && s + 2 < steps) wait_loads<STAGES == 3 ? kStepLoads : 0>();
+      else wait_loads<>();
       barrier();
-      fix_tail(s + 1);
-      if (s + 2 < steps) issue(s & 1);
-      read((s + 1) & 1, 0, fa0, fb0);
-      mma(fa1, fb1);
+    };
+    int s = 0;
+    for (; s < steps - STAGES; s++) {
+      first_half(s);
+      if constexpr (DIRECT) {
+        half(kLoads, fa1, fb1, next, 0, fa0, fb0, now);
+      } else {
+        issue(now);
+        half(kNoLoads, fa1, fb1, next, 0, fa0, fb0, 0);
+      }
+      now = next;
+      next = next + 1 == STAGES ? 0 : next + 1;
     }
-    read((steps - 1) & 1, 1, fa1, fb1);
-    mma(fa0, fb0);
+    for (; s < steps - 1; s++) {
+      first_half(s);
+      fix_tail(s + 1);
+      half(kNoLoads, fa1, fb1, next, 0, fa0, fb0, 0);
+      now = next;
+      next = next + 1 == STAGES ? 0 : next + 1;
+    }
+    half(kNoLoads, fa0, fb0, now, 1, fa1, fb1, 0);
     mma(fa1, fb1);
   }
 
-  wait_loads();
+  wait_loads<>();
   barrier();                                   // every wave is done with the operands
   float* rows = (float*)smem + wave * kPass * kRowF;
-  constexpr int kLanes = EPI == kEpiGated ? 4 : 8;   // lanes of a row, eight columns each
+  constexpr int kLanes = (EPI == kEpiGated ? TN / 2 : TN) / 8;   // lanes of a row, eight columns each
   const int64_t part_cols = EPI == kEpiGated ? 2 * (int64_t)a.n : a.n;
 #pragma unroll
   for (int p = 0; p < TM / kPass; p++) {
