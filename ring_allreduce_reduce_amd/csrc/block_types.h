@@ -36,6 +36,18 @@ template <typename T, int N> __device__ inline void store_pack(T* p, const Pack<
   __builtin_memcpy(p, &v, sizeof(v));
 }
 
+// 16 bytes that are not wanted back soon: past the caches' keeping.
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+template <typename T, int N> __device__ inline void stream_pack(T* p, const Pack<T, N>& v) {
+  static_assert(sizeof(v) % 16 == 0, "whole 16-byte stores");
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(v) / 16; i++) {
+    f32x4 q;
+    __builtin_memcpy(&q, (const char*)&v + 16 * i, 16);
+    __builtin_nontemporal_store((f32x4_any)q, (f32x4_any*)p + i);
+  }
+}
+
 // exp and 1/x of the activations: the 16-bit types take the hardware's
 // exponential and reciprocal (relative error about 1e-6 against the 2e-3 of
 // their own rounding), fp32 the full-precision ones.
@@ -138,6 +150,7 @@ struct NormArgs {
   int groups;            // blocks of the backward grid
   float eps;
   float inv_cols;
+  bool stream;           // y goes past the caches
 };
 
 // ------------------------------------------------- products and their epilogue

@@ -229,11 +229,12 @@ template <typename T> __device__ inline void add8(const void* p, int64_t at, flo
   for (int i = 0; i < 8; i++) z[i] += (float)b.v[i];
 }
 
-template <typename T> __device__ inline void put8(void* p, int64_t at, const float* z) {
+template <typename T, bool STREAM = false> __device__ inline void put8(void* p, int64_t at, const float* z) {
   Pack<T, 8> o;
 #pragma unroll
   for (int i = 0; i < 8; i++) o.v[i] = (T)z[i];
-  store_pack<T, 8>((T*)p + at, o);
+  if constexpr (STREAM) stream_pack<T, 8>((T*)p + at, o);
+  else store_pack<T, 8>((T*)p + at, o);
 }
 
 template <bool FAST> __device__ inline void activate8(int act, float* z) {
@@ -252,27 +253,27 @@ template <bool FAST> __device__ inline void activate8(int act, float* z) {
   }
 }
 
-template <typename T> __device__ inline void finish8_linear(const GemmArgs& a, int64_t m, int64_t n, float* z) {
+template <typename T, bool STREAM> __device__ inline void finish8_linear(const GemmArgs& a, int64_t m, int64_t n, float* z) {
   if (a.bias) add8<T>(a.bias, n, z);
-  if (a.pre) put8<T>(a.pre, m * a.ldp + n, z);
+  if (a.pre) put8<T, STREAM>(a.pre, m * a.ldp + n, z);
   activate8<sizeof(T) == 2>(a.act, z);
   if (a.residual) add8<T>(a.residual, m * a.ldr + n, z);
-  put8<T>(a.c, m * a.ldc + n, z);
+  put8<T, STREAM>(a.c, m * a.ldc + n, z);
 }
 
-template <typename T> __device__ inline void finish8_gated(const GemmArgs& a, int64_t m, int64_t n, float* g, float* u) {
+template <typename T, bool STREAM> __device__ inline void finish8_gated(const GemmArgs& a, int64_t m, int64_t n, float* g, float* u) {
   if (a.bias) {
     add8<T>(a.bias, n, g);
     add8<T>(a.bias, a.n + n, u);
   }
   if (a.pre) {
-    put8<T>(a.pre, m * a.ldp + n, g);
-    put8<T>(a.pre, m * a.ldp + a.n + n, u);
+    put8<T, STREAM>(a.pre, m * a.ldp + n, g);
+    put8<T, STREAM>(a.pre, m * a.ldp + a.n + n, u);
   }
   activate8<sizeof(T) == 2>(a.act, g);
 #pragma unroll
   for (int i = 0; i < 8; i++) g[i] *= u[i];
-  put8<T>(a.c, m * a.ldc + n, g);
+  put8<T, STREAM>(a.c, m * a.ldc + n, g);
 }
 
 // Waits until all but the wave's last N loads into LDS have landed, and all
@@ -488,6 +489,9 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_tile(GemmArgs a) {
   wait_loads<>();
   barrier();                                   // every wave is done with the operands
   float* rows = (float*)smem + wave * kPass * kRowF;
+  // The largest tiles belong to outputs that would push the operands out of
+  // the L2s (8192 x 4096 x 16384 bf16: 776 us, not 833).
+  constexpr bool kStream = BM == 256;
   constexpr int kLanes = (EPI == kEpiGated ? TN / 2 : TN) / 8;   // lanes of a row, eight columns each
   const int64_t part_cols = EPI == kEpiGated ? 2 * (int64_t)a.n : a.n;
 #pragma unroll
@@ -517,12 +521,12 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_tile(GemmArgs a) {
             put8<float>(part, c, v);
             put8<float>(part, a.n + c, u);
           } else {
-            finish8_gated<T>(a, m, c, v, u);
+            finish8_gated<T, kStream>(a, m, c, v, u);
           }
         } else {
           if (a.splits > 1) put8<float>(part, c, v);
-          else if constexpr (EPI == kEpiLinear) finish8_linear<T>(a, m, c, v);
-          else put8<T>(a.c, m * a.ldc + c, v);
+          else if constexpr (EPI == kEpiLinear) finish8_linear<T, kStream>(a, m, c, v);
+          else put8<T, kStream>(a.c, m * a.ldc + c, v);
         }
       } else {
 #pragma unroll 1
