@@ -106,19 +106,15 @@ template <typename T, int TPR, int E, int V> struct Row {
       for (int j = 0; j < V; j++)
         if (j >= skip[i]) f(i * V + j, col[i] + j);
   }
-  __device__ inline void store(T* p, const float* in, bool stream) const {
+  template <bool STREAM> __device__ inline void store(T* p, const float* in) const {
 #pragma unroll
     for (int i = 0; i < P; i++) {
       if (skip[i] == 0) {
         Pack<T, V> q;
 #pragma unroll
         for (int j = 0; j < V; j++) q.v[j] = (T)in[i * V + j];
-        if constexpr (V * sizeof(T) == 16) {
-          if (stream) stream_pack<T, V>(p + col[i], q);
-          else store_pack<T, V>(p + col[i], q);
-        } else {
-          store_pack<T, V>(p + col[i], q);
-        }
+        if constexpr (STREAM) stream_pack<T, V>(p + col[i], q);
+        else store_pack<T, V>(p + col[i], q);
       } else {
 #pragma unroll
         for (int j = 0; j < V; j++)
@@ -128,7 +124,7 @@ template <typename T, int TPR, int E, int V> struct Row {
   }
 };
 
-template <typename T, typename W, int TPR, int E, int V>
+template <typename T, typename W, int TPR, int E, int V, bool STREAM>
 __global__ __launch_bounds__(TPR < kBlock ? kBlock : TPR) void norm_forward(NormArgs a) {
   using R = Row<T, TPR, E, V>;
   constexpr int kThreads = TPR < kBlock ? kBlock : TPR;
@@ -173,7 +169,7 @@ __global__ __launch_bounds__(TPR < kBlock ? kBlock : TPR) void norm_forward(Norm
       const float scale = a.weight ? (float)w.q[i / V].v[i % V] : 1.0f, shift = a.bias ? (float)b.q[i / V].v[i % V] : 0.0f;
       v[i] = fmaf(v[i] * rstd, scale, shift);
     }
-    r.store((T*)a.y + row * a.ldy, v, a.stream);
+    r.template store<STREAM>((T*)a.y + row * a.ldy, v);
   }
 }
 
@@ -203,7 +199,7 @@ template <typename T, typename W> __global__ __launch_bounds__(1024) void norm_f
   }
 }
 
-template <typename T, typename W, int TPR, int E, int V, int kRows>
+template <typename T, typename W, int TPR, int E, int V, int kRows, bool STREAM>
 __global__ __launch_bounds__(TPR * kRows) void norm_backward(NormArgs a) {
   using R = Row<T, TPR, E, V>;
   constexpr int kThreads = TPR * kRows;
@@ -256,7 +252,7 @@ __global__ __launch_bounds__(TPR * kRows) void norm_backward(NormArgs a) {
       sgh *= a.inv_cols;
 #pragma unroll
       for (int i = 0; i < E; i++) dy[i] = rstd * (dy[i] - sg - h[i] * sgh);
-      if (live) r.store((T*)a.y + row * a.ldy, dy, a.stream);
+      if (live) r.template store<STREAM>((T*)a.y + row * a.ldy, dy);
     }
   }
   if (!a.part) return;
@@ -357,14 +353,18 @@ template <typename T, typename W> hipError_t forward(const NormArgs& a, hipStrea
     return hipGetLastError();
   };
   constexpr int V = 16 / sizeof(T);
-  if (a.cols < V) return go(norm_forward<T, W, 16, 1, 1>, 16);
-  if (a.cols <= 16 * 8) return go(norm_forward<T, W, 16, 8, V>, 16);
-  if (a.cols <= 64 * 8) return go(norm_forward<T, W, 64, 8, V>, 64);
-  if (a.cols <= 64 * 16) return go(norm_forward<T, W, 64, 16, V>, 64);
-  if (a.cols <= 256 * 8) return go(norm_forward<T, W, 256, 8, V>, 256);
-  if (a.cols <= 256 * 16) return go(norm_forward<T, W, 256, 16, V>, 256);
-  if (a.cols <= 512 * 16) return go(norm_forward<T, W, 512, 16, V>, 512);
-  if (a.cols <= kLongest) return go(norm_forward<T, W, 1024, 16, V>, 1024);
+  if (a.cols < V) return go(norm_forward<T, W, 16, 1, 1, false>, 16);
+#define RINGAR_NORM(tpr, e) \
+  if (a.cols <= tpr * e) return a.stream ? go(norm_forward<T, W, tpr, e, V, true>, tpr) : go(norm_forward<T, W, tpr, e, V, false>, tpr)
+  RINGAR_NORM(16, 8);
+  RINGAR_NORM(64, 8);
+  RINGAR_NORM(64, 16);
+  RINGAR_NORM(256, 8);
+  RINGAR_NORM(256, 16);
+  RINGAR_NORM(512, 16);
+  RINGAR_NORM(1024, 16);
+#undef RINGAR_NORM
+  static_assert(kLongest == 1024 * 16, "the widest rows held in registers");
   hipLaunchKernelGGL((norm_forward_long<T, W>), dim3((unsigned)a.rows), dim3(1024), 0, st, a);
   return hipGetLastError();
 }
@@ -375,14 +375,18 @@ template <typename T, typename W> hipError_t backward(const NormArgs& a, hipStre
     return hipGetLastError();
   };
   constexpr int V = 16 / sizeof(T);
-  if (a.cols < V) return go(norm_backward<T, W, 16, 1, 1, 16>, 256);
-  if (a.cols <= 16 * 8) return go(norm_backward<T, W, 16, 8, V, 16>, 256);
-  if (a.cols <= 64 * 8) return go(norm_backward<T, W, 64, 8, V, 8>, 512);
-  if (a.cols <= 64 * 16) return go(norm_backward<T, W, 64, 16, V, 8>, 512);
-  if (a.cols <= 256 * 8) return go(norm_backward<T, W, 256, 8, V, 2>, 512);
-  if (a.cols <= 256 * 16) return go(norm_backward<T, W, 256, 16, V, 2>, 512);
-  if (a.cols <= 512 * 16) return go(norm_backward<T, W, 512, 16, V, 1>, 512);
-  if (a.cols <= kLongest) return go(norm_backward<T, W, 512, 32, V, 1>, 512);
+  if (a.cols < V) return go(norm_backward<T, W, 16, 1, 1, 16, false>, 256);
+#define RINGAR_NORM(tpr, e, rows)                                                                     \
+  if (a.cols <= tpr * e)                                                                              \
+    return a.stream ? go(norm_backward<T, W, tpr, e, V, rows, true>, tpr * rows) : go(norm_backward<T, W, tpr, e, V, rows, false>, tpr * rows)
+  RINGAR_NORM(16, 8, 16);
+  RINGAR_NORM(64, 8, 8);
+  RINGAR_NORM(64, 16, 8);
+  RINGAR_NORM(256, 8, 2);
+  RINGAR_NORM(256, 16, 2);
+  RINGAR_NORM(512, 16, 1);
+  RINGAR_NORM(512, 32, 1);
+#undef RINGAR_NORM
   if (a.y) {
     hipLaunchKernelGGL((norm_backward_long<T, W>), dim3((unsigned)a.rows), dim3(1024), 0, st, a);
     const hipError_t e = hipGetLastError();
