@@ -365,7 +365,7 @@ static ringar_result_t product_backward(const ringar_linear_backward_t* p, bool 
   z.lddz = (wide + 63) / 64 * 64;
   z.rows = p->rows;
   z.n = (int)p->out_features;
-  z.groups = p->rows && p->out_features ? dz_groups(p->rows, p->out_features) : 0;
+  z.groups = p->rows && p->out_features ? dz_groups(p->dtype, p->rows, p->out_features) : 0;
   z.act = p->act;
   z.gated = gated;
   // dx[m][k] = sum_n dz[m][n] w[n][k];  dw[n][k] = sum_m dz[m][n] x[m][k]
@@ -399,16 +399,27 @@ static ringar_result_t product_backward(const ringar_linear_backward_t* p, bool 
   Layout l;
   const size_t at_dz = l.add(need_dz ? (size_t)p->rows * z.lddz * es : 0);
   const size_t at_sum = l.add(p->dbias ? (size_t)z.groups * wide * 4 : 0);
-  const size_t at_gemm = l.add(px.bytes > pw.bytes ? px.bytes : pw.bytes);
+  const bool together = p->dx && p->dweight && gradients_together(px, pw);
+  const size_t at_x = l.add(together ? px.bytes : px.bytes > pw.bytes ? px.bytes : pw.bytes);
+  const size_t at_w = together ? l.add(pw.bytes) : at_x;
+  const bool finish = p->dbias && z.groups && dz_finishes(p->dtype, p->out_features, z.groups);
   std::lock_guard<std::mutex> lock(g_ws_mu);
   char* ws = nullptr;
   TRY(workspace(st, l.bytes, &ws));
   if (need_dz) px.args.a = pw.args.a = z.dz = ws + at_dz;
-  if (p->dbias) z.part = (float*)(ws + at_sum);
-  if ((z.dz || z.part) && p->rows && p->out_features) HIP_TRY(launch_dz(p->dtype, z, st));
-  if (p->dbias && wide) HIP_TRY(launch_col_sum(p->dtype, {z.part, z.groups, wide, wide, p->dbias, nullptr}, st));
-  if (p->dx) TRY(run_gemm(p->dtype, px, ws, at_gemm, st));
-  if (p->dweight) TRY(run_gemm(p->dtype, pw, ws, at_gemm, st));
+  if (p->dbias && ws) z.part = (float*)(ws + at_sum);
+  if (finish) {
+    z.sums = p->dbias;
+    z.arrived = (uint32_t*)(ws - kCounterBytes);
+  }
+  if ((z.dz || z.part) && z.groups) HIP_TRY(launch_dz(p->dtype, z, st));
+  if (p->dbias && wide && !finish) HIP_TRY(launch_col_sum(p->dtype, {z.part, z.groups, wide, wide, p->dbias, nullptr}, st));
+  if (together) {
+    HIP_TRY(launch_gradients(p->dtype, px, pw, ws ? ws + at_x : nullptr, ws ? ws + at_w : nullptr, st));
+  } else {
+    if (p->dx) TRY(run_gemm(p->dtype, px, ws, at_x, st));
+    if (p->dweight) TRY(run_gemm(p->dtype, pw, ws, at_w, st));
+  }
   return RINGAR_SUCCESS;
 }
 

@@ -134,6 +134,28 @@ template <bool FAST, int N> __device__ inline void activate_grad_n(int act, cons
   }
 }
 
+// Parts that blocks on different XCDs pass to each other: agent-scope
+// accesses, which go past the XCDs' own caches, so that no cache has to be
+// written back or discarded (fences that do this for every block cost 40 us
+// where the product takes 10).
+__device__ inline void put_part(float* p, float v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ inline float get_part(const float* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
+// Called by every thread of `blocks` blocks after their put_part()s: true in
+// the block that arrives last, which may then get_part() every part.  The
+// counter is zero before and after (it belongs to the workspace).
+__device__ inline bool last_to_arrive(uint32_t* counter, int blocks) {
+  __shared__ bool last;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this thread's parts have reached memory
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)blocks - 1;
+    if (last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  return last;
+}
+
 // ------------------------------------------------------------- layer norm
 struct NormArgs {
   const void* x;
@@ -211,6 +233,8 @@ struct DzArgs {
   const void* pre;       // [rows][n], gated [rows][2n]
   void* dz;              // [rows][n], gated [rows][2n]; null: not wanted
   float* part;           // [groups][n or 2n] partial column sums, or null
+  void* sums;            // the column sums, where the kernel finishes them, or null
+  uint32_t* arrived;     // groups > 1: a zero for every block of columns
   int64_t lddy, ldp, lddz;
   int64_t rows;
   int n;
@@ -236,7 +260,9 @@ hipError_t launch_norm_backward(int dtype, int wdtype, const NormArgs& a, hipStr
 int norm_backward_groups(int64_t rows, int cols);
 hipError_t launch_col_sum(int out_dtype, const ColSumArgs& a, hipStream_t st);
 hipError_t launch_dz(int dtype, const DzArgs& a, hipStream_t st);
-int dz_groups(int64_t rows, int64_t cols);
+int dz_groups(int dtype, int64_t rows, int64_t n);
+// Whether the dz kernel can finish the column sums itself.
+bool dz_finishes(int dtype, int64_t n, int groups);
 // Counters at the start of every workspace, zero between calls.
 constexpr int kCounters = 4096;
 // Chooses the kernel, the split of k and the copies from sizes, strides and
@@ -246,6 +272,10 @@ GemmPlan plan_gemm(int dtype, int epi, const GemmArgs& a);
 int64_t gemm_blocks(const GemmPlan& p);
 // `ws`: p.bytes of workspace; `counters`: kCounters zeros.
 hipError_t launch_gemm(int dtype, const GemmPlan& p, char* ws, uint32_t* counters, hipStream_t st);
+// dx and dweight in one launch (their workspaces apart), where both run the
+// same tile: a launch less, and the one fills what the other leaves idle.
+bool gradients_together(const GemmPlan& x, const GemmPlan& w);
+hipError_t launch_gradients(int dtype, const GemmPlan& x, const GemmPlan& w, char* ws_x, char* ws_w, hipStream_t st);
 hipError_t launch_pack(int dtype, const PackArgs& a, hipStream_t st);
 
 }  // namespace ringar

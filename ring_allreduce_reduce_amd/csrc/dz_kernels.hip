@@ -58,21 +58,47 @@ template <typename T, bool GATED, int V> __global__ __launch_bounds__(256) void 
       if constexpr (GATED) store_pack<T, V>(o + a.n, ou);
     }
   }
-  if (!a.part) return;
+  if (!a.part && !a.sums) return;
+  // Column sums: the waves' through LDS, then the blocks' rows of parts, added
+  // in order by the last block of these columns to arrive (or, where there
+  // are many, by a pass of their own).
+  constexpr int kSides = GATED ? 2 : 1;
   __shared__ float smem[4][64 * V];
-  const int64_t cols = GATED ? 2 * (int64_t)a.n : a.n;
+  const int64_t cols = kSides * (int64_t)a.n, first = (int64_t)blockIdx.x * 64 * V;
+  T* out = (T*)a.sums;
 #pragma unroll
-  for (int which = 0; which < (GATED ? 2 : 1); which++) {
+  for (int which = 0; which < kSides; which++) {
     if (which) __syncthreads();
 #pragma unroll
     for (int j = 0; j < V; j++)
-      if (j >= skip) smem[wave][c - (int64_t)blockIdx.x * 64 * V + j] = which ? su[j] : s[j];
+      if (j >= skip) smem[wave][c - first + j] = which ? su[j] : s[j];
     __syncthreads();
     for (int i = threadIdx.x; i < 64 * V; i += 256) {
-      const int64_t col = (int64_t)blockIdx.x * 64 * V + i;
-      if (col < a.n)
-        a.part[blockIdx.y * cols + (which ? a.n : 0) + col] = (smem[0][i] + smem[1][i]) + (smem[2][i] + smem[3][i]);
+      if (first + i >= a.n) continue;
+      const float sum = (smem[0][i] + smem[1][i]) + (smem[2][i] + smem[3][i]);
+      if (out && a.groups == 1) out[(which ? a.n : 0) + first + i] = (T)sum;
+      else put_part(a.part + blockIdx.y * cols + (which ? a.n : 0) + first + i, sum);
     }
+  }
+  if (!out || a.groups == 1 || !last_to_arrive(a.arrived + blockIdx.x, a.groups)) return;
+  // a thread's columns side by side, so that their loads are in flight together
+  constexpr int kMine = (64 * V + 255) / 256;
+  float sum[kSides * kMine];
+  int64_t at[kSides * kMine];
+#pragma unroll
+  for (int c = 0; c < kSides * kMine; c++) {
+    const int64_t col = first + threadIdx.x + c % kMine * 256;
+    at[c] = (c < kMine ? 0 : a.n) + (col < a.n ? col : a.n - 1);
+    sum[c] = 0.0f;
+  }
+#pragma unroll 8
+  for (int g = 0; g < a.groups; g++)
+#pragma unroll
+    for (int c = 0; c < kSides * kMine; c++) sum[c] += get_part(a.part + g * cols + at[c]);
+#pragma unroll
+  for (int c = 0; c < kSides * kMine; c++) {
+    const int i = threadIdx.x + c % kMine * 256;
+    if (i < 64 * V && first + i < a.n) out[at[c]] = (T)sum[c];
   }
 }
 
@@ -118,14 +144,22 @@ template <typename T> hipError_t pack(const PackArgs& a, hipStream_t st) {
 }  // namespace
 
 // Row groups: enough blocks to fill the GPU (about 2048 with the column
-// groups), no more than the rows hold.
-int dz_groups(int64_t rows, int64_t n) {
-  const int64_t column_blocks = (n + 511) / 512;
-  int64_t g = 2048 / column_blocks;
-  const int64_t most = (rows + 3) / 4;
+// groups), four rows a wave or more.
+static int64_t column_blocks(int dtype, int64_t n) {
+  const int64_t v = dtype == kF32 ? 4 : 8, each = 64 * (n < v ? 1 : v);
+  return (n + each - 1) / each;
+}
+
+int dz_groups(int dtype, int64_t rows, int64_t n) {
+  int64_t g = 2048 / column_blocks(dtype, n);
+  const int64_t most = (rows + 15) / 16;
   if (g > most) g = most;
   return (int)(g < 1 ? 1 : g);
 }
+
+// Up to 32 parts a column, which a last block adds in about 2 us (a launch
+// for it costs more); 100 would take it longer than col_sum's whole grid.
+bool dz_finishes(int dtype, int64_t n, int groups) { return groups == 1 || (groups <= 32 && column_blocks(dtype, n) <= kCounters); }
 
 hipError_t launch_pack(int dtype, const PackArgs& a, hipStream_t st) {
   if (dtype == kF32) return pack<float>(a, st);

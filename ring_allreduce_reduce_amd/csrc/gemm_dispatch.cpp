@@ -6,6 +6,9 @@ namespace ringar {
 hipError_t launch_gemm_f16(int epi, const GemmArgs& a, hipStream_t st);
 hipError_t launch_gemm_bf16(int epi, const GemmArgs& a, hipStream_t st);
 hipError_t launch_gemm_f32(int epi, const GemmArgs& a, hipStream_t st);
+hipError_t launch_gradients_f16(const GemmArgs& x, const GemmArgs& w, hipStream_t st);
+hipError_t launch_gradients_bf16(const GemmArgs& x, const GemmArgs& w, hipStream_t st);
+hipError_t launch_gradients_f32(const GemmArgs& x, const GemmArgs& w, hipStream_t st);
 
 namespace {
 
@@ -153,9 +156,10 @@ GemmPlan plan_gemm(int dtype, int epi, const GemmArgs& given) {
 
 int64_t gemm_blocks(const GemmPlan& p) { return p.args.m && p.args.n ? tiles_of(p.args.variant, p.epi, p.args) * p.args.splits : 0; }
 
-hipError_t launch_gemm(int dtype, const GemmPlan& p, char* ws, uint32_t* counters, hipStream_t st) {
+// The planned product's arguments with its workspace in place and its copies
+// enqueued.
+static hipError_t prepare(int dtype, const GemmPlan& p, char* ws, uint32_t* counters, hipStream_t st, GemmArgs* out) {
   GemmArgs a = p.args;
-  if (a.m == 0 || a.n == 0) return hipSuccess;
   const int es = dtype == kF32 ? 4 : 2;
   const int64_t wide = p.epi == kEpiGated ? 2 * (int64_t)a.n : a.n;
   auto part = [&](size_t n) {
@@ -176,10 +180,34 @@ hipError_t launch_gemm(int dtype, const GemmPlan& p, char* ws, uint32_t* counter
   hipError_t e = hipSuccess;
   if (p.pack_a) e = a.sak == 1 ? pack(&a.a, &a.sam, p.packed_a, a.m, a.k) : pack(&a.a, &a.sak, p.packed_a, a.k, a.m);
   if (e == hipSuccess && p.pack_b) e = a.sbk == 1 ? pack(&a.b, &a.sbn, p.packed_b, wide, a.k) : pack(&a.b, &a.sbk, p.packed_b, a.k, wide);
+  *out = a;
+  return e;
+}
+
+hipError_t launch_gemm(int dtype, const GemmPlan& p, char* ws, uint32_t* counters, hipStream_t st) {
+  if (p.args.m == 0 || p.args.n == 0) return hipSuccess;
+  GemmArgs a;
+  const hipError_t e = prepare(dtype, p, ws, counters, st, &a);
   if (e != hipSuccess) return e;
   if (dtype == kF16) return launch_gemm_f16(p.epi, a, st);
   if (dtype == kBF16) return launch_gemm_bf16(p.epi, a, st);
   return launch_gemm_f32(p.epi, a, st);
+}
+
+bool gradients_together(const GemmPlan& x, const GemmPlan& w) {
+  const int v = x.args.variant;
+  return x.args.m && x.args.n && w.args.m && w.args.n && v == w.args.variant && (v == kTile64 || v == kTile128) &&
+         gemm_blocks(x) + gemm_blocks(w) < 0x7fffffff;
+}
+
+hipError_t launch_gradients(int dtype, const GemmPlan& x, const GemmPlan& w, char* ws_x, char* ws_w, hipStream_t st) {
+  GemmArgs ax, aw;
+  hipError_t e = prepare(dtype, x, ws_x, nullptr, st, &ax);
+  if (e == hipSuccess) e = prepare(dtype, w, ws_w, nullptr, st, &aw);
+  if (e != hipSuccess) return e;
+  if (dtype == kF16) return launch_gradients_f16(ax, aw, st);
+  if (dtype == kBF16) return launch_gradients_bf16(ax, aw, st);
+  return launch_gradients_f32(ax, aw, st);
 }
 
 }  // namespace ringar

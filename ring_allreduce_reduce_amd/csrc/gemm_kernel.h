@@ -32,28 +32,6 @@ template <typename T> __device__ inline void finish_gated(const GemmArgs& a, int
   ((T*)a.c)[m * a.ldc + n] = (T)(activate<kFast>(a.act, g) * u);
 }
 
-// Parts that blocks on different XCDs pass to each other: agent-scope
-// accesses, which go past the XCDs' own caches, so that no cache has to be
-// written back or discarded (fences that do this for every block cost 40 us
-// where the product takes 10).
-__device__ inline void put_part(float* p, float v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
-__device__ inline float get_part(const float* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
-
-// Called by every thread of `blocks` blocks after their put_part()s: true in
-// the block that arrives last, which may then get_part() every part.  The
-// counter is zero before and after (it belongs to the workspace).
-__device__ inline bool last_to_arrive(uint32_t* counter, int blocks) {
-  __shared__ bool last;
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this thread's parts have reached memory
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)blocks - 1;
-    if (last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  __syncthreads();
-  return last;
-}
-
 // ------------------------------------------------------- matrix instructions
 // One 16 x 16 block of C gains the products over KSTEP values of k.  Lane l
 // holds KSTEP / 4 values of row (column) l % 16; which ones is the same on

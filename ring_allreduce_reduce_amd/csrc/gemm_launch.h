@@ -11,7 +11,16 @@ inline unsigned blocks_of(const GemmArgs& a, int cols_of_tile, int rows_of_tile,
   return (unsigned)((cols + cols_of_tile - 1) / cols_of_tile * (((int64_t)a.m + rows_of_tile - 1) / rows_of_tile) * a.splits);
 }
 
+template <typename T, bool AROW, bool BROW, int EPI> struct Kernels {
+  using Large = GemmTile<T, AROW, BROW, EPI, 256, 256, 2, 4, true>;
+  using Middle = GemmTile<T, AROW, BROW, EPI, 128, 128, 4, 2, true>;
+  static constexpr int kCols = EPI == kEpiGated ? 128 : 64;
+  using Small = GemmTile<T, AROW, BROW, EPI, 64, kCols, 2, 2, true, 3>;
+  using Staged = GemmTile<T, AROW, BROW, EPI, 64, kCols, 2, 2, false>;
+};
+
 template <typename T, bool AROW, bool BROW, int EPI> hipError_t launch_tiled(const GemmArgs& a, hipStream_t st) {
+  using K = Kernels<T, AROW, BROW, EPI>;
   const int64_t cols = EPI == kEpiGated ? 2 * (int64_t)a.n : a.n;
   auto go = [&](auto kernel, int bm, int bn, int threads) {
     hipLaunchKernelGGL(kernel, dim3(blocks_of(a, bn, bm, cols)), dim3(threads), 0, st, a);
@@ -19,7 +28,7 @@ template <typename T, bool AROW, bool BROW, int EPI> hipError_t launch_tiled(con
   };
   switch (a.variant) {
     case kTile256:
-      if constexpr (sizeof(T) == 2) return go(gemm_tile<T, AROW, BROW, EPI, 256, 256, 2, 4, 2, true>, 256, 256, 512);
+      if constexpr (sizeof(T) == 2) return go(gemm_tile<typename K::Large, 2>, 256, 256, 512);
       return hipErrorInvalidValue;
     case kRows:
       if constexpr (EPI != kEpiStore) {
@@ -27,14 +36,24 @@ template <typename T, bool AROW, bool BROW, int EPI> hipError_t launch_tiled(con
         return hipGetLastError();
       }
       return hipErrorInvalidValue;
-    case kTile128: return go(gemm_tile<T, AROW, BROW, EPI, 128, 128, 4, 2, 4, true>, 128, 128, 512);
-    case kTile64:
-      if constexpr (EPI == kEpiGated) return go(gemm_tile<T, AROW, BROW, EPI, 64, 128, 2, 2, 2, true, 3>, 64, 128, 256);
-      else return go(gemm_tile<T, AROW, BROW, EPI, 64, 64, 2, 2, 2, true, 3>, 64, 64, 256);
-    default:
-      if constexpr (EPI == kEpiGated) return go(gemm_tile<T, AROW, BROW, EPI, 64, 128, 2, 2, 2, false>, 64, 128, 256);
-      else return go(gemm_tile<T, AROW, BROW, EPI, 64, 64, 2, 2, 2, false>, 64, 64, 256);
+    case kTile128: return go(gemm_tile<typename K::Middle, 4>, 128, 128, 512);
+    case kTile64: return go(gemm_tile<typename K::Small, 2>, 64, K::kCols, 256);
+    default: return go(gemm_tile<typename K::Staged, 2>, 64, K::kCols, 256);
   }
+}
+
+// dx and dweight together: both of kTile128 or both of kTile64.
+template <typename T> hipError_t launch_gradients(const GemmArgs& x, const GemmArgs& w, hipStream_t st) {
+  using X = Kernels<T, true, false, kEpiStore>;
+  using W = Kernels<T, false, false, kEpiStore>;
+  if (x.variant == kTile128) {
+    const unsigned bx = blocks_of(x, 128, 128, x.n), bw = blocks_of(w, 128, 128, w.n);
+    hipLaunchKernelGGL((gemm_pair<typename X::Middle, typename W::Middle, 4>), dim3(bx + bw), dim3(512), 0, st, x, w, bx);
+  } else {
+    const unsigned bx = blocks_of(x, 64, 64, x.n), bw = blocks_of(w, 64, 64, w.n);
+    hipLaunchKernelGGL((gemm_pair<typename X::Small, typename W::Small, 2>), dim3(bx + bw), dim3(256), 0, st, x, w, bx);
+  }
+  return hipGetLastError();
 }
 
 template <typename T, int EPI> hipError_t join(const GemmArgs& a, hipStream_t st) {

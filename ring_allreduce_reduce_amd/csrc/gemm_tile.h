@@ -290,20 +290,26 @@ __device__ inline void barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <typename T, bool AROW, bool BROW, int EPI, int BM, int BN, int WM, int WN, int OCC, bool DIRECT, int STAGES = 2>
-__global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_tile(GemmArgs a) {
-  constexpr int NW = WM * WN;
+// One tile's kernel: run() computes block `block` of the product's grid.
+template <typename T, bool AROW, bool BROW, int EPI, int BM, int BN, int WM, int WN, bool DIRECT, int STAGES = 2>
+struct GemmTile {
+  static constexpr int NW = WM * WN, kThreads = 64 * NW;
   using OA = std::conditional_t<DIRECT, Operand<T, AROW, BM, NW>, StagedOperand<T, AROW, BM, NW>>;
   using OB = std::conditional_t<DIRECT, Operand<T, BROW, BN, NW>, StagedOperand<T, BROW, BN, NW>>;
-  constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
-  constexpr int kBK = OA::kBK;
+  static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+  static constexpr int kBK = OA::kBK;
   static_assert(TN == 64 || (TN == 32 && EPI != kEpiGated), "eight or four lanes finish a wave's row");
   static_assert(BROW || EPI == kEpiStore, "epilogues with columns of their own read weights by rows");
-  constexpr int kStage = OA::kBytes + OB::kBytes;
+  static constexpr int kStage = OA::kBytes + OB::kBytes;
   // epilogue: a wave's rows in fp32, shifted 16 bytes over the banks
-  constexpr int kPass = TM < 32 ? TM : 32, kRowF = TN + 4;
-  constexpr int kShared = STAGES * kStage > NW * kPass * kRowF * 4 ? STAGES * kStage : NW * kPass * kRowF * 4;
-  __shared__ __attribute__((aligned(1024))) char smem[kShared];
+  static constexpr int kPass = TM < 32 ? TM : 32, kRowF = TN + 4;
+  static constexpr int kShared = STAGES * kStage > NW * kPass * kRowF * 4 ? STAGES * kStage : NW * kPass * kRowF * 4;
+
+  static __device__ inline void run(const GemmArgs& a, unsigned block, char* smem);
+};
+
+template <typename T, bool AROW, bool BROW, int EPI, int BM, int BN, int WM, int WN, bool DIRECT, int STAGES>
+__device__ inline void GemmTile<T, AROW, BROW, EPI, BM, BN, WM, WN, DIRECT, STAGES>::run(const GemmArgs& a, unsigned block, char* smem) {
   using Frag = typename Mma<T>::Frag;
 
   // Blocks go round the 8 XCDs in turn: give each XCD a run of neighbouring
@@ -312,8 +318,8 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_tile(GemmArgs a) {
   const int tiles_m = (a.m + BM - 1) / BM, tiles_n = (a.n + kOut - 1) / kOut;
   const int tiles = tiles_m * tiles_n;
   const int total = tiles * a.splits;
-  const int q = total >> 3, rest = total & 7, xcd = blockIdx.x & 7;
-  const int id = xcd * q + (xcd < rest ? xcd : rest) + (blockIdx.x >> 3);
+  const int q = total >> 3, rest = total & 7, xcd = block & 7;
+  const int id = xcd * q + (xcd < rest ? xcd : rest) + (block >> 3);
   const int split = id / tiles, tile = id % tiles;
   const int band = tile / (8 * tiles_n), in_band = tile % (8 * tiles_n);
   const int deep = tiles_m - band * 8 < 8 ? tiles_m - band * 8 : 8;
@@ -548,6 +554,20 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_tile(GemmArgs a) {
     }
     asm volatile("" ::: "memory");
   }
+}
+
+template <typename K, int OCC> __global__ __launch_bounds__(K::kThreads, OCC) void gemm_tile(GemmArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[K::kShared];
+  K::run(a, blockIdx.x, smem);
+}
+
+// Two products that do not wait for each other in one launch: the first
+// `blocks` blocks are the first's.
+template <typename K, typename L, int OCC> __global__ __launch_bounds__(K::kThreads, OCC) void gemm_pair(GemmArgs a, GemmArgs b, unsigned blocks) {
+  static_assert(K::kThreads == L::kThreads, "one block size");
+  __shared__ __attribute__((aligned(1024))) char smem[K::kShared > L::kShared ? K::kShared : L::kShared];
+  if (blockIdx.x < blocks) K::run(a, blockIdx.x, smem);
+  else L::run(b, blockIdx.x - blocks, smem);
 }
 
 }  // namespace ringar
