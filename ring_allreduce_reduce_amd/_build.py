@@ -40,6 +40,30 @@ def _hipcc() -> str:
     return os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 
+EXT = os.path.join(HERE, "_block_ext.so")
+
+
+def build_ext() -> str:
+    """The block operators' torch binding (host code only), linked to the
+    library next to it."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "/opt/rocm/include", sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[a for i in inc for a in ("-isystem", i)], os.path.join(CSRC, "torch_block.cpp"), "-o", EXT + ".tmp",
+           "-L", HERE, "-lringar", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(base, "lib"), "-Wl,-rpath," + os.path.join(base, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on torch_block.cpp:\n{r.stderr}")
+    os.replace(EXT + ".tmp", EXT)
+    return EXT
+
+
 def build(out: str = LIB, extra: list | None = None, verbose: bool = False, jobs: int = 8) -> str:
     inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
     with tempfile.TemporaryDirectory(prefix="ringar_build_") as tmp:
@@ -73,3 +97,4 @@ if __name__ == "__main__":
     else:
         build(verbose=False)
         print(LIB)
+        print(build_ext())

@@ -87,6 +87,21 @@ def test_nothing_to_do_needs_no_gpu():
     assert call("ringar_gated_ffn", lin(out_features=0, weight=None, y=None)) == ra.SUCCESS
 
 
+def test_tensor_calls_refuse_what_is_not_on_a_gpu():
+    import torch
+    libutil.lib()
+    t = torch.zeros(4, 8)
+    stats = torch.zeros(4)
+    calls = [lambda: ra.layer_norm(t), lambda: ra.linear(t, t), lambda: ra.gated_ffn(t, t),
+             lambda: ra.layer_norm_backward(t, t, stats, stats), lambda: ra.linear_backward(t, t, t, t),
+             lambda: ra.gated_ffn_backward(t, t, t, t), lambda: ra.linear(None, t), lambda: ra.layer_norm("x"),
+             lambda: ra.linear(t, t, act="swish"), lambda: ra.gated_ffn_backward(t, t, t, t, act=3)]
+    for i, call in enumerate(calls):
+        with pytest.raises(ra.RingarError) as e:
+            call()
+        assert e.value.code == BAD_ARG, i
+
+
 def test_struct_layouts_match_the_header(tmp_path):
     """sizeof and every field's offset, as a C compiler sees the header."""
     import os
