@@ -181,7 +181,7 @@ ringar_result_t run_gemm(int dtype, const GemmPlan& p, char* ws, size_t at, hipS
 }
 
 ringar_result_t check_plan(const GemmPlan& p) {
-  if (gemm_blocks(p) > kMaxDim) return refuse(RINGAR_ERR_INVALID_USAGE, "the product has more tiles than one launch takes");
+  if (p.too_many) return refuse(RINGAR_ERR_INVALID_USAGE, "the product has more tiles than one launch takes");
   return RINGAR_SUCCESS;
 }
 

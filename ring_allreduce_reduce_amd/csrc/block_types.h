@@ -198,6 +198,10 @@ struct GemmArgs {
   int variant;           // kernel, set with the split by plan_gemm
   int splits;            // parts of k, each a multiple of the tile's k
   int k_per_split;
+  int tile_first;        // tiles of this launch (of twice the kernel's tile
+  int tile_count;        // either way where `quarters`: four blocks each)
+  bool quarters;
+  int tail_count;        // kTile256: tiles left to 128 x 128 blocks
   float* part;           // splits > 1: [splits][m][n, gated 2n]
   uint32_t* arrived;     // kRows with splits > 1: a zero for every tile
   // epilogue
@@ -218,6 +222,7 @@ struct GemmPlan {
   bool pack_a, pack_b;
   int64_t packed_a, packed_b;   // the copies' row strides
   size_t bytes;                 // workspace
+  bool too_many;                // more blocks than a launch takes
 };
 struct PackArgs {
   const void* from;
@@ -268,8 +273,6 @@ constexpr int kCounters = 4096;
 // Chooses the kernel, the split of k and the copies from sizes, strides and
 // alignment alone.
 GemmPlan plan_gemm(int dtype, int epi, const GemmArgs& a);
-// Blocks of the planned launch.
-int64_t gemm_blocks(const GemmPlan& p);
 // `ws`: p.bytes of workspace; `counters`: kCounters zeros.
 hipError_t launch_gemm(int dtype, const GemmPlan& p, char* ws, uint32_t* counters, hipStream_t st);
 // dx and dweight in one launch (their workspaces apart), where both run the

@@ -69,6 +69,14 @@ struct Choice {
   double us;
 };
 
+// 256 x 256 tiles run one to a CU: a few left over for a last round are done
+// in quarters by 128 x 128 blocks, which take less than half as long (2500 x
+// 4096 x 2 * 10240 bf16: 800 tiles, 32 of them in quarters).
+int tail_of(int variant, int splits, int64_t tiles) {
+  const int left = (int)(tiles % 256);
+  return variant == kTile256 && splits == 1 && tiles > 256 && left <= 64 ? left : 0;
+}
+
 // The cheapest split of one kernel: parts of k fill the GPU where the output
 // has few tiles, and cost a pass over the parts.
 Choice cheapest(int variant, int epi, int es, const GemmArgs& a) {
@@ -80,7 +88,8 @@ Choice cheapest(int variant, int epi, int es, const GemmArgs& a) {
     if (s > 1 && steps < 2 * s) break;
     const int64_t per = ceil_div(steps, s);
     const double at_once = c.shared * (double)ceil_div(tiles * s, 256);
-    const double us = c.start + (per + 1.5) * (at_once > c.alone ? at_once : c.alone) + (s > 1 ? 4.5 + outputs * s * 8 / 8e6 : 0);
+    double us = c.start + (per + 1.5) * (at_once > c.alone ? at_once : c.alone) + (s > 1 ? 4.5 + outputs * s * 8 / 8e6 : 0);
+    if (tail_of(variant, s, tiles)) us += (per + 1.5) * (cost_of(kTile128, epi, es, true, true).alone - c.shared);
     if (s == 1 || us < best.us) best = {variant, s, us};
   }
   return best;
@@ -147,14 +156,19 @@ GemmPlan plan_gemm(int dtype, int epi, const GemmArgs& given) {
   const int64_t step = 128 / es, steps = ceil_div(a.k, step), per = ceil_div(steps, best.splits);
   a.k_per_split = (int)(per * step < a.k ? per * step : a.k);
   a.splits = (int)(steps ? ceil_div(steps, per) : 1);
+  const int64_t tiles = tiles_of(a.variant, epi, a);
+  if (tiles * a.splits > 0x7fffffff - 1024) {
+    p.too_many = true;
+    return p;
+  }
+  a.tail_count = tail_of(a.variant, a.splits, tiles);
+  a.tile_count = (int)tiles - a.tail_count;
   auto part = [&](size_t n) { p.bytes += (n + 255) / 256 * 256; };
   if (a.splits > 1) part((size_t)a.splits * a.m * wide * 4);
   if (p.pack_a) part((size_t)rows_a * p.packed_a * es);
   if (p.pack_b) part((size_t)rows_b * p.packed_b * es);
   return p;
 }
-
-int64_t gemm_blocks(const GemmPlan& p) { return p.args.m && p.args.n ? tiles_of(p.args.variant, p.epi, p.args) * p.args.splits : 0; }
 
 // The planned product's arguments with its workspace in place and its copies
 // enqueued.
@@ -197,7 +211,7 @@ hipError_t launch_gemm(int dtype, const GemmPlan& p, char* ws, uint32_t* counter
 bool gradients_together(const GemmPlan& x, const GemmPlan& w) {
   const int v = x.args.variant;
   return x.args.m && x.args.n && w.args.m && w.args.n && v == w.args.variant && (v == kTile64 || v == kTile128) &&
-         gemm_blocks(x) + gemm_blocks(w) < 0x7fffffff;
+         (int64_t)x.args.tile_count * x.args.splits + (int64_t)w.args.tile_count * w.args.splits < 0x7fffffff;
 }
 
 hipError_t launch_gradients(int dtype, const GemmPlan& x, const GemmPlan& w, char* ws_x, char* ws_w, hipStream_t st) {

@@ -7,9 +7,7 @@
 
 namespace ringar {
 
-inline unsigned blocks_of(const GemmArgs& a, int cols_of_tile, int rows_of_tile, int64_t cols) {
-  return (unsigned)((cols + cols_of_tile - 1) / cols_of_tile * (((int64_t)a.m + rows_of_tile - 1) / rows_of_tile) * a.splits);
-}
+inline unsigned blocks_of(const GemmArgs& a) { return (unsigned)a.tile_count * (a.quarters ? 4 : 1) * (unsigned)a.splits; }
 
 template <typename T, bool AROW, bool BROW, int EPI> struct Kernels {
   using Large = GemmTile<T, AROW, BROW, EPI, 256, 256, 2, 4, true>;
@@ -21,14 +19,22 @@ template <typename T, bool AROW, bool BROW, int EPI> struct Kernels {
 
 template <typename T, bool AROW, bool BROW, int EPI> hipError_t launch_tiled(const GemmArgs& a, hipStream_t st) {
   using K = Kernels<T, AROW, BROW, EPI>;
-  const int64_t cols = EPI == kEpiGated ? 2 * (int64_t)a.n : a.n;
-  auto go = [&](auto kernel, int bm, int bn, int threads) {
-    hipLaunchKernelGGL(kernel, dim3(blocks_of(a, bn, bm, cols)), dim3(threads), 0, st, a);
+  auto go = [&](auto kernel, int threads) {
+    hipLaunchKernelGGL(kernel, dim3(blocks_of(a)), dim3(threads), 0, st, a);
     return hipGetLastError();
   };
   switch (a.variant) {
     case kTile256:
-      if constexpr (sizeof(T) == 2) return go(gemm_tile<typename K::Large, 2>, 256, 256, 512);
+      if constexpr (sizeof(T) == 2) {
+        if (a.tail_count == 0) return go(gemm_tile<typename K::Large, 2>, 512);
+        GemmArgs tail = a;
+        tail.tile_first = a.tile_count;
+        tail.tile_count = a.tail_count;
+        tail.quarters = true;
+        hipLaunchKernelGGL((gemm_pair<typename K::Large, typename K::Middle, 2>), dim3(blocks_of(a) + blocks_of(tail)), dim3(512), 0, st, a, tail,
+                           blocks_of(a));
+        return hipGetLastError();
+      }
       return hipErrorInvalidValue;
     case kRows:
       if constexpr (EPI != kEpiStore) {
@@ -36,9 +42,9 @@ template <typename T, bool AROW, bool BROW, int EPI> hipError_t launch_tiled(con
         return hipGetLastError();
       }
       return hipErrorInvalidValue;
-    case kTile128: return go(gemm_tile<typename K::Middle, 4>, 128, 128, 512);
-    case kTile64: return go(gemm_tile<typename K::Small, 2>, 64, K::kCols, 256);
-    default: return go(gemm_tile<typename K::Staged, 2>, 64, K::kCols, 256);
+    case kTile128: return go(gemm_tile<typename K::Middle, 4>, 512);
+    case kTile64: return go(gemm_tile<typename K::Small, 2>, 256);
+    default: return go(gemm_tile<typename K::Staged, 2>, 256);
   }
 }
 
@@ -47,10 +53,10 @@ template <typename T> hipError_t launch_gradients(const GemmArgs& x, const GemmA
   using X = Kernels<T, true, false, kEpiStore>;
   using W = Kernels<T, false, false, kEpiStore>;
   if (x.variant == kTile128) {
-    const unsigned bx = blocks_of(x, 128, 128, x.n), bw = blocks_of(w, 128, 128, w.n);
+    const unsigned bx = blocks_of(x), bw = blocks_of(w);
     hipLaunchKernelGGL((gemm_pair<typename X::Middle, typename W::Middle, 4>), dim3(bx + bw), dim3(512), 0, st, x, w, bx);
   } else {
-    const unsigned bx = blocks_of(x, 64, 64, x.n), bw = blocks_of(w, 64, 64, w.n);
+    const unsigned bx = blocks_of(x), bw = blocks_of(w);
     hipLaunchKernelGGL((gemm_pair<typename X::Small, typename W::Small, 2>), dim3(bx + bw), dim3(256), 0, st, x, w, bx);
   }
   return hipGetLastError();

@@ -315,15 +315,19 @@ __device__ inline void GemmTile<T, AROW, BROW, EPI, BM, BN, WM, WN, DIRECT, STAG
   // Blocks go round the 8 XCDs in turn: give each XCD a run of neighbouring
   // tiles, 8 tiles of rows deep, so that its blocks share operands in its L2.
   constexpr int kOut = EPI == kEpiGated ? BN / 2 : BN;    // output columns of a tile
-  const int tiles_m = (a.m + BM - 1) / BM, tiles_n = (a.n + kOut - 1) / kOut;
-  const int tiles = tiles_m * tiles_n;
+  const int sub = a.quarters ? 2 : 1;
+  const int tiles_m = (a.m + BM * sub - 1) / (BM * sub), tiles_n = (a.n + kOut * sub - 1) / (kOut * sub);
+  const int tiles = a.tile_count * sub * sub;
   const int total = tiles * a.splits;
   const int q = total >> 3, rest = total & 7, xcd = block & 7;
   const int id = xcd * q + (xcd < rest ? xcd : rest) + (block >> 3);
-  const int split = id / tiles, tile = id % tiles;
+  const int split = id / tiles, unit = id % tiles, quarter = unit % (sub * sub);
+  const int tile = a.tile_first + unit / (sub * sub);
   const int band = tile / (8 * tiles_n), in_band = tile % (8 * tiles_n);
   const int deep = tiles_m - band * 8 < 8 ? tiles_m - band * 8 : 8;
-  const int64_t m0 = (int64_t)(band * 8 + in_band % deep) * BM, n0 = (int64_t)(in_band / deep) * kOut;
+  const int64_t m0 = ((int64_t)(band * 8 + in_band % deep) * sub + (quarter & 1)) * BM;
+  const int64_t n0 = ((int64_t)(in_band / deep) * sub + (quarter >> 1)) * kOut;
+  if (m0 >= a.m || n0 >= a.n) return;          // a quarter past the edge
   const int k_begin = split * a.k_per_split;
   const int k_len = (a.k - k_begin < a.k_per_split ? a.k - k_begin : a.k_per_split);
   const int steps = (k_len + kBK - 1) / kBK;

@@ -159,7 +159,7 @@ def test_products(rows, k, n, dtype, gated):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("gated", [False, True])
-@pytest.mark.parametrize("rows,k,n", [(3601, 3608, 3624), (5000, 72, 5016)])
+@pytest.mark.parametrize("rows,k,n", [(3601, 3608, 3624), (5000, 72, 5016), (4200, 4160, 4136)])
 def test_large_products(rows, k, n, gated, dtype):
     """The largest tiles, with edges and a ragged last step in every product."""
     g = torch.Generator(device="cuda")
