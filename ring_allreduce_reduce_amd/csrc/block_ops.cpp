@@ -392,30 +392,28 @@ static ringar_result_t product_backward(const ringar_linear_backward_t* p, bool 
   gx.a = gw.a = need_dz ? (const void*)256 : p->dy;
   gx.sam = gw.sak = need_dz ? z.lddz : p->lddy;
   GemmPlan px = {}, pw = {};
-  if (p->dx) px = plan_gemm(p->dtype, kEpiStore, gx);
-  if (p->dweight) pw = plan_gemm(p->dtype, kEpiStore, gw);
+  const bool together = p->dx && p->dweight && plan_gradients(p->dtype, gx, gw, &px, &pw);
+  if (p->dx && !p->dweight) px = plan_gemm(p->dtype, kEpiStore, gx);
+  if (p->dweight && !p->dx) pw = plan_gemm(p->dtype, kEpiStore, gw);
   TRY(check_plan(px));
   TRY(check_plan(pw));
   Layout l;
   const size_t at_dz = l.add(need_dz ? (size_t)p->rows * z.lddz * es : 0);
   const size_t at_sum = l.add(p->dbias ? (size_t)z.groups * wide * 4 : 0);
-  const bool together = p->dx && p->dweight && gradients_together(px, pw);
   const size_t at_x = l.add(together ? px.bytes : px.bytes > pw.bytes ? px.bytes : pw.bytes);
   const size_t at_w = together ? l.add(pw.bytes) : at_x;
-  const bool finish = p->dbias && z.groups && dz_finishes(p->dtype, p->out_features, z.groups);
   std::lock_guard<std::mutex> lock(g_ws_mu);
   char* ws = nullptr;
   TRY(workspace(st, l.bytes, &ws));
   if (need_dz) px.args.a = pw.args.a = z.dz = ws + at_dz;
-  if (p->dbias && ws) z.part = (float*)(ws + at_sum);
-  if (finish) {
-    z.sums = p->dbias;
-    z.arrived = (uint32_t*)(ws - kCounterBytes);
-  }
-  if ((z.dz || z.part) && z.groups) HIP_TRY(launch_dz(p->dtype, z, st));
-  if (p->dbias && wide && !finish) HIP_TRY(launch_col_sum(p->dtype, {z.part, z.groups, wide, wide, p->dbias, nullptr}, st));
+  if (p->dbias && z.groups == 1) z.sums = p->dbias;
+  else if (p->dbias && z.groups) z.part = (float*)(ws + at_sum);
+  if ((z.dz || z.part || z.sums) && z.groups) HIP_TRY(launch_dz(p->dtype, z, st));
+  // the bias's parts (none: zeros), beside the products or in a launch of their own
+  const ColSumArgs sums = {z.part, z.groups, p->dbias && !z.sums ? wide : 0, wide, p->dbias, nullptr};
+  if (sums.width && !together) HIP_TRY(launch_col_sum(p->dtype, sums, st));
   if (together) {
-    HIP_TRY(launch_gradients(p->dtype, px, pw, ws ? ws + at_x : nullptr, ws ? ws + at_w : nullptr, st));
+    HIP_TRY(launch_gradients(p->dtype, px, pw, sums, ws ? ws + at_x : nullptr, ws ? ws + at_w : nullptr, st));
   } else {
     if (p->dx) TRY(run_gemm(p->dtype, px, ws, at_x, st));
     if (p->dweight) TRY(run_gemm(p->dtype, pw, ws, at_w, st));

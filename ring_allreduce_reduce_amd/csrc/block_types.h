@@ -225,11 +225,14 @@ struct GemmPlan {
   bool too_many;                // more blocks than a launch takes
 };
 struct PackArgs {
-  const void* from;
-  void* to;
-  int64_t ld_from, ld_to;
-  int64_t rows;
-  int cols;
+  struct One {
+    const void* from;
+    void* to;
+    int64_t ld_from, ld_to;
+    int64_t rows;
+    int cols;
+    unsigned blocks;
+  } one[2];               // the second may have no blocks
 };
 
 // activation's backward pass and column sums
@@ -238,8 +241,7 @@ struct DzArgs {
   const void* pre;       // [rows][n], gated [rows][2n]
   void* dz;              // [rows][n], gated [rows][2n]; null: not wanted
   float* part;           // [groups][n or 2n] partial column sums, or null
-  void* sums;            // the column sums, where the kernel finishes them, or null
-  uint32_t* arrived;     // groups > 1: a zero for every block of columns
+  void* sums;            // the column sums themselves (one group), or null
   int64_t lddy, ldp, lddz;
   int64_t rows;
   int n;
@@ -259,6 +261,28 @@ struct ColSumArgs {
   void* out1;
 };
 
+// One block's 64 columns of column sums: its waves take the partial rows in
+// turn, eight loads in flight each; then the waves' sums in order.  smem: 64
+// floats a wave.
+template <typename O> __device__ inline void col_sum_block(const ColSumArgs& a, unsigned block, int waves, float* smem) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t c = (int64_t)block * 64 + lane;
+  float s = 0.0f;
+  if (c < a.width) {
+    const float* p = a.part + c;
+#pragma unroll 8
+    for (int i = w; i < a.parts; i += waves) s += p[i * a.width];
+  }
+  smem[w * 64 + lane] = s;
+  __syncthreads();
+  if (w == 0 && c < a.width) {
+    s = 0.0f;
+    for (int i = 0; i < waves; i++) s += smem[i * 64 + lane];
+    O* out = c < a.n0 ? (O*)a.out0 : (O*)a.out1;
+    if (out) out[c < a.n0 ? c : c - a.n0] = (O)s;
+  }
+}
+
 // the kernels' launchers (dtype codes of the public header)
 hipError_t launch_norm_forward(int dtype, int wdtype, const NormArgs& a, hipStream_t st);
 hipError_t launch_norm_backward(int dtype, int wdtype, const NormArgs& a, hipStream_t st);
@@ -266,8 +290,6 @@ int norm_backward_groups(int64_t rows, int cols);
 hipError_t launch_col_sum(int out_dtype, const ColSumArgs& a, hipStream_t st);
 hipError_t launch_dz(int dtype, const DzArgs& a, hipStream_t st);
 int dz_groups(int dtype, int64_t rows, int64_t n);
-// Whether the dz kernel can finish the column sums itself.
-bool dz_finishes(int dtype, int64_t n, int groups);
 // Counters at the start of every workspace, zero between calls.
 constexpr int kCounters = 4096;
 // Chooses the kernel, the split of k and the copies from sizes, strides and
@@ -277,8 +299,10 @@ GemmPlan plan_gemm(int dtype, int epi, const GemmArgs& a);
 hipError_t launch_gemm(int dtype, const GemmPlan& p, char* ws, uint32_t* counters, hipStream_t st);
 // dx and dweight in one launch (their workspaces apart), where both run the
 // same tile: a launch less, and the one fills what the other leaves idle.
-bool gradients_together(const GemmPlan& x, const GemmPlan& w);
-hipError_t launch_gradients(int dtype, const GemmPlan& x, const GemmPlan& w, char* ws_x, char* ws_w, hipStream_t st);
-hipError_t launch_pack(int dtype, const PackArgs& a, hipStream_t st);
+// plan_gradients() chooses so, and plans both.
+bool plan_gradients(int dtype, const GemmArgs& x, const GemmArgs& w, GemmPlan* px, GemmPlan* pw);
+// `sums`: column sums that the launch adds up beside them (no columns: none).
+hipError_t launch_gradients(int dtype, const GemmPlan& x, const GemmPlan& w, const ColSumArgs& sums, char* ws_x, char* ws_w, hipStream_t st);
+hipError_t launch_pack(int dtype, PackArgs a, hipStream_t st);
 
 }  // namespace ringar

@@ -59,13 +59,11 @@ template <typename T, bool GATED, int V> __global__ __launch_bounds__(256) void 
     }
   }
   if (!a.part && !a.sums) return;
-  // Column sums: the waves' through LDS, then the blocks' rows of parts, added
-  // in order by the last block of these columns to arrive (or, where there
-  // are many, by a pass of their own).
+  // Column sums: the waves' through LDS, then the block's row of parts; added
+  // by the launch that follows (or final, where one block has all rows).
   constexpr int kSides = GATED ? 2 : 1;
   __shared__ float smem[4][64 * V];
   const int64_t cols = kSides * (int64_t)a.n, first = (int64_t)blockIdx.x * 64 * V;
-  T* out = (T*)a.sums;
 #pragma unroll
   for (int which = 0; which < kSides; which++) {
     if (which) __syncthreads();
@@ -76,29 +74,10 @@ template <typename T, bool GATED, int V> __global__ __launch_bounds__(256) void 
     for (int i = threadIdx.x; i < 64 * V; i += 256) {
       if (first + i >= a.n) continue;
       const float sum = (smem[0][i] + smem[1][i]) + (smem[2][i] + smem[3][i]);
-      if (out && a.groups == 1) out[(which ? a.n : 0) + first + i] = (T)sum;
-      else put_part(a.part + blockIdx.y * cols + (which ? a.n : 0) + first + i, sum);
+      const int64_t at = (which ? a.n : 0) + first + i;
+      if (a.sums) ((T*)a.sums)[at] = (T)sum;
+      else a.part[blockIdx.y * cols + at] = sum;
     }
-  }
-  if (!out || a.groups == 1 || !last_to_arrive(a.arrived + blockIdx.x, a.groups)) return;
-  // a thread's columns side by side, so that their loads are in flight together
-  constexpr int kMine = (64 * V + 255) / 256;
-  float sum[kSides * kMine];
-  int64_t at[kSides * kMine];
-#pragma unroll
-  for (int c = 0; c < kSides * kMine; c++) {
-    const int64_t col = first + threadIdx.x + c % kMine * 256;
-    at[c] = (c < kMine ? 0 : a.n) + (col < a.n ? col : a.n - 1);
-    sum[c] = 0.0f;
-  }
-#pragma unroll 8
-  for (int g = 0; g < a.groups; g++)
-#pragma unroll
-    for (int c = 0; c < kSides * kMine; c++) sum[c] += get_part(a.part + g * cols + at[c]);
-#pragma unroll
-  for (int c = 0; c < kSides * kMine; c++) {
-    const int i = threadIdx.x + c % kMine * 256;
-    if (i < 64 * V && first + i < a.n) out[at[c]] = (T)sum[c];
   }
 }
 
@@ -116,9 +95,11 @@ template <typename T> hipError_t launch(const DzArgs& a, hipStream_t st) {
 
 // A copy with rows padded to 128 bytes (zeros), for loads that need them to
 // start at 16-byte boundaries.
-template <typename T, int V> __global__ __launch_bounds__(256) void pack_rows(PackArgs a) {
+template <typename T, int V> __global__ __launch_bounds__(256) void pack_rows(PackArgs both) {
+  const bool second = blockIdx.x >= both.one[0].blocks;
+  const PackArgs::One& a = both.one[second];
   const int64_t per_row = a.ld_to / V;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t i = (int64_t)(blockIdx.x - (second ? both.one[0].blocks : 0)) * 256 + threadIdx.x;
   const int64_t row = i / per_row;
   if (row >= a.rows) return;
   const int64_t c = i % per_row * V;
@@ -133,35 +114,32 @@ template <typename T, int V> __global__ __launch_bounds__(256) void pack_rows(Pa
   store_pack<T, V>((T*)a.to + row * a.ld_to + c, v);
 }
 
-template <typename T> hipError_t pack(const PackArgs& a, hipStream_t st) {
+template <typename T> hipError_t pack(PackArgs& a, hipStream_t st) {
   constexpr int V = 16 / sizeof(T);
-  const int64_t blocks = (a.rows * (a.ld_to / V) + 255) / 256;
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  if (blocks) hipLaunchKernelGGL((pack_rows<T, V>), dim3((unsigned)blocks), dim3(256), 0, st, a);
+  int64_t total = 0;
+  for (PackArgs::One& o : a.one) {
+    const int64_t blocks = (o.rows * (o.ld_to / V) + 255) / 256;
+    total += blocks;
+    if (total > 0x7fffffff) return hipErrorInvalidValue;
+    o.blocks = (unsigned)blocks;
+  }
+  if (total) hipLaunchKernelGGL((pack_rows<T, V>), dim3((unsigned)total), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 // Row groups: enough blocks to fill the GPU (about 2048 with the column
-// groups), four rows a wave or more.
-static int64_t column_blocks(int dtype, int64_t n) {
-  const int64_t v = dtype == kF32 ? 4 : 8, each = 64 * (n < v ? 1 : v);
-  return (n + each - 1) / each;
-}
-
+// groups); a few rows stay in one, whose sums are then final.
 int dz_groups(int dtype, int64_t rows, int64_t n) {
-  int64_t g = 2048 / column_blocks(dtype, n);
-  const int64_t most = (rows + 15) / 16;
+  const int64_t v = dtype == kF32 ? 4 : 8, each = 64 * (n < v ? 1 : v);
+  int64_t g = 2048 / ((n + each - 1) / each);
+  const int64_t most = rows <= 8 ? 1 : (rows + 3) / 4;
   if (g > most) g = most;
   return (int)(g < 1 ? 1 : g);
 }
 
-// Up to 32 parts a column, which a last block adds in about 2 us (a launch
-// for it costs more); 100 would take it longer than col_sum's whole grid.
-bool dz_finishes(int dtype, int64_t n, int groups) { return groups == 1 || (groups <= 32 && column_blocks(dtype, n) <= kCounters); }
-
-hipError_t launch_pack(int dtype, const PackArgs& a, hipStream_t st) {
+hipError_t launch_pack(int dtype, PackArgs a, hipStream_t st) {
   if (dtype == kF32) return pack<float>(a, st);
   if (dtype == kF16) return pack<_Float16>(a, st);
   return pack<__bf16>(a, st);

@@ -6,9 +6,9 @@ namespace ringar {
 hipError_t launch_gemm_f16(int epi, const GemmArgs& a, hipStream_t st);
 hipError_t launch_gemm_bf16(int epi, const GemmArgs& a, hipStream_t st);
 hipError_t launch_gemm_f32(int epi, const GemmArgs& a, hipStream_t st);
-hipError_t launch_gradients_f16(const GemmArgs& x, const GemmArgs& w, hipStream_t st);
-hipError_t launch_gradients_bf16(const GemmArgs& x, const GemmArgs& w, hipStream_t st);
-hipError_t launch_gradients_f32(const GemmArgs& x, const GemmArgs& w, hipStream_t st);
+hipError_t launch_gradients_f16(const GemmArgs& x, const GemmArgs& w, const ColSumArgs& sums, hipStream_t st);
+hipError_t launch_gradients_bf16(const GemmArgs& x, const GemmArgs& w, const ColSumArgs& sums, hipStream_t st);
+hipError_t launch_gradients_f32(const GemmArgs& x, const GemmArgs& w, const ColSumArgs& sums, hipStream_t st);
 
 namespace {
 
@@ -60,7 +60,7 @@ Cost cost_of(int variant, int epi, int es, bool arow, bool brow) {
     case kTile256: return {6, 1.43, 1.43};
     case kTile128: return {2.6, 0.6, 0.55};
     case kTile64: return epi == kEpiGated ? Cost{2.6, 0.31, 0.29} : arow ? Cost{2.6, 0.24, 0.18} : Cost{2.6, 0.25, 0.23};
-    default: return epi == kEpiGated ? Cost{2, 0.7, 0.5} : brow ? Cost{2, 0.5, 0.3} : Cost{2, 0.7, 0.5};
+    default: return epi == kEpiGated ? Cost{2, 1.0, 0.6} : brow ? Cost{2, 0.95, 0.45} : Cost{2, 0.95, 0.6};
   }
 }
 
@@ -83,12 +83,15 @@ Choice cheapest(int variant, int epi, int es, const GemmArgs& a) {
   const Cost c = cost_of(variant, epi, es, a.sak == 1, a.sbk == 1);
   const int64_t tiles = tiles_of(variant, epi, a), steps = ceil_div(a.k, 128 / es);
   const double outputs = (double)a.m * a.n * (epi == kEpiGated ? 2 : 1);
+  // what comes from memory at 5 TB/s at best
+  const double memory = ((double)a.m * a.k + (double)a.k * a.n * (epi == kEpiGated ? 2 : 1) + (double)a.m * a.n) * es / 5e6;
   Choice best = {variant, 1, 0};
   for (int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
     if (s > 1 && steps < 2 * s) break;
     const int64_t per = ceil_div(steps, s);
     const double at_once = c.shared * (double)ceil_div(tiles * s, 256);
-    double us = c.start + (per + 1.5) * (at_once > c.alone ? at_once : c.alone) + (s > 1 ? 4.5 + outputs * s * 8 / 8e6 : 0);
+    double us = (per + 1.5) * (at_once > c.alone ? at_once : c.alone);
+    us = c.start + (us > memory ? us : memory) + (s > 1 ? 4.5 + outputs * s * 8 / 8e6 : 0);
     if (tail_of(variant, s, tiles)) us += (per + 1.5) * (cost_of(kTile128, epi, es, true, true).alone - c.shared);
     if (s == 1 || us < best.us) best = {variant, s, us};
   }
@@ -97,7 +100,8 @@ Choice cheapest(int variant, int epi, int es, const GemmArgs& a) {
 
 }  // namespace
 
-GemmPlan plan_gemm(int dtype, int epi, const GemmArgs& given) {
+// `only`: the one tiled kernel to consider, or -1.
+static GemmPlan plan_tiles(int dtype, int epi, const GemmArgs& given, int only, Choice* chosen) {
   GemmPlan p = {};
   p.epi = epi;
   p.args = given;
@@ -133,25 +137,27 @@ GemmPlan plan_gemm(int dtype, int epi, const GemmArgs& given) {
   const int64_t pad = 128 / es;
   p.packed_a = ceil_div(cols_a, pad) * pad;
   p.packed_b = ceil_div(cols_b, pad) * pad;
-  auto copy_us = [&](int64_t rows, int64_t pitch) { return 3 + (double)rows * pitch * es * 2 / 4.5e6; };
-  Choice best = cheapest(kTile64, epi, es, a);
+  auto copy_us = [&](int64_t rows, int64_t pitch) { return (double)rows * pitch * es * 2 / 4.5e6; };
+  Choice best = cheapest(only < 0 ? kTile64 : only, epi, es, a);
   for (int v : {kTile128, kTile256}) {
-    if (v == kTile256 && es == 4) continue;
+    if (only >= 0 || (v == kTile256 && es == 4)) continue;
     const Choice c = cheapest(v, epi, es, a);
     if (c.us < best.us) best = c;
   }
   if (!ok_a || !ok_b) {
-    const double copies = (ok_a ? 0 : copy_us(rows_a, p.packed_a)) + (ok_b ? 0 : copy_us(rows_b, p.packed_b));
+    const double copies = 3.5 + (ok_a ? 0 : copy_us(rows_a, p.packed_a)) + (ok_b ? 0 : copy_us(rows_b, p.packed_b));
     const bool fits = ((arow ? 256 : 64) * p.packed_a + 64) * es < (1ll << 32) - 4096 &&
                       ((brow ? 256 + (epi == kEpiGated ? a.n : 0) : 64) * p.packed_b + 64) * es < (1ll << 32) - 4096;
     const Choice staged = cheapest(kStaged64, epi, es, a);
-    if (fits && best.us + copies < staged.us) {
+    best.us += copies;
+    if (fits && best.us < staged.us) {
       p.pack_a = !ok_a;
       p.pack_b = !ok_b;
     } else {
       best = staged;
     }
   }
+  *chosen = best;
   a.variant = best.variant;
   const int64_t step = 128 / es, steps = ceil_div(a.k, step), per = ceil_div(steps, best.splits);
   a.k_per_split = (int)(per * step < a.k ? per * step : a.k);
@@ -170,6 +176,41 @@ GemmPlan plan_gemm(int dtype, int epi, const GemmArgs& given) {
   return p;
 }
 
+GemmPlan plan_gemm(int dtype, int epi, const GemmArgs& a) {
+  Choice c = {};
+  return plan_tiles(dtype, epi, a, -1, &c);
+}
+
+bool plan_gradients(int dtype, const GemmArgs& x, const GemmArgs& w, GemmPlan* px, GemmPlan* pw) {
+  Choice cx = {}, cw = {};
+  *px = plan_tiles(dtype, kEpiStore, x, -1, &cx);
+  *pw = plan_tiles(dtype, kEpiStore, w, -1, &cw);
+  if (!x.m || !x.n || !w.m || !w.n || px->too_many || pw->too_many) return false;
+  const int es = dtype == kF32 ? 4 : 2;
+  double best = cx.us + cw.us;
+  bool together = false;
+  for (int v : {kTile64, kTile128}) {
+    Choice tx = {}, tw = {};
+    const GemmPlan qx = plan_tiles(dtype, kEpiStore, x, v, &tx), qw = plan_tiles(dtype, kEpiStore, w, v, &tw);
+    if (qx.args.variant != v || qw.args.variant != v || qx.too_many || qw.too_many) continue;
+    // The blocks share the CUs: the longer product's time alone, or all their
+    // steps at the CU's throughput; a start and a launch less.
+    const Cost c = cost_of(v, kEpiStore, es, true, false);
+    auto steps = [&](const GemmArgs& a) { return (double)a.tile_count * a.splits * (a.k_per_split / (128.0 / es) + 1.5); };
+    const double shared = c.start + (steps(qx.args) + steps(qw.args)) * c.shared / 256;
+    const double alone = tx.us > tw.us ? tx.us : tw.us;
+    const double joins = (qx.args.splits > 1 ? 4.5 : 0) + (qw.args.splits > 1 ? 4.5 : 0) + (qx.pack_a || qx.pack_b ? 3.5 : 0) +
+                         (qw.pack_a || qw.pack_b ? 3.5 : 0);
+    const double us = (shared > alone ? shared : alone) + (shared > alone ? joins : 0);
+    if (us >= best) continue;
+    best = us;
+    *px = qx;
+    *pw = qw;
+    together = true;
+  }
+  return together;
+}
+
 // The planned product's arguments with its workspace in place and its copies
 // enqueued.
 static hipError_t prepare(int dtype, const GemmPlan& p, char* ws, uint32_t* counters, hipStream_t st, GemmArgs* out) {
@@ -184,16 +225,21 @@ static hipError_t prepare(int dtype, const GemmPlan& p, char* ws, uint32_t* coun
   a.part = (float*)ws;
   a.arrived = counters;
   if (a.variant != kRows && a.splits > 1) a.part = (float*)part((size_t)a.splits * a.m * wide * 4);
+  PackArgs packs = {};
+  int count = 0;
   auto pack = [&](const void** from, int64_t* pitch, int64_t packed, int64_t rows, int64_t cols) {
     void* to = part((size_t)rows * packed * es);
-    const hipError_t e = launch_pack(dtype, {*from, to, *pitch, packed, rows, (int)cols}, st);
+    packs.one[count++] = {*from, to, *pitch, packed, rows, (int)cols, 0};
     *from = to;
     *pitch = packed;
-    return e;
   };
-  hipError_t e = hipSuccess;
-  if (p.pack_a) e = a.sak == 1 ? pack(&a.a, &a.sam, p.packed_a, a.m, a.k) : pack(&a.a, &a.sak, p.packed_a, a.k, a.m);
-  if (e == hipSuccess && p.pack_b) e = a.sbk == 1 ? pack(&a.b, &a.sbn, p.packed_b, wide, a.k) : pack(&a.b, &a.sbk, p.packed_b, a.k, wide);
+  if (p.pack_a) a.sak == 1 ? pack(&a.a, &a.sam, p.packed_a, a.m, a.k) : pack(&a.a, &a.sak, p.packed_a, a.k, a.m);
+  if (p.pack_b) a.sbk == 1 ? pack(&a.b, &a.sbn, p.packed_b, wide, a.k) : pack(&a.b, &a.sbk, p.packed_b, a.k, wide);
+  if (count == 1) {                  // no second copy: one without rows
+    packs.one[1] = packs.one[0];
+    packs.one[1].rows = 0;
+  }
+  const hipError_t e = count ? launch_pack(dtype, packs, st) : hipSuccess;
   *out = a;
   return e;
 }
@@ -208,20 +254,14 @@ hipError_t launch_gemm(int dtype, const GemmPlan& p, char* ws, uint32_t* counter
   return launch_gemm_f32(p.epi, a, st);
 }
 
-bool gradients_together(const GemmPlan& x, const GemmPlan& w) {
-  const int v = x.args.variant;
-  return x.args.m && x.args.n && w.args.m && w.args.n && v == w.args.variant && (v == kTile64 || v == kTile128) &&
-         (int64_t)x.args.tile_count * x.args.splits + (int64_t)w.args.tile_count * w.args.splits < 0x7fffffff;
-}
-
-hipError_t launch_gradients(int dtype, const GemmPlan& x, const GemmPlan& w, char* ws_x, char* ws_w, hipStream_t st) {
+hipError_t launch_gradients(int dtype, const GemmPlan& x, const GemmPlan& w, const ColSumArgs& sums, char* ws_x, char* ws_w, hipStream_t st) {
   GemmArgs ax, aw;
   hipError_t e = prepare(dtype, x, ws_x, nullptr, st, &ax);
   if (e == hipSuccess) e = prepare(dtype, w, ws_w, nullptr, st, &aw);
   if (e != hipSuccess) return e;
-  if (dtype == kF16) return launch_gradients_f16(ax, aw, st);
-  if (dtype == kBF16) return launch_gradients_bf16(ax, aw, st);
-  return launch_gradients_f32(ax, aw, st);
+  if (dtype == kF16) return launch_gradients_f16(ax, aw, sums, st);
+  if (dtype == kBF16) return launch_gradients_bf16(ax, aw, sums, st);
+  return launch_gradients_f32(ax, aw, sums, st);
 }
 
 }  // namespace ringar

@@ -49,15 +49,16 @@ template <typename T, bool AROW, bool BROW, int EPI> hipError_t launch_tiled(con
 }
 
 // dx and dweight together: both of kTile128 or both of kTile64.
-template <typename T> hipError_t launch_gradients(const GemmArgs& x, const GemmArgs& w, hipStream_t st) {
+template <typename T> hipError_t launch_gradients(const GemmArgs& x, const GemmArgs& w, const ColSumArgs& sums, hipStream_t st) {
+  const unsigned bs = (unsigned)((sums.width + 63) / 64);
   using X = Kernels<T, true, false, kEpiStore>;
   using W = Kernels<T, false, false, kEpiStore>;
   if (x.variant == kTile128) {
     const unsigned bx = blocks_of(x), bw = blocks_of(w);
-    hipLaunchKernelGGL((gemm_pair<typename X::Middle, typename W::Middle, 4>), dim3(bx + bw), dim3(512), 0, st, x, w, bx);
+    hipLaunchKernelGGL((gemm_gradients<T, typename X::Middle, typename W::Middle, 4>), dim3(bx + bw + bs), dim3(512), 0, st, x, w, sums, bx, bw);
   } else {
     const unsigned bx = blocks_of(x), bw = blocks_of(w);
-    hipLaunchKernelGGL((gemm_pair<typename X::Small, typename W::Small, 2>), dim3(bx + bw), dim3(256), 0, st, x, w, bx);
+    hipLaunchKernelGGL((gemm_gradients<T, typename X::Small, typename W::Small, 2>), dim3(bx + bw + bs), dim3(256), 0, st, x, w, sums, bx, bw);
   }
   return hipGetLastError();
 }

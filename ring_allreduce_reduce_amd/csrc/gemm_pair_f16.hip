@@ -2,8 +2,8 @@
 #include "gemm_launch.h"
 
 namespace ringar {
-hipError_t launch_gradients_f16(const GemmArgs& x, const GemmArgs& w, hipStream_t st) {
-  hipError_t e = launch_gradients<_Float16>(x, w, st);
+hipError_t launch_gradients_f16(const GemmArgs& x, const GemmArgs& w, const ColSumArgs& sums, hipStream_t st) {
+  hipError_t e = launch_gradients<_Float16>(x, w, sums, st);
   if (e == hipSuccess) e = join<_Float16, kEpiStore>(x, st);
   return e == hipSuccess ? join<_Float16, kEpiStore>(w, st) : e;
 }

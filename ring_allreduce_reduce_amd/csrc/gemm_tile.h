@@ -298,7 +298,8 @@ struct GemmTile {
   using OB = std::conditional_t<DIRECT, Operand<T, BROW, BN, NW>, StagedOperand<T, BROW, BN, NW>>;
   static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   static constexpr int kBK = OA::kBK;
-  static_assert(TN == 64 || (TN == 32 && EPI != kEpiGated), "eight or four lanes finish a wave's row");
+  static_assert(TN == 64 || (TN == 32 && EPI != kEpiGated), "four or eight lanes finish a wave's row");
+  static constexpr int kHalf = TN / 2;         // gated: a wave's columns are half gate, half up
   static_assert(BROW || EPI == kEpiStore, "epilogues with columns of their own read weights by rows");
   static constexpr int kStage = OA::kBytes + OB::kBytes;
   // epilogue: a wave's rows in fp32, shifted 16 bytes over the banks
@@ -343,9 +344,9 @@ __device__ inline void GemmTile<T, AROW, BROW, EPI, BM, BN, WM, WN, DIRECT, STAG
     auto row_a = [&](int r) { return m0 + r < a.m ? (int64_t)r : a.m - 1 - m0; };
     auto row_b = [&](int r) -> int64_t {
       if constexpr (EPI == kEpiGated) {
-        // 64 rows: 32 of the gate, then the same 32 of the up projection
-        const int64_t c = (r >> 6) * 32 + (r & 31);
-        return (n0 + c < a.n ? c : a.n - 1 - n0) + (r & 32 ? a.n : 0);
+        // a wave's rows: first of the gate, then the same ones of the up projection
+        const int64_t c = r / TN * kHalf + r % kHalf;
+        return (n0 + c < a.n ? c : a.n - 1 - n0) + (r % TN >= kHalf ? a.n : 0);
       } else {
         return n0 + r < a.n ? r : a.n - 1 - n0;
       }
@@ -450,15 +451,20 @@ __device__ inline void GemmTile<T, AROW, BROW, EPI, BM, BN, WM, WN, DIRECT, STAG
     constexpr std::false_type kNoLoads;
     constexpr std::true_type kLoads;
     Frag fa0[FM], fb0[FN], fa1[FM], fb1[FN];
-    // STAGES - 1 steps are on their way before the first is used
-    issue(0);
-    commit(0);
-    if (STAGES == 3 && steps > 1) {
-      issue(1);
-      wait_loads<STAGES == 3 ? kStepLoads : 0>();
-    } else {
-      wait_loads<>();
+    // STAGES - 1 steps are on their way before the first is used (four, and
+    // one block a CU less, were slower: 1866 x 320 x 3200 fp16 gradients 21.0
+    // us, not 20.2).  Waits until only the last `ahead` steps' loads are outstanding
+    auto wait_all_but = [&](int ahead) {
+      if (STAGES == 3 && ahead == 1) wait_loads<STAGES == 3 ? kStepLoads : 0>();
+      else wait_loads<>();
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; i++) {
+      if (i >= steps) break;
+      issue(i);
+      commit(i);
     }
+    wait_all_but(steps - 1 < STAGES - 2 ? steps - 1 : STAGES - 2);
     barrier();
     fix_tail(0);
     if (STAGES - 1 < steps) issue(STAGES - 1);
@@ -468,9 +474,8 @@ __device__ inline void GemmTile<T, AROW, BROW, EPI, BM, BN, WM, WN, DIRECT, STAG
     auto first_half = [&](int s) {
       half(kNoLoads, fa0, fb0, now, 1, fa1, fb1, 0);
       commit(next);                   // its readers of step s - 1 passed the last barrier
-      // step s + 1 has landed; with three buffers step s + 2 may still be on its way
-      if (STAGES == 3 && s + 2 < steps) wait_loads<STAGES == 3 ? kStepLoads : 0>();
-      else wait_loads<>();
+      // step s + 1 has landed; with more buffers the steps after it may still be on their way
+      wait_all_but(steps - 2 - s < STAGES - 2 ? steps - 2 - s : STAGES - 2);
       barrier();
     };
     int s = 0;
@@ -525,8 +530,8 @@ __device__ inline void GemmTile<T, AROW, BROW, EPI, BM, BN, WM, WN, DIRECT, STAG
         *(f32x4*)(v + 4) = *(const f32x4*)(from + 4);
         if constexpr (EPI == kEpiGated) {
           float u[8];
-          *(f32x4*)u = *(const f32x4*)(from + 32);
-          *(f32x4*)(u + 4) = *(const f32x4*)(from + 36);
+          *(f32x4*)u = *(const f32x4*)(from + kHalf);
+          *(f32x4*)(u + 4) = *(const f32x4*)(from + kHalf + 4);
           if (a.splits > 1) {
             put8<float>(part, c, v);
             put8<float>(part, a.n + c, u);
@@ -544,9 +549,9 @@ __device__ inline void GemmTile<T, AROW, BROW, EPI, BM, BN, WM, WN, DIRECT, STAG
           if constexpr (EPI == kEpiGated) {
             if (a.splits > 1) {
               part[c + i] = from[i];
-              part[a.n + c + i] = from[32 + i];
+              part[a.n + c + i] = from[kHalf + i];
             } else {
-              finish_gated<T>(a, m, (int)(c + i), from[i], from[32 + i]);
+              finish_gated<T>(a, m, (int)(c + i), from[i], from[kHalf + i]);
             }
           } else {
             if (a.splits > 1) part[c + i] = from[i];
@@ -572,6 +577,16 @@ template <typename K, typename L, int OCC> __global__ __launch_bounds__(K::kThre
   __shared__ __attribute__((aligned(1024))) char smem[K::kShared > L::kShared ? K::kShared : L::kShared];
   if (blockIdx.x < blocks) K::run(a, blockIdx.x, smem);
   else L::run(b, blockIdx.x - blocks, smem);
+}
+
+// Both gradient products, and the bias's column sums beside them.
+template <typename T, typename K, typename L, int OCC>
+__global__ __launch_bounds__(K::kThreads, OCC) void gemm_gradients(GemmArgs a, GemmArgs b, ColSumArgs sums, unsigned blocks_a, unsigned blocks_b) {
+  static_assert(K::kThreads == L::kThreads, "one block size");
+  __shared__ __attribute__((aligned(1024))) char smem[K::kShared > L::kShared ? K::kShared : L::kShared];
+  if (blockIdx.x < blocks_a) K::run(a, blockIdx.x, smem);
+  else if (blockIdx.x < blocks_a + blocks_b) L::run(b, blockIdx.x - blocks_a, smem);
+  else col_sum_block<T>(sums, blockIdx.x - blocks_a - blocks_b, K::kThreads / 64, (float*)smem);
 }
 
 }  // namespace ringar

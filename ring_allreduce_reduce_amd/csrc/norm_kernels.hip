@@ -318,28 +318,9 @@ template <typename T> __global__ __launch_bounds__(256) void norm_params_long(No
   a.part[((int64_t)blockIdx.y * 2 + 1) * a.cols + c] = db;
 }
 
-// Column sums of the partial rows: a block takes 64 columns, its 16 waves
-// every 16th row, eight loads in flight each; then the waves' sums in order.
 template <typename O> __global__ __launch_bounds__(1024) void col_sum(ColSumArgs a) {
-  constexpr int kStrips = 16;
-  __shared__ float smem[kStrips][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
-  float s = 0.0f;
-  if (c < a.width) {
-    const float* p = a.part + c;
-#pragma unroll 8
-    for (int i = w; i < a.parts; i += kStrips) s += p[i * a.width];
-  }
-  smem[w][lane] = s;
-  __syncthreads();
-  if (w == 0 && c < a.width) {
-    s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kStrips; i++) s += smem[i][lane];
-    O* out = c < a.n0 ? (O*)a.out0 : (O*)a.out1;
-    if (out) out[c < a.n0 ? c : c - a.n0] = (O)s;
-  }
+  __shared__ float smem[16 * 64];
+  col_sum_block<O>(a, blockIdx.x, 16, smem);
 }
 
 // Threads and elements per thread of a row: the smallest shape that holds it.
