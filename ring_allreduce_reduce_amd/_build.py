@@ -18,7 +18,7 @@ _TYPES = ("i8", "i32", "f16", "bf16", "f32", "f64")
 SOURCES = ([f"tree_{t}.hip" for t in _TYPES] + [f"ring_kernel_{t}.hip" for t in _TYPES] +
            [f"ring_rs_{t}.hip" for t in _TYPES] + [f"captured_{t}.hip" for t in _TYPES] +
            ["ring_ag.hip", "ring_launch.hip", "ringar.cpp"] +
-           ["norm_kernels.hip", "dz_kernels.hip", "gemm_dispatch.cpp", "block_ops.cpp"] +
+           ["norm_kernels.hip", "dz_kernels.hip", "few_kernels.hip", "gemm_dispatch.cpp", "block_ops.cpp"] +
            [f"gemm_{lay}_{t}.hip" for lay in ("nt", "nn", "tn", "pair") for t in ("f16", "bf16", "f32")])
 
 HIPCC_FLAGS = [

@@ -355,6 +355,36 @@ static ringar_result_t product_backward(const ringar_linear_backward_t* p, bool 
                   {"dx", p->dx, p->dx ? p->rows : 0, p->in_features, p->lddx, es, true},
                   {"dweight", p->dweight, p->dweight ? wide : 0, p->in_features, p->lddw, es, true},
                   VEC("dbias", p->dbias, wide, es, true)}));
+  if (few_rows(p->dtype, p->rows, wide, p->in_features)) {
+    if (!p->dx && !p->dweight && !p->dbias) return RINGAR_SUCCESS;
+    FewArgs f = {};
+    f.dy = p->dy;
+    f.pre = use_pre ? p->pre : nullptr;
+    f.x = p->x;
+    f.w = p->weight;
+    f.dx = p->dx;
+    f.dw = p->dweight;
+    f.db = p->dbias;
+    f.lddy = p->lddy;
+    f.ldp = p->ldp;
+    f.ldx = p->ldx;
+    f.ldw = p->ldw;
+    f.lddx = p->lddx;
+    f.lddw = p->lddw;
+    f.k = p->in_features;
+    f.rows = (int)p->rows;
+    f.n = (int)p->out_features;
+    f.wide = (int)wide;
+    f.act = p->act;
+    f.gated = gated;
+    const size_t part = plan_few(p->dtype, f);
+    std::lock_guard<std::mutex> lock(g_ws_mu);
+    char* ws = nullptr;
+    TRY(workspace(st, part, &ws));
+    f.part = (float*)ws;
+    HIP_TRY(launch_few(p->dtype, f, st));
+    return RINGAR_SUCCESS;
+  }
   // dz = dy where there is nothing to undo
   const bool need_dz = use_pre && (p->dx || p->dweight);
   DzArgs z = {};

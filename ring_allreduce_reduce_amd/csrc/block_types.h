@@ -261,6 +261,24 @@ struct ColSumArgs {
   void* out1;
 };
 
+// backward pass of a few rows (few_rows)
+struct FewArgs {
+  const void* dy;
+  const void* pre;       // or null
+  const void* x;
+  const void* w;
+  void* dx;              // or null
+  void* dw;              // or null
+  void* db;              // or null
+  float* part;           // parts > 1: [parts][rows][k] of dx
+  int64_t lddy, ldp, ldx, ldw, lddx, lddw, k;
+  int rows, n, wide;     // wide: n, gated 2n
+  int act;
+  int gated;
+  // plan_few
+  int n_each, parts, across_log;
+};
+
 // One block's 64 columns of column sums: its waves take the partial rows in
 // turn, eight loads in flight each; then the waves' sums in order.  smem: 64
 // floats a wave.
@@ -303,6 +321,9 @@ hipError_t launch_gemm(int dtype, const GemmPlan& p, char* ws, uint32_t* counter
 bool plan_gradients(int dtype, const GemmArgs& x, const GemmArgs& w, GemmPlan* px, GemmPlan* pw);
 // `sums`: column sums that the launch adds up beside them (no columns: none).
 hipError_t launch_gradients(int dtype, const GemmPlan& x, const GemmPlan& w, const ColSumArgs& sums, char* ws_x, char* ws_w, hipStream_t st);
+bool few_rows(int dtype, int64_t rows, int64_t wide, int64_t k);
+size_t plan_few(int dtype, FewArgs& a);       // returns the bytes of parts
+hipError_t launch_few(int dtype, const FewArgs& a, hipStream_t st);
 hipError_t launch_pack(int dtype, PackArgs a, hipStream_t st);
 
 }  // namespace ringar

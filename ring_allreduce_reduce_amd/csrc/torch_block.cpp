@@ -136,7 +136,10 @@ PyObject* tuple(std::initializer_list<PyObject*> v) {
   return r;
 }
 
-bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+bool truth(PyObject* o, const char* what) {
+  if (o != Py_True && o != Py_False) bad(std::string(what) + " must be True or False");
+  return o == Py_True;
+}
 void* ptr(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
 PyObject* layer_norm(PyObject* const* v) {
@@ -144,7 +147,7 @@ PyObject* layer_norm(PyObject* const* v) {
   const at::Tensor *weight = tensor(v[1], "weight"), *bias = tensor(v[2], "bias"), *out = tensor(v[5], "out");
   const double eps = PyFloat_AsDouble(v[3]);
   if (eps == -1.0 && PyErr_Occurred()) return nullptr;
-  const bool stats = truth(v[4]);
+  const bool stats = truth(v[4], "stats");
   Call call(x, "x");
   const Rows rx(x, "x", call);
   const at::ScalarType ptype = weight ? weight->scalar_type() : bias ? bias->scalar_type() : call.type;
@@ -205,9 +208,9 @@ PyObject* layer_norm_backward(PyObject* const* v) {
   a.rstd = (const float*)rstd.data_ptr();
   a.weight = vec(weight, rx.cols, "weight", ptype, call);
   at::Tensor gx, gw, gb;
-  if (truth(v[5])) gx = call.make(x.sizes());
-  if (truth(v[6])) gw = call.make({rx.cols}, ptype);
-  if (truth(v[7])) gb = call.make({rx.cols}, ptype);
+  if (truth(v[5], "dx")) gx = call.make(x.sizes());
+  if (truth(v[6], "dweight")) gw = call.make({rx.cols}, ptype);
+  if (truth(v[7], "dbias")) gb = call.make({rx.cols}, ptype);
   a.dx = ptr(gx);
   a.lddx = rx.cols;
   a.dweight = ptr(gw);
@@ -219,7 +222,7 @@ PyObject* layer_norm_backward(PyObject* const* v) {
 PyObject* forward(PyObject* const* v) {
   const at::Tensor &x = needed(v[0], "x"), &weight = needed(v[1], "weight");
   const at::Tensor *bias = tensor(v[2], "bias"), *residual = tensor(v[4], "residual"), *out = tensor(v[6], "out");
-  const bool save_pre = truth(v[5]), gated = truth(v[7]);
+  const bool save_pre = truth(v[5], "save_pre"), gated = truth(v[7], "gated");
   Call call(x, "x");
   const Rows rx(x, "x", call), rw(weight, "weight", call);
   if (rw.cols != rx.cols || weight.dim() != 2 || (gated && rw.rows % 2))
@@ -268,7 +271,7 @@ PyObject* forward(PyObject* const* v) {
 PyObject* backward(PyObject* const* v) {
   const at::Tensor& dy = needed(v[0], "dy");
   const at::Tensor *x = tensor(v[1], "x"), *weight = tensor(v[2], "weight"), *pre = tensor(v[3], "pre");
-  const bool want_x = truth(v[5]), want_w = truth(v[6]), want_b = truth(v[7]), gated = truth(v[8]);
+  const bool want_x = truth(v[5], "dx"), want_w = truth(v[6], "dweight"), want_b = truth(v[7], "dbias"), gated = truth(v[8], "gated");
   Call call(dy, "dy");
   const Rows rdy(dy, "dy", call);
   const int64_t n = rdy.cols, wide = gated ? 2 * n : n;

@@ -247,6 +247,35 @@ def test_products_strided_in_nan(rows, k, n, dtype, gated):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("rows,k,n", [(1, 1031, 1024), (2, 9, 120000), (3, 130000, 9), (4, 2056, 1030), (5, 1024, 1100), (8, 100, 10490),
+                                      (9, 1040, 1040)])
+def test_few_rows_backward(rows, k, n, gated, dtype):
+    """The gradients of a few rows through a weight of a million values."""
+    g = _gen("few", rows, k, n, gated, dtype)
+    wide = 2 * n if gated else n
+    act = "gelu" if rows % 2 else "silu"
+    back = ra.gated_ffn_backward if gated else ra.linear_backward
+    dy, x, w, pre = _rand(g, (rows, n), dtype), _rand(g, (rows, k), dtype), _rand(g, (wide, k), dtype, wide ** -0.5), _rand(g, (rows, wide), dtype)
+    for place in (lambda t: t, lambda t: _inside(t, pad=5, shift=3)):
+        dy1, x1, w1, pre1 = place(dy), place(x), place(w), place(pre)
+        grads = back(dy1, x1, w1, pre1, act=act)
+        want, bound = R.backward(dy, x, w, pre, act, gated)
+        for a, c, e, what in zip(grads, want, bound, ("dx", "dweight", "dbias")):
+            R.assert_within(a, c, e, what)
+        for which in range(3):
+            names = ("dx", "dweight", "dbias")
+            one = back(dy1, x1, w1, pre1, act=act, **{v: False for v in names if v != names[which]})
+            assert sum(v is not None for v in one) == 1
+            R.assert_within(one[which], want[which], bound[which], names[which] + " alone")
+    if not gated:
+        grads = back(dy, x, w)                      # no activation
+        want, bound = R.backward(dy, x, w, None, "none", False)
+        for a, c, e, what in zip(grads, want, bound, ("dx", "dweight", "dbias")):
+            R.assert_within(a, c, e, what)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_linear_broadcast_rows_and_residual_in_place(dtype):
     g = _gen("broadcast", dtype)
     x1, w, r1 = _rand(g, (1, 136), dtype), _rand(g, (72, 136), dtype, 0.1), _rand(g, (1, 72), dtype)
@@ -510,3 +539,11 @@ def test_gradients_against_differences(op):
         slack = float((bound[i].reshape(step.shape) * step.abs()).sum())
         # pre and the statistics are fp32 roundings of the pass's own: their effect is within twice the bounds
         assert abs(got - along) <= abs(plain - along64) + noise + 2 * slack, (op, i, got, along, plain, along64)
+
+
+def test_flags_must_be_flags():
+    x, w = torch.ones(2, 8, device="cuda"), torch.ones(4, 8, device="cuda")
+    for call in (lambda: ra.linear_backward(torch.ones(2, 4, device="cuda"), x, w, dx=x), lambda: ra.layer_norm(x, stats=x),
+                 lambda: ra.linear(x, w, save_pre=1)):
+        with pytest.raises(ra.RingarError, match="must be True or False"):
+            call()
