@@ -287,13 +287,17 @@ static ringar_result_t norm_backward(const ringar_layer_norm_backward_t* p, ring
   a.inv_cols = 1.0f / (float)p->cols;
   a.groups = norm_backward_groups(p->rows, a.cols);
   std::lock_guard<std::mutex> lock(g_ws_mu);
-  if (params) {
+  const bool split = params && (a.groups != 1 || p->cols > kNormLongest);
+  if (split) {
     char* ws_p = nullptr;
     TRY(workspace(st, (size_t)2 * a.groups * p->cols * 4, &ws_p));
     a.part = (float*)ws_p;
+  } else {
+    a.dweight = p->dweight;
+    a.dbias = p->dbias;
   }
   if (p->rows) HIP_TRY(launch_norm_backward(p->dtype, p->param_dtype, a, st));
-  if (params)
+  if (split)
     HIP_TRY(launch_col_sum(p->param_dtype, {a.part, a.groups, 2 * p->cols, p->cols, p->dweight, p->dbias}, st));
   return RINGAR_SUCCESS;
 }

@@ -166,6 +166,8 @@ struct NormArgs {
   float* mean;           // forward: may be null; backward: inputs
   float* rstd;
   float* part;           // backward: partial sums [groups][dweight, dbias], or null
+  void* dweight;         // backward, without part: the sums of the one block, or null
+  void* dbias;
   int64_t ldx, lddy, ldy;
   int64_t rows;
   int cols;
@@ -304,6 +306,7 @@ template <typename O> __device__ inline void col_sum_block(const ColSumArgs& a, 
 // the kernels' launchers (dtype codes of the public header)
 hipError_t launch_norm_forward(int dtype, int wdtype, const NormArgs& a, hipStream_t st);
 hipError_t launch_norm_backward(int dtype, int wdtype, const NormArgs& a, hipStream_t st);
+constexpr int kNormLongest = 16384;            // columns of the rows that registers hold
 int norm_backward_groups(int64_t rows, int cols);
 hipError_t launch_col_sum(int out_dtype, const ColSumArgs& a, hipStream_t st);
 hipError_t launch_dz(int dtype, const DzArgs& a, hipStream_t st);

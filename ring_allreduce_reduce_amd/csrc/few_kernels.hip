@@ -130,12 +130,23 @@ template <typename T, int V, int M> __global__ __launch_bounds__(256) void few_b
   }
 }
 
-template <typename T> __global__ __launch_bounds__(256) void few_join(FewArgs a) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (int64_t)a.rows * a.k) return;
+// 64 values of dx a block; its waves take the parts in turn (one thread for
+// all 412 parts of 4 x 117: 11 us), then the waves' sums in order.
+template <typename T> __global__ __launch_bounds__(1024) void few_join(FewArgs a) {
+  __shared__ float lds[16][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t width = (int64_t)a.rows * a.k, i = (int64_t)blockIdx.x * 64 + lane;
   float s = 0.0f;
+  if (i < width) {
 #pragma unroll 8
-  for (int p = 0; p < a.parts; p++) s += a.part[p * (int64_t)a.rows * a.k + i];
+    for (int p = w; p < a.parts; p += 16) s += a.part[p * width + i];
+  }
+  lds[w][lane] = s;
+  __syncthreads();
+  if (w || i >= width) return;
+  s = 0.0f;
+#pragma unroll
+  for (int p = 0; p < 16; p++) s += lds[p][lane];
   ((T*)a.dx)[i / a.k * a.lddx + i % a.k] = (T)s;
 }
 
@@ -144,20 +155,20 @@ template <typename T, int V, int M> hipError_t launch(const FewArgs& a, hipStrea
   hipLaunchKernelGGL((few_backward<T, V, M>), dim3((unsigned)((packs + (1 << a.across_log) - 1) >> a.across_log), a.parts), dim3(256), 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.dx || a.parts == 1) return e;
-  hipLaunchKernelGGL(few_join<T>, dim3((unsigned)(((int64_t)a.rows * a.k + 255) / 256)), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(few_join<T>, dim3((unsigned)(((int64_t)a.rows * a.k + 63) / 64)), dim3(1024), 0, st, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// Where the one pass wins over the three products of the matrix kernels.  Its
+// Where the one pass wins over the products of the matrix kernels.  Its
 // multiply-adds are 2 a row and value on the vector units, so rows end it: at
-// 4096 x 4096 bf16 the call took 21.8, 27.3 and 34.1 us for 1, 4 and 8 rows
-// where the products took 30.6, 30.2 and 30.7; at 8 rows of fp32 39.7 against
-// 57.8.  Small weights are bound by the launches either way (192 x 384: 11.7
-// against 10.7 us, 704 x 2000: 14.7 and 14.6).
+// 4096 x 4096 bf16 the call took 17.4, 23.9 and 33 us for 1, 4 and 8 rows
+// where the products took 30.6, 30.2 and 30.7; at 8 rows of fp32 39 against
+// 58.  Small weights are near each other (512 x 512: 9.2 and 12.6 us, 192 x
+// 384: 10.1 and 9.4), without dx the pass has one launch (5.4 and 8 us).
 bool few_rows(int dtype, int64_t rows, int64_t wide, int64_t k) {
-  return rows >= 1 && rows <= (dtype == kF32 ? 8 : 4) && k >= 8 && wide * k >= 1 << 20 && wide <= 65535ll * kMostN;
+  return rows >= 1 && rows <= (dtype == kF32 ? 8 : 4) && k >= 8 && wide >= 1 && wide <= 65535ll * kMostN;
 }
 
 // Columns across, rows of W a block, parts of dx.

@@ -203,13 +203,16 @@ template <typename T, typename W, int TPR, int E, int V, int kRows, bool STREAM>
 __global__ __launch_bounds__(TPR * kRows) void norm_backward(NormArgs a) {
   using R = Row<T, TPR, E, V>;
   constexpr int kThreads = TPR * kRows;
+  // A row of 32 values a thread leaves no registers for the next one (kept
+  // ahead, 4096 x 16384 fp32 spilled 70 of them: 328 us, not 170).
+  constexpr bool kAhead = E < 32;
   __shared__ float smem[kThreads / 64 * 2];
   const int t = threadIdx.x % TPR;
   const int lane_row = threadIdx.x / TPR;
   const R r(a.cols, t);
-  // The next row is loaded while this one is worked on.  Every thread of a
-  // block runs the same number of turns; a row past the end is the last one
-  // again, not counted and not stored.
+  // The next row is loaded while this one is worked on (kAhead).  Every thread
+  // of a block runs the same number of turns; a row past the end is the last
+  // one again, not counted and not stored.
   const int64_t stride = (int64_t)a.groups * kRows;
   int64_t row = (int64_t)blockIdx.x * kRows + lane_row;
   typename R::template Raw<T> rx, rdy;
@@ -221,7 +224,7 @@ __global__ __launch_bounds__(TPR * kRows) void norm_backward(NormArgs a) {
     next_mean = a.mean[i];
     next_rstd = a.rstd[i];
   };
-  fetch(row);
+  if (kAhead) fetch(row);
   float dw[E], db[E];
   typename R::template Raw<W> wt;
   if (a.weight) r.template load<W>((const W*)a.weight, wt);
@@ -230,11 +233,12 @@ __global__ __launch_bounds__(TPR * kRows) void norm_backward(NormArgs a) {
   for (int i = 0; i < E; i++) dw[i] = db[i] = 0.0f;
   for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.rows; base += stride, row += stride) {
     const bool live = row < a.rows;
+    if (!kAhead) fetch(row);
     float h[E], dy[E];
     r.template widen<T>(rx, h);
     r.template widen<T>(rdy, dy);
     const float mean = next_mean, rstd = next_rstd;
-    fetch(row + stride);
+    if (kAhead) fetch(row + stride);
     float sg = 0.0f, sgh = 0.0f;
 #pragma unroll
     for (int i = 0; i < E; i++) {
@@ -255,9 +259,14 @@ __global__ __launch_bounds__(TPR * kRows) void norm_backward(NormArgs a) {
       if (live) r.template store<STREAM>((T*)a.y + row * a.ldy, dy);
     }
   }
-  if (!a.part) return;
-  // the block's rows into one partial row
+  if (!a.part && !a.dweight && !a.dbias) return;
+  // the block's rows into one partial row, or where it has them all into the gradients
   float* out = a.part + (int64_t)blockIdx.x * 2 * a.cols;
+  auto put = [&](int which, int c, float s) {
+    W* g = (W*)(which ? a.dbias : a.dweight);
+    if (a.part) out[which * a.cols + c] = s;
+    else if (g) g[c] = (W)s;
+  };
   if constexpr (kRows > 1) {
     __shared__ float rows[kRows][TPR * E];
 #pragma unroll
@@ -269,13 +278,13 @@ __global__ __launch_bounds__(TPR * kRows) void norm_backward(NormArgs a) {
         float s = 0.0f;
 #pragma unroll 4
         for (int i = 0; i < kRows; i++) s += rows[i][c];
-        out[which * a.cols + c] = s;
+        put(which, c, s);
       }
     }
   } else {
     r.each([&](int i, int c) {
-      out[c] = dw[i];
-      out[a.cols + c] = db[i];
+      put(0, c, dw[i]);
+      put(1, c, db[i]);
     });
   }
 }
@@ -324,7 +333,6 @@ template <typename O> __global__ __launch_bounds__(1024) void col_sum(ColSumArgs
 }
 
 // Threads and elements per thread of a row: the smallest shape that holds it.
-constexpr int kLongest = 1024 * 16;
 template <typename T, typename W> hipError_t forward(const NormArgs& a, hipStream_t st) {
   auto go = [&](auto kernel, int tpr) {
     const int threads = tpr < kBlock ? kBlock : tpr, rows = threads / tpr;
@@ -345,7 +353,7 @@ template <typename T, typename W> hipError_t forward(const NormArgs& a, hipStrea
   RINGAR_NORM(512, 16);
   RINGAR_NORM(1024, 16);
 #undef RINGAR_NORM
-  static_assert(kLongest == 1024 * 16, "the widest rows held in registers");
+  static_assert(kNormLongest == 1024 * 16, "the widest rows held in registers");
   hipLaunchKernelGGL((norm_forward_long<T, W>), dim3((unsigned)a.rows), dim3(1024), 0, st, a);
   return hipGetLastError();
 }
@@ -381,11 +389,14 @@ template <typename T, typename W> hipError_t backward(const NormArgs& a, hipStre
 
 // Blocks of the backward grid, each of which leaves one partial row: enough
 // to fill the GPU (8 waves a CU), few enough that the partial rows stay small beside
-// the rows themselves.
+// the rows themselves.  Two turns of one block cost less than a second block
+// and the launch that adds their rows (16 x 832 fp16: 7.0 us, not 8.3; one
+// turn 5.7).
 int norm_backward_groups(int64_t rows, int cols) {
-  if (cols > kLongest) return (int)(rows < 64 ? rows : 64);
+  if (cols > kNormLongest) return (int)(rows < 64 ? rows : 64);
   const int per = cols <= 128 ? 16 : cols <= 1024 ? 8 : cols <= 4096 ? 2 : 1;   // rows of a block at a time
   const int64_t blocks = (rows + per - 1) / per;
+  if (blocks == 2) return 1;
   const int64_t most = cols <= 128 ? 512 : 256;
   return (int)(blocks < most ? blocks : most);
 }
