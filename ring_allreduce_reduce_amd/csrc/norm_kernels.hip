@@ -106,6 +106,26 @@ template <typename T, int TPR, int E, int V> struct Row {
       for (int j = 0; j < V; j++)
         if (j >= skip[i]) f(i * V + j, col[i] + j);
   }
+  // fp32 sums, 16 bytes at a time (value by value the partial rows of 8192 x
+  // 8192 bf16 cost 10 us more: 83, not 73)
+  __device__ inline void sums(float* p, const float* in) const {
+    constexpr int S = V < 4 ? V : 4;
+#pragma unroll
+    for (int i = 0; i < P; i++)
+#pragma unroll
+      for (int h = 0; h < V; h += S) {
+        if (skip[i] <= h) {
+          Pack<float, S> q;
+#pragma unroll
+          for (int j = 0; j < S; j++) q.v[j] = in[i * V + h + j];
+          store_pack<float, S>(p + col[i] + h, q);
+        } else {
+#pragma unroll
+          for (int j = 0; j < S; j++)
+            if (h + j >= skip[i]) p[col[i] + h + j] = in[i * V + h + j];
+        }
+      }
+  }
   template <bool STREAM> __device__ inline void store(T* p, const float* in) const {
 #pragma unroll
     for (int i = 0; i < P; i++) {
@@ -272,7 +292,7 @@ __global__ __launch_bounds__(TPR * kRows) void norm_backward(NormArgs a) {
 #pragma unroll
     for (int which = 0; which < 2; which++) {
       if (which) __syncthreads();
-      r.each([&](int i, int c) { rows[lane_row][c] = which ? db[i] : dw[i]; });
+      r.sums(rows[lane_row], which ? db : dw);
       __syncthreads();
       for (int c = threadIdx.x; c < a.cols; c += kThreads) {
         float s = 0.0f;
@@ -282,10 +302,15 @@ __global__ __launch_bounds__(TPR * kRows) void norm_backward(NormArgs a) {
       }
     }
   } else {
-    r.each([&](int i, int c) {
-      put(0, c, dw[i]);
-      put(1, c, db[i]);
-    });
+    if (a.part) {
+      r.sums(out, dw);
+      r.sums(out + a.cols, db);
+    } else {
+      r.each([&](int i, int c) {
+        put(0, c, dw[i]);
+        put(1, c, db[i]);
+      });
+    }
   }
 }
 
