@@ -98,18 +98,25 @@ template <typename T> hipError_t launch(const DzArgs& a, hipStream_t st) {
 template <typename T, int V> __global__ __launch_bounds__(256) void pack_rows(PackArgs both) {
   const bool second = blockIdx.x >= both.one[0].blocks;
   const PackArgs::One& a = both.one[second];
-  const int64_t per_row = a.ld_to / V;
-  const int64_t i = (int64_t)(blockIdx.x - (second ? both.one[0].blocks : 0)) * 256 + threadIdx.x;
-  const int64_t row = i / per_row;
+  // the block's first pack by one scalar division, the threads' in 32 bits
+  const uint32_t per_row = (uint32_t)(a.ld_to / V);
+  const int64_t first = (int64_t)(blockIdx.x - (second ? both.one[0].blocks : 0)) * 256;
+  const int64_t first_row = first / per_row;
+  const uint32_t in_row = (uint32_t)(first - first_row * per_row) + threadIdx.x;
+  const int64_t row = first_row + in_row / per_row;
   if (row >= a.rows) return;
-  const int64_t c = i % per_row * V;
-  const T* from = (const T*)a.from + row * a.ld_from + c;
+  const int64_t c = (int64_t)(in_row % per_row) * V;
+  const T* from = (const T*)a.from + row * a.ld_from;
   Pack<T, V> v;
   if (c + V <= a.cols) {
-    v = load_pack<T, V>(from);
+    v = load_pack<T, V>(from + c);
   } else {
+    // no load depends on another's condition: all are in flight together
 #pragma unroll
-    for (int j = 0; j < V; j++) v.v[j] = c + j < a.cols ? from[j] : (T)0.0f;
+    for (int j = 0; j < V; j++) {
+      const T x = from[c + j < a.cols ? c + j : a.cols - 1];
+      v.v[j] = c + j < a.cols ? x : (T)0.0f;
+    }
   }
   store_pack<T, V>((T*)a.to + row * a.ld_to + c, v);
 }
