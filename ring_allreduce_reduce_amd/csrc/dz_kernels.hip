@@ -4,7 +4,9 @@
 //   gated:  dg = dh u act'(g), du = dh act(g)
 // dz is rounded to the operand type once, for the matrix products that read
 // it twice; the sums are taken of the unrounded values.  Memory bound: each
-// thread moves 16-byte packs of one column group down its block's rows.
+// thread moves 16-byte packs of one column group down its block's rows, and
+// the groups of rows leave a partial sum each (8192 x 2 * 10240 bf16 gated: 145
+// us, 5.8 TB/s; 4096 x 16384 with sums: 72 us, 5.6 TB/s).
 #include "block_types.h"
 
 namespace ringar {
@@ -94,7 +96,8 @@ template <typename T> hipError_t launch(const DzArgs& a, hipStream_t st) {
 }
 
 // A copy with rows padded to 128 bytes (zeros), for loads that need them to
-// start at 16-byte boundaries.
+// start at 16-byte boundaries; both operands in one launch (333 and 2049 rows
+// of 1023 fp16: 4.7 us, most of it the launch and one round trip).
 template <typename T, int V> __global__ __launch_bounds__(256) void pack_rows(PackArgs both) {
   const bool second = blockIdx.x >= both.one[0].blocks;
   const PackArgs::One& a = both.one[second];

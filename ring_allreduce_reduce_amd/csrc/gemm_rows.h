@@ -3,12 +3,14 @@
 // how much of it is in flight.
 //
 // A block takes 16 rows of the weight (gated: 8 of the gate and the same 8 of
-// the up projection), its waves the steps of k in turn; a wave's lane loads 16 bytes of weight row
-// l % 16 at a time, which is the matrix instruction's own operand layout, so
-// nothing passes through LDS until the waves' sums are added, in wave order.
+// the up projection), its waves the steps of k in turn; a wave's lane loads 16
+// bytes of weight row l % 16 at a time, which is the matrix instruction's own
+// operand layout, so nothing passes through LDS until the waves' sums are
+// added, in wave order.
 // The step after the next is on its way while one is multiplied.  Where the
 // blocks are too few to fill the GPU, k is split over several; the last of
-// them to arrive adds the parts, in their order.
+// them to arrive adds the parts, in their order.  1 x 4096 x 4096 bf16: 8.4 us,
+// 4.0 TB/s; 16 rows cost as one (one matrix instruction holds them all).
 #pragma once
 
 #include "gemm_kernel.h"

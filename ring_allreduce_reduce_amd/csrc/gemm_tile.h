@@ -7,7 +7,10 @@
 // to arrive.  Within a step the fragments of one half are read while the
 // other half's matrix instructions run, and the next step's first half is
 // read across the barrier, so the matrix units wait for LDS only where a
-// wave waits for the slowest one.
+// wave waits for the slowest one.  8192 x 4096 x 16384 bf16: 776 us (1417
+// TFLOP/s) forward without an epilogue, 838 .. 910 with bias, gelu and the kept
+// pre-activation; the matrix units are busy 67 .. 70% of the time at the 1.9 GHz
+// that the power leaves.
 //
 // LDS holds an operand as it lies in memory:
 //   ROW (k contiguous): one 128-byte line per row, its eight 16-byte chunks

@@ -11,6 +11,9 @@
 // every row it meets: the parameter gradients build up in registers, leave
 // as one partial row per block, and are added in block order by a second
 // kernel (no atomics: results do not depend on scheduling).
+//
+// Memory bound: forward 16384 x 8192 bf16 94 us (5.7 TB/s), backward 16384 x
+// 4096 bf16 74 us and 5 us of column sums (5.4 TB/s).
 #include "block_types.h"
 
 namespace ringar {
