@@ -547,3 +547,29 @@ def test_flags_must_be_flags():
                  lambda: ra.linear(x, w, save_pre=1)):
         with pytest.raises(ra.RingarError, match="must be True or False"):
             call()
+
+
+@pytest.mark.parametrize("rows", [1, 3, 12, 20])
+def test_weight_beyond_32_bit_offsets(rows):
+    """out_features * in_features past 2^31 elements, forward and backward:
+    first, middle and last rows of the weight."""
+    k, n = 2048, (1 << 31) // 2048 + 300
+    g = _gen("wide", rows)
+    at = [0, 1, 77777, (1 << 20) - 1, 1 << 20, n - 1]
+    x, some = _rand(g, (rows, k), BF16), _rand(g, (len(at), k), BF16, k ** -0.5)
+    w = torch.zeros(n, k, dtype=BF16, device="cuda")
+    w[at] = some
+    y = ra.linear(x, w)
+    want, bound = R.linear_forward(x, some, None, "none", None)
+    R.assert_within(y[:, at], want[0], bound[0], "y")
+    assert int(torch.count_nonzero(y)) == int(torch.count_nonzero(y[:, at]))
+    dy = torch.zeros(rows, n, dtype=BF16, device="cuda")
+    dy[:, at] = _rand(g, (rows, len(at)), BF16)
+    del y
+    dx, dw, db = ra.linear_backward(dy, x, w)
+    want, bound = R.backward(dy[:, at].contiguous(), x, some, None, "none", False)
+    R.assert_within(dx, want[0], bound[0], "dx")
+    R.assert_within(dw[at], want[1], bound[1], "dweight")
+    R.assert_within(db[at], want[2], bound[2], "dbias")
+    dw[at] = 0
+    assert int(torch.count_nonzero(dw.view(-1, 1 << 11)[::1009])) == 0 and int(torch.count_nonzero(dw[-400:])) == 0
