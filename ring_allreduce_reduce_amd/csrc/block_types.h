@@ -164,6 +164,21 @@ template <bool FAST, int N> __device__ inline void activate_grad_n(int act, cons
 __device__ inline void put_part(float* p, float v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 __device__ inline float get_part(const float* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
+// The sum of parts first, first + step, .. below `count`, in that order.  N
+// loads are in flight at a time, the last ones too (an unrolled loop takes
+// its rest one by one: backward of 4 x 117 x 13184 fp16 11.4 us, not 10.2).
+template <int N, typename F> __device__ inline float sum_parts(int first, int step, int count, F load) {
+  float s = 0.0f;
+  for (int i = first; i < count; i += N * step) {
+    float v[N];
+#pragma unroll
+    for (int j = 0; j < N; j++) v[j] = load(i + j * step < count ? i + j * step : i);
+#pragma unroll
+    for (int j = 0; j < N; j++) s += i + j * step < count ? v[j] : 0.0f;
+  }
+  return s;
+}
+
 // Called by every thread of `blocks` blocks after their put_part()s: true in
 // the block that arrives last, which may then get_part() every part.  The
 // counter is zero before and after (it belongs to the workspace).
@@ -313,8 +328,7 @@ template <typename O> __device__ inline void col_sum_block(const ColSumArgs& a, 
   float s = 0.0f;
   if (c < a.width) {
     const float* p = a.part + c;
-#pragma unroll 8
-    for (int i = w; i < a.parts; i += waves) s += p[i * a.width];
+    s = sum_parts<8>(w, waves, a.parts, [&](int i) { return p[i * a.width]; });
   }
   smem[w * 64 + lane] = s;
   __syncthreads();

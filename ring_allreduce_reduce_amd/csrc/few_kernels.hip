@@ -137,10 +137,7 @@ template <typename T> __global__ __launch_bounds__(1024) void few_join(FewArgs a
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t width = (int64_t)a.rows * a.k, i = (int64_t)blockIdx.x * 64 + lane;
   float s = 0.0f;
-  if (i < width) {
-#pragma unroll 8
-    for (int p = w; p < a.parts; p += 16) s += a.part[p * width + i];
-  }
+  if (i < width) s = sum_parts<8>(w, 16, a.parts, [&](int p) { return a.part[p * width + i]; });
   lds[w][lane] = s;
   __syncthreads();
   if (w || i >= width) return;

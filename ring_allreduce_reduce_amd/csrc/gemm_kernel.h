@@ -63,12 +63,9 @@ template <typename T, int EPI> __global__ __launch_bounds__(256) void gemm_join(
   const int n = (int)(i % a.n);
   if (m >= a.m) return;
   const float* p = a.part + m * cols + n;
-  float s = 0.0f, u = 0.0f;
-  for (int k = 0; k < a.splits; k++) {
-    s += p[(int64_t)k * a.m * cols];
-    if constexpr (EPI == kEpiGated) u += p[(int64_t)k * a.m * cols + a.n];
-  }
-  if constexpr (EPI == kEpiGated) finish_gated<T>(a, m, n, s, u);
+  auto sum = [&](const float* p) { return sum_parts<4>(0, 1, a.splits, [&](int k) { return p[k * (a.m * cols)]; }); };
+  const float s = sum(p);
+  if constexpr (EPI == kEpiGated) finish_gated<T>(a, m, n, s, sum(p + a.n));
   else if constexpr (EPI == kEpiLinear) finish_linear<T>(a, m, n, s);
   else ((T*)a.c)[m * a.ldc + n] = (T)s;
 }

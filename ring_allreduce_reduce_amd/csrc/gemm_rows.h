@@ -104,11 +104,7 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_rows(GemmArgs a) {
     const int64_t next = (int64_t)a.m * 16;
     if (mine) put_part(part + split * next, v);
     if (!last_to_arrive(a.arrived + tile, a.splits)) return;
-    if (mine) {
-      v = 0.0f;
-#pragma unroll 8
-      for (int i = 0; i < a.splits; i++) v += get_part(part + i * next);
-    }
+    if (mine) v = sum_parts<8>(0, 1, a.splits, [&](int i) { return get_part(part + i * next); });
   }
   if constexpr (EPI == kEpiGated) {
     const float up = __shfl_down(v, 8);      // the up projection's sums sit eight lanes on
