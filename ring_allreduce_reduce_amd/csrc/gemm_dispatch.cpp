@@ -112,10 +112,10 @@ static GemmPlan plan_tiles(int dtype, int epi, const GemmArgs& given, int only, 
   if (a.m == 0 || a.n == 0) return p;
   const int es = dtype == kF32 ? 4 : 2;
   const int64_t wide = epi == kEpiGated ? 2 * (int64_t)a.n : a.n;
-  // Up to 16 rows; where the weight is large the tiles, which read the rows
+  // Up to 16 rows of 16 bytes or more; where the weight is large the tiles, which read the rows
   // once for 128 columns, win from 9 on (16 x 4096 x 20480 bf16: 36 us, not
   // 43; 16 x 4096 x 4096: 16 us, not 10).
-  if (epi != kEpiStore && a.m <= (wide >= 16384 ? 8 : 16)) {
+  if (epi != kEpiStore && a.k >= 16 / es && a.m <= (wide >= 16384 ? 8 : 16)) {
     a.variant = kRows;
     // k over several blocks until there are two for every CU, each with
     // two steps for each of its 8 waves or more

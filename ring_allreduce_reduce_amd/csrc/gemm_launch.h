@@ -38,7 +38,15 @@ template <typename T, bool AROW, bool BROW, int EPI> hipError_t launch_tiled(con
       return hipErrorInvalidValue;
     case kRows:
       if constexpr (EPI != kEpiStore) {
-        hipLaunchKernelGGL((gemm_rows<T, EPI, 8>), dim3((unsigned)(rows_tiles(EPI, a.n) * a.splits)), dim3(512), 0, st, a);
+        const dim3 grid((unsigned)(rows_tiles(EPI, a.n) * a.splits));
+        const bool halves = ((uintptr_t)a.a | (uintptr_t)a.b | (uintptr_t)(a.sam | a.sbn) * sizeof(T)) % 4 != 0;
+        if constexpr (sizeof(T) == 2) {
+          if (halves) {
+            hipLaunchKernelGGL((gemm_rows<T, EPI, 8, true>), grid, dim3(512), 0, st, a);
+            return hipGetLastError();
+          }
+        }
+        hipLaunchKernelGGL((gemm_rows<T, EPI, 8, false>), grid, dim3(512), 0, st, a);
         return hipGetLastError();
       }
       return hipErrorInvalidValue;

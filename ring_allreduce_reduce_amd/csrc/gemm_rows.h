@@ -19,7 +19,23 @@ namespace ringar {
 
 constexpr int kRowsMost = 16;      // rows of one matrix instruction
 
-template <typename T, int EPI, int WAVES>
+// 16 bytes at an address that is a multiple of 2 alone: from the five words
+// around them (each holds at least one of the bytes).  One load there costs
+// as much as several (1 x 4095 x 16384 fp16: 31 us, 56 with it).
+__device__ inline f32x4 load_from_words(const void* p) {
+  typedef uint32_t words __attribute__((ext_vector_type(4), aligned(4)));
+  const uintptr_t at = (uintptr_t)p & ~(uintptr_t)3;
+  const bool half = (uintptr_t)p & 2;
+  const words w = *(const words*)at;
+  const uint32_t last = *(const uint32_t*)(at + (half ? 16 : 12));
+  const uint32_t shift = half ? 16 : 0;
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(f32x4, u32x4{__builtin_amdgcn_alignbit(w[1], w[0], shift), __builtin_amdgcn_alignbit(w[2], w[1], shift),
+                                         __builtin_amdgcn_alignbit(w[3], w[2], shift), __builtin_amdgcn_alignbit(last, w[3], shift)});
+}
+
+// HALVES: rows may start between two words.
+template <typename T, int EPI, int WAVES, bool HALVES>
 __global__ __launch_bounds__(64 * WAVES) void gemm_rows(GemmArgs a) {
   using Frag = typename Mma<T>::Frag;
   constexpr int kVec = 16 / sizeof(T);
@@ -31,36 +47,32 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_rows(GemmArgs a) {
   const int64_t n0 = (int64_t)tile * kCols;
   const int k_end = a.k - split * a.k_per_split < a.k_per_split ? a.k : (split + 1) * a.k_per_split;
   const int64_t col = n0 + t % kCols < a.n ? n0 + t % kCols : a.n - 1;   // past the edge: the last column again, not stored
-  const T* w = (const T*)a.b + (col + (kCols == 8 && t >= 8 ? a.n : 0)) * a.sbn + g * kVec;
-  const T* x = (const T*)a.a + (t < a.m ? t : 0) * a.sam + g * kVec;
+  const T* w = (const T*)a.b + (col + (kCols == 8 && t >= 8 ? a.n : 0)) * a.sbn;
+  const T* x = (const T*)a.a + (t < a.m ? t : 0) * a.sam;
 
   struct Step {
     Frag w[U], x[U];
   };
   auto load16 = [](const T* p) {
     Frag f;
-    __builtin_memcpy(&f, p, 16);
-    return f;
-  };
-  auto load_tail = [](const T* p, int n) {   // the first n values, zeros after them
-    Frag f;
-#pragma unroll
-    for (int i = 0; i < kVec; i++) f[i] = i < n ? p[i] : (T)0.0f;
+    if constexpr (HALVES) f = __builtin_bit_cast(Frag, load_from_words(p));
+    else __builtin_memcpy(&f, p, 16);
     return f;
   };
   auto load = [&](Step& s, int k0) {
-    if (k0 + kStep <= k_end) {
+    // What would pass the end starts kVec before it instead, with zeros in
+    // place of the values that another lane holds.
+    const int at = k0 + g * kVec, last = k_end - kVec;
 #pragma unroll
-      for (int u = 0; u < U; u++) s.w[u] = load16(w + k0 + u * kK);
+    for (int u = 0; u < U; u++) s.w[u] = load16(w + (at + u * kK < last ? at + u * kK : last));
 #pragma unroll
-      for (int u = 0; u < U; u++) s.x[u] = load16(x + k0 + u * kK);
-    } else {
+    for (int u = 0; u < U; u++) s.x[u] = load16(x + (at + u * kK < last ? at + u * kK : last));
+    if (k0 + kStep > k_end) {
 #pragma unroll
-      for (int u = 0; u < U; u++) {
-        const int n = k_end - (k0 + u * kK + g * kVec);
-        s.w[u] = load_tail(w + k0 + u * kK, n);
-        s.x[u] = load_tail(x + k0 + u * kK, n);
-      }
+      for (int u = 0; u < U; u++)
+#pragma unroll
+        for (int i = 0; i < kVec; i++)
+          if (i < at + u * kK - last) s.w[u][i] = s.x[u][i] = (T)0.0f;
     }
   };
   f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
