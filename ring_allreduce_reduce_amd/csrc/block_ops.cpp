@@ -116,6 +116,7 @@ struct Mat {
   int64_t rows, cols, ld;
   size_t es;
   bool output;
+  bool in_place = false;   // an input that may be y's very place
 };
 
 // Null where something is to be read or written, misalignment, a row stride
@@ -147,16 +148,17 @@ bool overlap(const Mat& a, const Mat& b) {
 
 bool same_place(const Mat& a, const Mat& b) { return a.p == b.p && (a.ld == b.ld || a.rows <= 1) && a.es == b.es; }
 
-// Every operand's own checks, and no output over another operand.  `alias`:
-// an input that may be y's very place (the elements are read before
-// they are written, by the same thread).
-ringar_result_t check_mats(std::initializer_list<Mat> all, const void* alias_in = nullptr) {
+// Every operand's own checks, and no output over another operand.  The one
+// exception is the operand marked `in_place` (its elements are read before y's
+// are written, by the same thread); another one that lies at the same address,
+// say a square product's x that is the residual too, is refused.
+ringar_result_t check_mats(std::initializer_list<Mat> all) {
   for (const Mat& m : all) TRY(check_mat(m));
   for (const Mat* o = all.begin(); o != all.end(); o++) {
     if (!o->output) continue;
     for (const Mat* m = all.begin(); m != all.end(); m++) {
       if (m == o || (m->output && m < o)) continue;
-      if (alias_in && m->p == alias_in && !m->output && !strcmp(o->name, "y") && same_place(*m, *o)) continue;
+      if (m->in_place && !strcmp(o->name, "y") && same_place(*m, *o)) continue;
       if (overlap(*o, *m))
         return refuse(RINGAR_ERR_INVALID_USAGE, std::string(o->name) + " overlaps " + m->name);
     }
@@ -230,13 +232,12 @@ static ringar_result_t norm_forward(const ringar_layer_norm_t* p, ringar_stream_
   if (!dims_ok({p->rows, p->cols}) || p->cols == 0) return refuse(RINGAR_ERR_INVALID_ARGUMENT, "rows or cols out of range");
   if (!(p->eps >= 0.0f)) return refuse(RINGAR_ERR_INVALID_ARGUMENT, "eps below zero");
   const size_t es = size_of(p->dtype), ws = size_of(p->param_dtype);
-  TRY(check_mats({{"x", p->x, p->rows, p->cols, p->ldx, es, false},
+  TRY(check_mats({{"x", p->x, p->rows, p->cols, p->ldx, es, false, true},
                   VEC("weight", p->weight, p->cols, ws, false),
                   VEC("bias", p->bias, p->cols, ws, false),
                   {"y", p->y, p->rows, p->cols, p->ldy, es, true},
                   VEC("mean", p->mean, p->rows, 4, true),
-                  VEC("rstd", p->rstd, p->rows, 4, true)},
-                 p->x));
+                  VEC("rstd", p->rstd, p->rows, 4, true)}));
   if (p->rows == 0) return RINGAR_SUCCESS;
   NormArgs a = {};
   a.x = p->x;
@@ -313,10 +314,9 @@ static ringar_result_t product_forward(const ringar_linear_t* p, bool gated, hip
   TRY(check_mats({{"x", p->x, p->rows, p->in_features, p->ldx, es, false},
                   {"weight", p->weight, wide, p->in_features, p->ldw, es, false},
                   VEC("bias", p->bias, wide, es, false),
-                  {"residual", p->residual, p->residual ? p->rows : 0, p->out_features, p->ldr, es, false},
+                  {"residual", p->residual, p->residual ? p->rows : 0, p->out_features, p->ldr, es, false, true},
                   {"y", p->y, p->rows, p->out_features, p->ldy, es, true},
-                  {"pre", p->pre, p->pre ? p->rows : 0, wide, p->ldp, es, true}},
-                 p->residual));
+                  {"pre", p->pre, p->pre ? p->rows : 0, wide, p->ldp, es, true}}));
   if (p->rows == 0 || p->out_features == 0) return RINGAR_SUCCESS;
   const int epi = gated ? kEpiGated : kEpiLinear;
   GemmArgs a = {};
