@@ -467,8 +467,9 @@ ringar_result_t ringar_chunk_range(size_t count, ringar_dtype_t dtype, int nrank
  * said.  Results do not depend on scheduling (no atomic sums).
  *
  * Calls enqueue on `stream` and return; the caller keeps the operands until
- * the work is done.  Workspaces are the library's, one per stream, grown as
- * needed (growing waits for the stream) and freed by ringar_release; under
+ * the work is done.  Workspaces are the library's, one per stream (on
+ * hipStreamPerThread one per host thread), grown as needed (growing waits for
+ * the stream), kept at the largest size needed and freed by ringar_release; under
  * stream capture nothing is allocated: the stream must have run a call of
  * the same shape first, else RINGAR_ERR_INVALID_USAGE, and a graph must not
  * be replayed after ringar_release, nor beside other work of its stream.

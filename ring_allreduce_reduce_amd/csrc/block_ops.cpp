@@ -3,13 +3,14 @@
 // feed-forward, each with its backward pass.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <initializer_list>
 #include <map>
 #include <mutex>
 #include <string>
-#include <utility>
+#include <tuple>
 #include <vector>
 
 #include "block_types.h"
@@ -55,8 +56,17 @@ struct Workspace {
   std::vector<void*> retired;          // replaced buffers such graphs may hold
 };
 
+// hipStreamPerThread is one handle for a stream of every host thread: there
+// the thread's number (never used again) tells the streams apart.
+uint64_t thread_of(hipStream_t st) {
+  static std::atomic<uint64_t> threads{0};
+  if (st != hipStreamPerThread) return 0;
+  static thread_local const uint64_t mine = ++threads;
+  return mine;
+}
+
 std::mutex g_ws_mu;
-std::map<std::pair<int, hipStream_t>, Workspace> g_ws;
+std::map<std::tuple<int, hipStream_t, uint64_t>, Workspace> g_ws;
 
 // The buffer starts with kCounters zeroed words, which every kernel that uses
 // one leaves at zero; *out is what follows them.
@@ -70,7 +80,7 @@ ringar_result_t workspace(hipStream_t st, size_t bytes, char** out) {
   HIP_TRY(hipGetDevice(&dev));
   hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
   HIP_TRY(hipStreamIsCapturing(st, &cap));
-  Workspace& w = g_ws[std::make_pair(dev, st)];
+  Workspace& w = g_ws[std::make_tuple(dev, st, thread_of(st))];
   w.device = dev;
   if (cap != hipStreamCaptureStatusNone) {
     if (w.bytes < bytes)
