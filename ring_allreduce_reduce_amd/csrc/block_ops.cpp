@@ -96,8 +96,13 @@ ringar_result_t workspace(hipStream_t st, size_t bytes, char** out) {
     w.captured_ever = false;
     const size_t want = (bytes + (4u << 20) - 1) / (4u << 20) * (4u << 20);
     HIP_TRY(hipMalloc((void**)&w.p, want));
+    const hipError_t e = launch_fill((uint64_t*)w.p, kCounterBytes / 8, 0, st);
+    if (e != hipSuccess) {                   // counters unset: the next call starts over
+      (void)hipFree(w.p);
+      w.p = nullptr;
+      return hip_fail(e, "clearing the workspace's counters");
+    }
     w.bytes = want;
-    HIP_TRY(launch_fill((uint64_t*)w.p, kCounterBytes / 8, 0, st));
   }
   *out = w.p + kCounterBytes;
   return RINGAR_SUCCESS;
