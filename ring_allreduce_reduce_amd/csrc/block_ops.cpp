@@ -22,7 +22,10 @@ using namespace ringar;
 
 namespace {
 
+// The call's result tells of the error: nothing of it is left for
+// hipGetLastError().
 ringar_result_t hip_fail(hipError_t e, const char* what) {
+  (void)hipGetLastError();
   last_error_text() = std::string(what) + ": " + hipGetErrorString(e);
   return RINGAR_ERR_DEVICE;
 }

@@ -6,7 +6,20 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace ringar {
+
+// Launches `kernel` and returns that launch's own error.  (hipGetLastError()
+// would return any error that an earlier call, not the library's perhaps, has
+// left behind; a failed launch leaves none, as the result tells of it.)
+template <typename... P>
+inline hipError_t launch_kernel(void (*kernel)(P...), dim3 grid, unsigned threads, hipStream_t st, std::common_type_t<P>... args) {
+  void* params[] = {(void*)&args...};
+  const hipError_t e = hipLaunchKernel((const void*)kernel, grid, dim3(threads), params, 0, st);
+  if (e != hipSuccess) (void)hipGetLastError();
+  return e;
+}
 
 // activation codes of the public header
 enum : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4, kActSigmoid = 5 };

@@ -85,9 +85,7 @@ template <typename T, bool GATED, int V> __global__ __launch_bounds__(256) void 
 
 template <typename T, int V> hipError_t launch(const DzArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)(((int64_t)a.n + 64 * V - 1) / (64 * V)), a.groups);
-  if (a.gated) hipLaunchKernelGGL((dz_kernel<T, true, V>), grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((dz_kernel<T, false, V>), grid, dim3(256), 0, st, a);
-  return hipGetLastError();
+  return a.gated ? launch_kernel(dz_kernel<T, true, V>, grid, 256, st, a) : launch_kernel(dz_kernel<T, false, V>, grid, 256, st, a);
 }
 
 template <typename T> hipError_t launch(const DzArgs& a, hipStream_t st) {
@@ -133,8 +131,7 @@ template <typename T> hipError_t pack(PackArgs& a, hipStream_t st) {
     if (total > 0x7fffffff) return hipErrorInvalidValue;
     o.blocks = (unsigned)blocks;
   }
-  if (total) hipLaunchKernelGGL((pack_rows<T, V>), dim3((unsigned)total), dim3(256), 0, st, a);
-  return hipGetLastError();
+  return total ? launch_kernel(pack_rows<T, V>, dim3((unsigned)total), 256, st, a) : hipSuccess;
 }
 
 }  // namespace

@@ -149,11 +149,9 @@ template <typename T> __global__ __launch_bounds__(1024) void few_join(FewArgs a
 
 template <typename T, int V, int M> hipError_t launch(const FewArgs& a, hipStream_t st) {
   const int64_t packs = (a.k + V - 1) / V;
-  hipLaunchKernelGGL((few_backward<T, V, M>), dim3((unsigned)((packs + (1 << a.across_log) - 1) >> a.across_log), a.parts), dim3(256), 0, st, a);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = launch_kernel(few_backward<T, V, M>, dim3((unsigned)((packs + (1 << a.across_log) - 1) >> a.across_log), a.parts), 256, st, a);
   if (e != hipSuccess || !a.dx || a.parts == 1) return e;
-  hipLaunchKernelGGL(few_join<T>, dim3((unsigned)(((int64_t)a.rows * a.k + 63) / 64)), dim3(1024), 0, st, a);
-  return hipGetLastError();
+  return launch_kernel(few_join<T>, dim3((unsigned)(((int64_t)a.rows * a.k + 63) / 64)), 1024, st, a);
 }
 
 }  // namespace

@@ -20,8 +20,7 @@ template <typename T, bool AROW, bool BROW, int EPI> struct Kernels {
 template <typename T, bool AROW, bool BROW, int EPI> hipError_t launch_tiled(const GemmArgs& a, hipStream_t st) {
   using K = Kernels<T, AROW, BROW, EPI>;
   auto go = [&](auto kernel, int threads) {
-    hipLaunchKernelGGL(kernel, dim3(blocks_of(a)), dim3(threads), 0, st, a);
-    return hipGetLastError();
+    return launch_kernel(kernel, dim3(blocks_of(a)), threads, st, a);
   };
   switch (a.variant) {
     case kTile256:
@@ -31,9 +30,8 @@ template <typename T, bool AROW, bool BROW, int EPI> hipError_t launch_tiled(con
         tail.tile_first = a.tile_count;
         tail.tile_count = a.tail_count;
         tail.quarters = true;
-        hipLaunchKernelGGL((gemm_pair<typename K::Large, typename K::Middle, 2>), dim3(blocks_of(a) + blocks_of(tail)), dim3(512), 0, st, a, tail,
-                           blocks_of(a));
-        return hipGetLastError();
+        return launch_kernel(gemm_pair<typename K::Large, typename K::Middle, 2>, dim3(blocks_of(a) + blocks_of(tail)), 512, st, a, tail,
+                             blocks_of(a));
       }
       return hipErrorInvalidValue;
     case kRows:
@@ -41,13 +39,9 @@ template <typename T, bool AROW, bool BROW, int EPI> hipError_t launch_tiled(con
         const dim3 grid((unsigned)(rows_tiles(EPI, a.n) * a.splits));
         const bool halves = ((uintptr_t)a.a | (uintptr_t)a.b | (uintptr_t)(a.sam | a.sbn) * sizeof(T)) % 4 != 0;
         if constexpr (sizeof(T) == 2) {
-          if (halves) {
-            hipLaunchKernelGGL((gemm_rows<T, EPI, 8, true>), grid, dim3(512), 0, st, a);
-            return hipGetLastError();
-          }
+          if (halves) return launch_kernel(gemm_rows<T, EPI, 8, true>, grid, 512, st, a);
         }
-        hipLaunchKernelGGL((gemm_rows<T, EPI, 8, false>), grid, dim3(512), 0, st, a);
-        return hipGetLastError();
+        return launch_kernel(gemm_rows<T, EPI, 8, false>, grid, 512, st, a);
       }
       return hipErrorInvalidValue;
     case kTile128: return go(gemm_tile<typename K::Middle, 4>, 512);
@@ -61,20 +55,15 @@ template <typename T> hipError_t launch_gradients(const GemmArgs& x, const GemmA
   const unsigned bs = (unsigned)((sums.width + 63) / 64);
   using X = Kernels<T, true, false, kEpiStore>;
   using W = Kernels<T, false, false, kEpiStore>;
-  if (x.variant == kTile128) {
-    const unsigned bx = blocks_of(x), bw = blocks_of(w);
-    hipLaunchKernelGGL((gemm_gradients<T, typename X::Middle, typename W::Middle, 4>), dim3(bx + bw + bs), dim3(512), 0, st, x, w, sums, bx, bw);
-  } else {
-    const unsigned bx = blocks_of(x), bw = blocks_of(w);
-    hipLaunchKernelGGL((gemm_gradients<T, typename X::Small, typename W::Small, 2>), dim3(bx + bw + bs), dim3(256), 0, st, x, w, sums, bx, bw);
-  }
-  return hipGetLastError();
+  const unsigned bx = blocks_of(x), bw = blocks_of(w);
+  if (x.variant == kTile128)
+    return launch_kernel(gemm_gradients<T, typename X::Middle, typename W::Middle, 4>, dim3(bx + bw + bs), 512, st, x, w, sums, bx, bw);
+  return launch_kernel(gemm_gradients<T, typename X::Small, typename W::Small, 2>, dim3(bx + bw + bs), 256, st, x, w, sums, bx, bw);
 }
 
 template <typename T, int EPI> hipError_t join(const GemmArgs& a, hipStream_t st) {
   if (a.splits == 1 || a.variant == kRows) return hipSuccess;
-  hipLaunchKernelGGL((gemm_join<T, EPI>), dim3((unsigned)(((int64_t)a.m * a.n + 255) / 256)), dim3(256), 0, st, a);
-  return hipGetLastError();
+  return launch_kernel(gemm_join<T, EPI>, dim3((unsigned)(((int64_t)a.m * a.n + 255) / 256)), 256, st, a);
 }
 
 }  // namespace ringar

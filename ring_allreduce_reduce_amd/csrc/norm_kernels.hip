@@ -366,8 +366,7 @@ template <typename T, typename W> hipError_t forward(const NormArgs& a, hipStrea
     const int threads = tpr < kBlock ? kBlock : tpr, rows = threads / tpr;
     // 16 waves a CU, which the kernels' registers allow
     const int64_t blocks = (a.rows + rows - 1) / rows, most = 256 * 1024 / threads;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(threads), 0, st, a);
-    return hipGetLastError();
+    return launch_kernel(kernel, dim3((unsigned)(blocks < most ? blocks : most)), threads, st, a);
   };
   constexpr int V = 16 / sizeof(T);
   if (a.cols < V) return go(norm_forward<T, W, 16, 1, 1, false>, 16);
@@ -382,15 +381,11 @@ template <typename T, typename W> hipError_t forward(const NormArgs& a, hipStrea
   RINGAR_NORM(1024, 16);
 #undef RINGAR_NORM
   static_assert(kNormLongest == 1024 * 16, "the widest rows held in registers");
-  hipLaunchKernelGGL((norm_forward_long<T, W>), dim3((unsigned)a.rows), dim3(1024), 0, st, a);
-  return hipGetLastError();
+  return launch_kernel(norm_forward_long<T, W>, dim3((unsigned)a.rows), 1024, st, a);
 }
 
 template <typename T, typename W> hipError_t backward(const NormArgs& a, hipStream_t st) {
-  auto go = [&](auto kernel, int threads) {
-    hipLaunchKernelGGL(kernel, dim3(a.groups), dim3(threads), 0, st, a);
-    return hipGetLastError();
-  };
+  auto go = [&](auto kernel, int threads) { return launch_kernel(kernel, dim3(a.groups), threads, st, a); };
   constexpr int V = 16 / sizeof(T);
   if (a.cols < V) return go(norm_backward<T, W, 16, 1, 1, 16, false>, 256);
 #define RINGAR_NORM(tpr, e, rows)                                                                     \
@@ -404,13 +399,10 @@ template <typename T, typename W> hipError_t backward(const NormArgs& a, hipStre
   RINGAR_NORM(512, 16, 1);
   RINGAR_NORM(512, 32, 1);
 #undef RINGAR_NORM
-  if (a.y) {
-    hipLaunchKernelGGL((norm_backward_long<T, W>), dim3((unsigned)a.rows), dim3(1024), 0, st, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !a.part) return e;
-  }
-  if (a.part) hipLaunchKernelGGL((norm_params_long<T>), dim3((unsigned)((a.cols + 255) / 256), a.groups), dim3(256), 0, st, a);
-  return hipGetLastError();
+  hipError_t e = hipSuccess;
+  if (a.y) e = launch_kernel(norm_backward_long<T, W>, dim3((unsigned)a.rows), 1024, st, a);
+  if (e != hipSuccess || !a.part) return e;
+  return launch_kernel(norm_params_long<T>, dim3((unsigned)((a.cols + 255) / 256), a.groups), 256, st, a);
 }
 
 }  // namespace
@@ -451,11 +443,10 @@ hipError_t launch_norm_backward(int dtype, int wdtype, const NormArgs& given, hi
 }
 
 hipError_t launch_col_sum(int out_dtype, const ColSumArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)((a.width + 63) / 64)), block(1024);
-  if (out_dtype == kF32) hipLaunchKernelGGL(col_sum<float>, grid, block, 0, st, a);
-  else if (out_dtype == kF16) hipLaunchKernelGGL(col_sum<_Float16>, grid, block, 0, st, a);
-  else hipLaunchKernelGGL(col_sum<__bf16>, grid, block, 0, st, a);
-  return hipGetLastError();
+  const dim3 grid((unsigned)((a.width + 63) / 64));
+  if (out_dtype == kF32) return launch_kernel(col_sum<float>, grid, 1024, st, a);
+  if (out_dtype == kF16) return launch_kernel(col_sum<_Float16>, grid, 1024, st, a);
+  return launch_kernel(col_sum<__bf16>, grid, 1024, st, a);
 }
 
 }  // namespace ringar

@@ -53,3 +53,31 @@ def test_a_workspace_whose_counters_were_not_cleared_is_not_used(fake):
         assert len(names) == 2 and "fill_u64" in names[0] and "gemm_rows" in names[1], names
         assert fake.fake_mallocs() == 2 and fake.fake_frees() == 1
     """)
+
+
+def test_an_error_of_somebody_elses_call_is_not_the_operators(fake):
+    """An error that another runtime call has left on the thread: every
+    operator still runs, first use of the workspace included, and leaves it
+    for whoever asks."""
+    host_runtime.run(fake, """
+        many = dict(rows=300, in_features=256, out_features=512)
+        for name, args in (("ringar_layer_norm", norm()), ("ringar_layer_norm_backward", norm_back(rows=400)), ("ringar_linear", lin()),
+                           ("ringar_gated_ffn", lin()), ("ringar_linear", lin(**many, ldx=256, ldw=256, ldy=512, ldp=512)),
+                           ("ringar_linear_backward", lin_back()), ("ringar_gated_ffn_backward", lin_back(ldp=64)),
+                           ("ringar_linear_backward", lin_back(**many, ldx=256, ldw=256, lddx=256, lddw=256, lddy=512, ldp=512))):
+            fake.fake_stale_error(2)
+            assert on(name, args, 0x1000) == 0, (name, ra.ringar_last_error())
+            assert fake.hipGetLastError() == 2, name
+    """)
+
+
+def test_a_failed_call_leaves_no_error_behind(fake):
+    host_runtime.run(fake, """
+        fake.fake_fail(b"norm_forward")
+        assert on("ringar_layer_norm", norm(), 0) == ra.DEVICE and fake.hipGetLastError() == 0
+        assert on("ringar_layer_norm", norm(), 0) == 0
+        # a workspace beyond the memory
+        far = lin_back(rows=1 << 20, out_features=1 << 18, in_features=1 << 12, ldx=1 << 12, ldw=1 << 12, lddx=1 << 12, lddw=1 << 12,
+                       lddy=1 << 18, ldp=1 << 18, **{k: (i + 1) << 46 for i, k in enumerate(("dy", "pre", "x", "weight", "dx", "dweight", "dbias"))})
+        assert on("ringar_linear_backward", far, 0) == ra.DEVICE and fake.hipGetLastError() == 0
+    """)
