@@ -10,6 +10,9 @@
 
 namespace ringar {
 
+// Blocks of a launch's dimension: the runtime counts their threads in 32 bits.
+constexpr int64_t most_blocks(int threads) { return 0xffffffffll / threads; }
+
 // Launches `kernel` and returns that launch's own error.  (hipGetLastError()
 // would return any error that an earlier call, not the library's perhaps, has
 // left behind; a failed launch leaves none, as the result tells of it.)
@@ -252,7 +255,7 @@ struct GemmArgs {
   int splits;            // parts of k, each a multiple of the tile's k
   int k_per_split;
   int tile_first;        // tiles of this launch (of twice the kernel's tile
-  int tile_count;        // either way where `quarters`: four blocks each)
+  int tile_count;        // either way where `quarters`: four blocks each; kRows: of columns)
   bool quarters;
   int tail_count;        // kTile256: tiles left to 128 x 128 blocks
   float* part;           // splits > 1: [splits][m][n, gated 2n]

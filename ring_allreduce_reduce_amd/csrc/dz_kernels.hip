@@ -126,9 +126,8 @@ template <typename T> hipError_t pack(PackArgs& a, hipStream_t st) {
   constexpr int V = 16 / sizeof(T);
   int64_t total = 0;
   for (PackArgs::One& o : a.one) {
-    const int64_t blocks = (o.rows * (o.ld_to / V) + 255) / 256;
+    const int64_t blocks = (o.rows * (o.ld_to / V) + 255) / 256;   // few enough: plan_gemm
     total += blocks;
-    if (total > 0x7fffffff) return hipErrorInvalidValue;
     o.blocks = (unsigned)blocks;
   }
   return total ? launch_kernel(pack_rows<T, V>, dim3((unsigned)total), 256, st, a) : hipSuccess;

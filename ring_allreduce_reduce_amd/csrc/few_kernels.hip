@@ -162,8 +162,9 @@ template <typename T, int V, int M> hipError_t launch(const FewArgs& a, hipStrea
 // where the products took 30.6, 30.2 and 30.7; at 8 rows of fp32 39 against
 // 58.  Small weights are near each other (512 x 512: 9.2 and 12.6 us, 192 x
 // 384: 10.1 and 9.4), without dx the pass has one launch (5.4 and 8 us).
+// The launch that adds the parts takes a block for every 64 values of dx.
 bool few_rows(int dtype, int64_t rows, int64_t wide, int64_t k) {
-  return rows >= 1 && rows <= (dtype == kF32 ? 8 : 4) && k >= 8 && wide >= 1 && wide <= 65535ll * kMostN;
+  return (rows * k + 63) / 64 <= most_blocks(1024) && rows >= 1 && rows <= (dtype == kF32 ? 8 : 4) && k >= 8 && wide >= 1 && wide <= 65535ll * kMostN;
 }
 
 // Columns across, rows of W a block, parts of dx.

@@ -71,10 +71,11 @@ struct Choice {
 
 // 256 x 256 tiles run one to a CU: a few left over for a last round are done
 // in quarters by 128 x 128 blocks, which take less than half as long (2500 x
-// 4096 x 2 * 10240 bf16: 800 tiles, 32 of them in quarters).
+// 4096 x 2 * 10240 bf16: 800 tiles, 32 of them in quarters).  Both run in one
+// launch, whose blocks must be few enough for it.
 int tail_of(int variant, int splits, int64_t tiles) {
   const int left = (int)(tiles % 256);
-  return variant == kTile256 && splits == 1 && tiles > 256 && left <= 64 ? left : 0;
+  return variant == kTile256 && splits == 1 && tiles > 256 && tiles < most_blocks(512) - 256 && left <= 64 ? left : 0;
 }
 
 // The cheapest split of one kernel: parts of k fill the GPU where the output
@@ -126,6 +127,7 @@ static GemmPlan plan_tiles(int dtype, int epi, const GemmArgs& given, int only, 
     const int64_t per = ceil_div(turns, splits) * turn;
     a.k_per_split = (int)(per < a.k ? per : a.k);
     a.splits = a.k ? (int)ceil_div(a.k, per) : 1;
+    a.tile_count = (int)tiles;
     p.bytes = a.splits > 1 ? (size_t)tiles * a.splits * a.m * 16 * 4 : 0;
     return p;
   }
@@ -146,7 +148,8 @@ static GemmPlan plan_tiles(int dtype, int epi, const GemmArgs& given, int only, 
   }
   if (!ok_a || !ok_b) {
     const double copies = 3.5 + (ok_a ? 0 : copy_us(rows_a, p.packed_a)) + (ok_b ? 0 : copy_us(rows_b, p.packed_b));
-    const bool fits = ((arow ? 256 : 64) * p.packed_a + 64) * es < (1ll << 32) - 4096 &&
+    const int64_t packs = (ok_a ? 0 : rows_a * p.packed_a) + (ok_b ? 0 : rows_b * p.packed_b);
+    const bool fits = packs / (16 / es) / 256 < most_blocks(256) - 2 && ((arow ? 256 : 64) * p.packed_a + 64) * es < (1ll << 32) - 4096 &&
                       ((brow ? 256 + (epi == kEpiGated ? a.n : 0) : 64) * p.packed_b + 64) * es < (1ll << 32) - 4096;
     const Choice staged = cheapest(kStaged64, epi, es, a);
     best.us += copies;
@@ -193,6 +196,9 @@ bool plan_gradients(int dtype, const GemmArgs& x, const GemmArgs& w, GemmPlan* p
     Choice tx = {}, tw = {};
     const GemmPlan qx = plan_tiles(dtype, kEpiStore, x, v, &tx), qw = plan_tiles(dtype, kEpiStore, w, v, &tw);
     if (qx.args.variant != v || qw.args.variant != v || qx.too_many || qw.too_many) continue;
+    // one launch, with a block for every 64 of the bias's column sums
+    const int64_t blocks = (int64_t)qx.args.tile_count * qx.args.splits + (int64_t)qw.args.tile_count * qw.args.splits + w.m / 64 + 1;
+    if (blocks > most_blocks(v == kTile128 ? 512 : 256)) continue;
     // The blocks share the CUs: the longer product's time alone, or all their
     // steps at the CU's throughput; a start and a launch less.
     const Cost c = cost_of(v, kEpiStore, es, true, false);

@@ -9,6 +9,19 @@ namespace ringar {
 
 inline unsigned blocks_of(const GemmArgs& a) { return (unsigned)a.tile_count * (a.quarters ? 4 : 1) * (unsigned)a.splits; }
 
+// A product's tiles in as many launches as their blocks need.
+template <typename F> hipError_t in_parts(const GemmArgs& all, int threads, F launch_part) {
+  GemmArgs a = all;
+  const int64_t most = most_blocks(threads) / a.splits, end = (int64_t)a.tile_first + a.tile_count;
+  hipError_t e = hipSuccess;
+  for (int64_t at = a.tile_first; at < end && e == hipSuccess; at += most) {
+    a.tile_first = (int)at;
+    a.tile_count = (int)(end - at < most ? end - at : most);
+    e = launch_part(a);
+  }
+  return e;
+}
+
 template <typename T, bool AROW, bool BROW, int EPI> struct Kernels {
   using Large = GemmTile<T, AROW, BROW, EPI, 256, 256, 2, 4, true>;
   using Middle = GemmTile<T, AROW, BROW, EPI, 128, 128, 4, 2, true>;
@@ -20,7 +33,7 @@ template <typename T, bool AROW, bool BROW, int EPI> struct Kernels {
 template <typename T, bool AROW, bool BROW, int EPI> hipError_t launch_tiled(const GemmArgs& a, hipStream_t st) {
   using K = Kernels<T, AROW, BROW, EPI>;
   auto go = [&](auto kernel, int threads) {
-    return launch_kernel(kernel, dim3(blocks_of(a)), threads, st, a);
+    return in_parts(a, threads, [&](const GemmArgs& part) { return launch_kernel(kernel, dim3(blocks_of(part)), threads, st, part); });
   };
   switch (a.variant) {
     case kTile256:
@@ -36,12 +49,11 @@ template <typename T, bool AROW, bool BROW, int EPI> hipError_t launch_tiled(con
       return hipErrorInvalidValue;
     case kRows:
       if constexpr (EPI != kEpiStore) {
-        const dim3 grid((unsigned)(rows_tiles(EPI, a.n) * a.splits));
         const bool halves = ((uintptr_t)a.a | (uintptr_t)a.b | (uintptr_t)(a.sam | a.sbn) * sizeof(T)) % 4 != 0;
         if constexpr (sizeof(T) == 2) {
-          if (halves) return launch_kernel(gemm_rows<T, EPI, 8, true>, grid, 512, st, a);
+          if (halves) return go(gemm_rows<T, EPI, 8, true>, 512);
         }
-        return launch_kernel(gemm_rows<T, EPI, 8, false>, grid, 512, st, a);
+        return go(gemm_rows<T, EPI, 8, false>, 512);
       }
       return hipErrorInvalidValue;
     case kTile128: return go(gemm_tile<typename K::Middle, 4>, 512);

@@ -43,7 +43,7 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_rows(GemmArgs a) {
   constexpr int kK = 4 * kVec, kStep = U * kK;
   constexpr int kCols = EPI == kEpiGated ? 8 : 16;    // outputs of a block
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = lane & 15, g = lane >> 4;
-  const int tile = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
+  const int tile = a.tile_first + blockIdx.x / a.splits, split = blockIdx.x % a.splits;
   const int64_t n0 = (int64_t)tile * kCols;
   const int k_end = a.k - split * a.k_per_split < a.k_per_split ? a.k : (split + 1) * a.k_per_split;
   const int64_t col = n0 + t % kCols < a.n ? n0 + t % kCols : a.n - 1;   // past the edge: the last column again, not stored

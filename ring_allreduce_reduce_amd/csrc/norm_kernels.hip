@@ -199,26 +199,27 @@ __global__ __launch_bounds__(TPR < kBlock ? kBlock : TPR) void norm_forward(Norm
 // Rows too long for the registers: three passes, the later two from cache.
 template <typename T, typename W> __global__ __launch_bounds__(1024) void norm_forward_long(NormArgs a) {
   __shared__ float smem[16];
-  const int64_t row = blockIdx.x;
-  const T* x = (const T*)a.x + row * a.ldx;
-  float s = 0.0f;
-  for (int64_t c = threadIdx.x; c < a.cols; c += 1024) s += (float)x[c];
-  const float mean = row_sum<1024>(s, smem) * a.inv_cols;
-  s = 0.0f;
-  for (int64_t c = threadIdx.x; c < a.cols; c += 1024) {
-    const float e = (float)x[c] - mean;
-    s = fmaf(e, e, s);
-  }
-  const float rstd = 1.0f / sqrtf(row_sum<1024>(s, smem) * a.inv_cols + a.eps);
-  if (threadIdx.x == 0) {
-    if (a.mean) a.mean[row] = mean;
-    if (a.rstd) a.rstd[row] = rstd;
-  }
-  T* y = (T*)a.y + row * a.ldy;
-  for (int64_t c = threadIdx.x; c < a.cols; c += 1024) {
-    const float w = a.weight ? (float)((const W*)a.weight)[c] : 1.0f;
-    const float b = a.bias ? (float)((const W*)a.bias)[c] : 0.0f;
-    y[c] = (T)fmaf(((float)x[c] - mean) * rstd, w, b);
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* x = (const T*)a.x + row * a.ldx;
+    float s = 0.0f;
+    for (int64_t c = threadIdx.x; c < a.cols; c += 1024) s += (float)x[c];
+    const float mean = row_sum<1024>(s, smem) * a.inv_cols;
+    s = 0.0f;
+    for (int64_t c = threadIdx.x; c < a.cols; c += 1024) {
+      const float e = (float)x[c] - mean;
+      s = fmaf(e, e, s);
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<1024>(s, smem) * a.inv_cols + a.eps);
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    T* y = (T*)a.y + row * a.ldy;
+    for (int64_t c = threadIdx.x; c < a.cols; c += 1024) {
+      const float w = a.weight ? (float)((const W*)a.weight)[c] : 1.0f;
+      const float b = a.bias ? (float)((const W*)a.bias)[c] : 0.0f;
+      y[c] = (T)fmaf(((float)x[c] - mean) * rstd, w, b);
+    }
   }
 }
 
@@ -320,23 +321,24 @@ __global__ __launch_bounds__(TPR * kRows) void norm_backward(NormArgs a) {
 // dx of rows too long for the registers
 template <typename T, typename W> __global__ __launch_bounds__(1024) void norm_backward_long(NormArgs a) {
   __shared__ float smem[32];
-  const int64_t row = blockIdx.x;
-  const T* x = (const T*)a.x + row * a.ldx;
-  const T* dy = (const T*)a.dy + row * a.lddy;
-  const float mean = a.mean[row], rstd = a.rstd[row];
-  float sg = 0.0f, sgh = 0.0f;
-  for (int64_t c = threadIdx.x; c < a.cols; c += 1024) {
-    const float g = (float)dy[c] * (a.weight ? (float)((const W*)a.weight)[c] : 1.0f);
-    sg += g;
-    sgh = fmaf(g, ((float)x[c] - mean) * rstd, sgh);
-  }
-  row_sum2<1024>(sg, sgh, smem);
-  sg *= a.inv_cols;
-  sgh *= a.inv_cols;
-  T* dx = (T*)a.y + row * a.ldy;
-  for (int64_t c = threadIdx.x; c < a.cols; c += 1024) {
-    const float g = (float)dy[c] * (a.weight ? (float)((const W*)a.weight)[c] : 1.0f);
-    dx[c] = (T)(rstd * (g - sg - (((float)x[c] - mean) * rstd) * sgh));
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* x = (const T*)a.x + row * a.ldx;
+    const T* dy = (const T*)a.dy + row * a.lddy;
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float sg = 0.0f, sgh = 0.0f;
+    for (int64_t c = threadIdx.x; c < a.cols; c += 1024) {
+      const float g = (float)dy[c] * (a.weight ? (float)((const W*)a.weight)[c] : 1.0f);
+      sg += g;
+      sgh = fmaf(g, ((float)x[c] - mean) * rstd, sgh);
+    }
+    row_sum2<1024>(sg, sgh, smem);
+    sg *= a.inv_cols;
+    sgh *= a.inv_cols;
+    T* dx = (T*)a.y + row * a.ldy;
+    for (int64_t c = threadIdx.x; c < a.cols; c += 1024) {
+      const float g = (float)dy[c] * (a.weight ? (float)((const W*)a.weight)[c] : 1.0f);
+      dx[c] = (T)(rstd * (g - sg - (((float)x[c] - mean) * rstd) * sgh));
+    }
   }
 }
 
@@ -357,8 +359,14 @@ template <typename T> __global__ __launch_bounds__(256) void norm_params_long(No
 
 template <typename O> __global__ __launch_bounds__(1024) void col_sum(ColSumArgs a) {
   __shared__ float smem[16 * 64];
-  col_sum_block<O>(a, blockIdx.x, 16, smem);
+  for (unsigned block = blockIdx.x; (int64_t)block * 64 < a.width; block += gridDim.x) {
+    if (block != blockIdx.x) __syncthreads();
+    col_sum_block<O>(a, block, 16, smem);
+  }
 }
+
+// Blocks of a kernel that loops over what it has too few of.
+unsigned capped(int64_t blocks, int threads) { return (unsigned)(blocks < most_blocks(threads) ? blocks : most_blocks(threads)); }
 
 // Threads and elements per thread of a row: the smallest shape that holds it.
 template <typename T, typename W> hipError_t forward(const NormArgs& a, hipStream_t st) {
@@ -381,7 +389,7 @@ template <typename T, typename W> hipError_t forward(const NormArgs& a, hipStrea
   RINGAR_NORM(1024, 16);
 #undef RINGAR_NORM
   static_assert(kNormLongest == 1024 * 16, "the widest rows held in registers");
-  return launch_kernel(norm_forward_long<T, W>, dim3((unsigned)a.rows), 1024, st, a);
+  return launch_kernel(norm_forward_long<T, W>, dim3(capped(a.rows, 1024)), 1024, st, a);
 }
 
 template <typename T, typename W> hipError_t backward(const NormArgs& a, hipStream_t st) {
@@ -400,7 +408,7 @@ template <typename T, typename W> hipError_t backward(const NormArgs& a, hipStre
   RINGAR_NORM(512, 32, 1);
 #undef RINGAR_NORM
   hipError_t e = hipSuccess;
-  if (a.y) e = launch_kernel(norm_backward_long<T, W>, dim3((unsigned)a.rows), 1024, st, a);
+  if (a.y) e = launch_kernel(norm_backward_long<T, W>, dim3(capped(a.rows, 1024)), 1024, st, a);
   if (e != hipSuccess || !a.part) return e;
   return launch_kernel(norm_params_long<T>, dim3((unsigned)((a.cols + 255) / 256), a.groups), 256, st, a);
 }
@@ -443,7 +451,7 @@ hipError_t launch_norm_backward(int dtype, int wdtype, const NormArgs& given, hi
 }
 
 hipError_t launch_col_sum(int out_dtype, const ColSumArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)((a.width + 63) / 64));
+  const dim3 grid(capped((a.width + 63) / 64, 1024));
   if (out_dtype == kF32) return launch_kernel(col_sum<float>, grid, 1024, st, a);
   if (out_dtype == kF16) return launch_kernel(col_sum<_Float16>, grid, 1024, st, a);
   return launch_kernel(col_sum<__bf16>, grid, 1024, st, a);

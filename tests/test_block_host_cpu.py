@@ -81,3 +81,54 @@ def test_a_failed_call_leaves_no_error_behind(fake):
                        lddy=1 << 18, ldp=1 << 18, **{k: (i + 1) << 46 for i, k in enumerate(("dy", "pre", "x", "weight", "dx", "dweight", "dbias"))})
         assert on("ringar_linear_backward", far, 0) == ra.DEVICE and fake.hipGetLastError() == 0
     """)
+
+
+def test_launches_of_the_largest_sizes(fake):
+    """A launch takes fewer than 2^32 threads along a dimension: sizes whose
+    blocks exceed that run in several launches, or in blocks that loop."""
+    host_runtime.run(fake, """
+        far = {k: (i + 1) << 46 for i, k in enumerate(("x", "weight", "y", "dy", "pre", "dx", "dweight", "dbias", "mean", "rstd", "bias"))}
+
+        def product(name, rows, k, n, wide=None, **kw):
+            wide = wide or n
+            a = dict(rows=rows, in_features=k, out_features=n, ldx=k, ldw=k, **kw)
+            back = name.endswith("backward")
+            keys = ("x", "weight", "dy", "pre", "dx", "dweight", "dbias") if back else ("x", "weight", "y", "pre", "bias")
+            a.update({key: far[key] for key in keys if key not in kw})
+            a.update(dict(lddx=k, lddw=k, lddy=n, ldp=wide) if back else dict(ldy=n, ldp=wide))
+            return (lin_back if back else lin)(**a)
+
+        def blocks_of(name, args, kernel):
+            fake.fake_reset()
+            code = on(name, args, 0x1000)
+            assert code == 0, (name, ra.ringar_last_error())
+            found = [l for l in launches() if kernel in l[0]]
+            assert found, (name, kernel, launches())
+            return sum(l[1][0] * l[1][1] for l in found)
+
+        big = 1 << 27
+        # a few rows, 16 (gated: 8) columns a block
+        assert blocks_of("ringar_linear", product("linear", 1, 8, big + 20), "gemm_rows") == big // 16 + 2
+        assert blocks_of("ringar_gated_ffn", product("gated", 2, 8, big // 2 + 20, big + 40), "gemm_rows") == big // 16 + 3
+        # tiles of 64 x 64
+        for k in (8, 7):
+            got = blocks_of("ringar_linear", product("linear", 1 << 30, k, 8), "gemm_tile")
+            assert got == 1 << 24, got
+        assert blocks_of("ringar_linear_backward", product("linear_backward", 1 << 30, 8, 8, act=0, dbias=None, dweight=None),
+                         "gemm_") == 1 << 24
+        blocks_of("ringar_linear_backward", product("linear_backward", 1 << 30, 8, 8, act=0), "gemm_")
+        blocks_of("ringar_linear_backward", product("linear_backward", 20, 8, 1 << 29, act=4), "gemm_")
+        # copies of odd rows
+        blocks_of("ringar_linear", product("linear", 1 << 28, 129, 1001, pre=None), "gemm_tile")
+        # parts of a few rows' dx
+        blocks_of("ringar_linear_backward", product("linear_backward", 4, big, 520, act=4), "")
+        blocks_of("ringar_linear_backward", product("linear_backward", 1, big, 520, act=4), "few_join")
+        # rows beyond the registers, and their parameters' gradients
+        rows, cols = 5000000, 16400
+        norms = {k: far[k] for k in ("x", "weight", "bias", "mean", "rstd")}
+        blocks_of("ringar_layer_norm", norm(rows=rows, cols=cols, ldx=cols, ldy=cols, y=far["y"], **norms), "norm_forward_long")
+        del norms["bias"]
+        for rows, cols in ((rows, cols), (3, 1 << 29)):
+            blocks_of("ringar_layer_norm_backward", norm_back(rows=rows, cols=cols, ldx=cols, lddy=cols, lddx=cols, dy=far["dy"], dx=far["dx"],
+                      dweight=far["dweight"], dbias=far["dbias"], **norms), "col_sum")
+    """)
