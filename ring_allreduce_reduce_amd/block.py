@@ -7,7 +7,8 @@ AllReduces.  Tensors are CUDA tensors of one GPU whose last dimension is
 contiguous; the dimensions before it are rows (a view that does not collapse
 to one row stride is refused, never copied).  A call enqueues on ``stream`` (a
 torch stream; default: the current one) and returns the output tensors; it is
-not recorded by autograd: gradients come from the ``_backward`` calls.
+not recorded by autograd, whatever its inputs require: gradients come from the
+``_backward`` calls.  A tensor given as ``out`` counts as changed in place.
 """
 from __future__ import annotations
 

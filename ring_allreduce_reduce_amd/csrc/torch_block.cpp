@@ -136,6 +136,12 @@ PyObject* tuple(std::initializer_list<PyObject*> v) {
   return r;
 }
 
+// A caller's tensor that the call has written: autograd must not take a value
+// that it has kept of it for unchanged.  (Inference tensors are not counted.)
+void written(const at::Tensor* t) {
+  if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 bool truth(PyObject* o, const char* what) {
   if (o != Py_True && o != Py_False) bad(std::string(what) + " must be True or False");
   return o == Py_True;
@@ -179,6 +185,7 @@ PyObject* layer_norm(PyObject* const* v) {
     a.rstd = (float*)rstd.data_ptr();
   }
   done(ringar_layer_norm(&a, call.stream()), "ringar_layer_norm");
+  written(out);
   if (!stats) return wrap(y);
   return tuple({wrap(y), wrap(mean), wrap(rstd)});
 }
@@ -264,6 +271,7 @@ PyObject* forward(PyObject* const* v) {
   }
   if (gated) done(ringar_gated_ffn(&a, call.stream()), "ringar_gated_ffn");
   else done(ringar_linear(&a, call.stream()), "ringar_linear");
+  written(out);
   if (!save_pre) return wrap(y);
   return tuple({wrap(y), wrap(pre)});
 }
