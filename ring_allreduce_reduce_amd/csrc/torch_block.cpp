@@ -29,7 +29,9 @@ struct Refusal {
 const at::Tensor* tensor(PyObject* o, const char* what) {
   if (o == Py_None) return nullptr;
   if (!THPVariable_Check(o)) bad(std::string(what) + " must be a tensor");
-  return &THPVariable_Unpack(o);
+  const at::Tensor* t = &THPVariable_Unpack(o);
+  if (t->is_neg()) bad(std::string(what) + " is a negated view (call resolve_neg() first)");
+  return t;
 }
 
 const at::Tensor& needed(PyObject* o, const char* what) {
