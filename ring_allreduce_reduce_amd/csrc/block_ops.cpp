@@ -155,9 +155,11 @@ bool overlap(const Mat& a, const Mat& b) {
   const uintptr_t ea = pa + ((uint64_t)(a.rows - 1) * a.ld + a.cols) * a.es;
   const uintptr_t eb = pb + ((uint64_t)(b.rows - 1) * b.ld + b.cols) * b.es;
   if (pa >= eb || pb >= ea) return false;
-  // columns of one array: same row stride, column ranges apart
-  if (a.rows > 1 && b.rows > 1 && a.es == b.es && a.ld == b.ld && a.ld > 0) {
-    const uint64_t pitch = (uint64_t)a.ld * a.es;
+  // columns of one array: same row stride (a single row goes by the other's),
+  // column ranges apart
+  const uint64_t pitch_a = a.rows > 1 ? (uint64_t)a.ld * a.es : 0, pitch_b = b.rows > 1 ? (uint64_t)b.ld * b.es : 0;
+  const uint64_t pitch = pitch_a ? pitch_a : pitch_b;
+  if (pitch && (a.rows == 1 || pitch_a == pitch) && (b.rows == 1 || pitch_b == pitch)) {
     const uint64_t d = pb >= pa ? (pb - pa) % pitch : (pitch - (pa - pb) % pitch) % pitch;
     if (d >= a.cols * a.es && d + b.cols * b.es <= pitch) return false;
   }
