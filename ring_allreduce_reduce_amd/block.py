@@ -73,7 +73,7 @@ def _load():
 
 
 def _act(name):
-    code = ACTS.get(name)
+    code = ACTS.get(name) if isinstance(name, str) else None
     if code is None:
         raise RingarError(INVALID_ARGUMENT, f"unknown activation {name!r}: one of {', '.join(ACTS)}")
     return code
@@ -86,6 +86,8 @@ class _On:
     def __init__(self, stream, *tensors):
         import torch
         for t in tensors:
+            if t is not None and not isinstance(t, torch.Tensor):
+                raise RingarError(INVALID_ARGUMENT, f"a tensor is needed, not {type(t).__name__}")
             if t is not None and t.is_cuda and t.get_device() != stream.device_index:
                 raise RingarError(INVALID_ARGUMENT, "the stream belongs to another GPU than the operands")
         self.stream, self.tensors, self.on = stream, tensors, torch.cuda.stream(stream)

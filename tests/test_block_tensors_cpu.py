@@ -17,3 +17,31 @@ def test_negated_views_are_refused():
         with pytest.raises(ra.RingarError, match="negated") as e:
             call()
         assert e.value.code == ra.INVALID_ARGUMENT
+
+
+def test_arguments_that_are_no_tensors_with_a_stream():
+    """Refused as they are without a stream."""
+    libutil.lib()
+    t = torch.zeros(4, 8)
+
+    class Stream:
+        device_index = 0
+
+    import ring_allreduce_reduce_amd.block as B
+    for call in (lambda s: ra.layer_norm("x", stream=s), lambda s: ra.linear(t, 3, stream=s), lambda s: ra.linear_backward(t, t, t, [1], stream=s)):
+        with pytest.raises(ra.RingarError) as e:
+            call(None)
+        assert e.value.code == ra.INVALID_ARGUMENT
+    for bad in ("x", 3, [1]):
+        with pytest.raises(ra.RingarError) as e:
+            B._On(Stream(), t, None, bad)
+        assert e.value.code == ra.INVALID_ARGUMENT
+
+
+def test_an_activation_that_is_no_name():
+    libutil.lib()
+    t = torch.zeros(4, 8)
+    for act in ([], {}, 3, None):
+        with pytest.raises(ra.RingarError) as e:
+            ra.linear(t, t, act=act)
+        assert e.value.code == ra.INVALID_ARGUMENT and "activation" in str(e.value)
