@@ -456,9 +456,9 @@ ringar_result_t ringar_chunk_range(size_t count, ringar_dtype_t dtype, int nrank
  * residual) or averages the parameter gradients.
  *
  * All of them: dtype is RINGAR_FLOAT16, RINGAR_BFLOAT16 or RINGAR_FLOAT32,
- * every sum is held in fp32 and every output is rounded once (dz, the
- * activation's gradient that the backward products read, is rounded to dtype
- * too).  Matrices are row-major with a row stride in elements (ld; at least
+ * every sum is held in fp32 and every output is rounded once (where matrix
+ * instructions take dz, the activation's gradient that the backward products
+ * read, it is rounded to dtype too).  Matrices are row-major with a row stride in elements (ld; at least
  * the row's length, or 0 on an input to repeat one row), at any element
  * alignment; rows starting at 16-byte boundaries with in_features a multiple
  * of 16 bytes take the fast path.  Sizes lie in 0 .. 2^31 - 1025; no rows is a

@@ -23,7 +23,7 @@ template <typename T, int V, int M> __global__ __launch_bounds__(256) void few_b
   __shared__ float lds[256 * (V + 1)];
   const int n0 = blockIdx.y * a.n_each;
   const int count = a.wide - n0 < a.n_each ? a.wide - n0 : a.n_each;
-  // dz of the block's rows of W, rounded as the products read it
+  // dz of the block's rows of W; it feeds fp32 multiply-adds and stays as it is
   for (int i = threadIdx.x; i < count; i += 256) {
     const int col = n0 + i, at = a.gated && col >= a.n ? col - a.n : col;
     float sum = 0.0f;
@@ -40,7 +40,7 @@ template <typename T, int V, int M> __global__ __launch_bounds__(256) void few_b
         }
       }
       sum += v;
-      dz[m][i] = (float)(T)v;
+      dz[m][i] = v;
     }
     if (a.db && blockIdx.x == 0) ((T*)a.db)[col] = (T)sum;
   }
