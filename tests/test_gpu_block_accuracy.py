@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import block_refs as R
+from block_norms import ONE_ROUNDING, TWO_ROUNDINGS, distance
 import ring_allreduce_reduce_amd as ra
 
 pytestmark = pytest.mark.gpu
@@ -51,3 +52,26 @@ def test_gradients_of_few_rows_are_rounded_once(rows, k, n, gated, dtype):
     R.assert_within(dx, want, R.rounded(dtype, want, e @ w.abs() + R.mm_error(dz.abs() + e, w, wide)), "dx")
     want = dz.T @ x
     R.assert_within(dw, want, R.rounded(dtype, want, e.T @ x.abs() + R.mm_error((dz.abs() + e).T, x, rows)), "dweight")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("rows,k,n", [(3600, 3608, 3624), (5000, 72, 5016), (7500, 64, 48), (40, 20008, 48), (333, 1023, 2050), (16, 8192, 520)])
+def test_products_sum_in_fp32(rows, k, n, gated, dtype):
+    """Relative distances of whole outputs (test_block_bounds_cpu.py: what the
+    bounds come from, and that sums in the type miss them)."""
+    rand = _gen("norms", rows, k, n, gated, dtype)
+    n = n // 2 if gated else n
+    wide = 2 * n if gated else n
+    x, w, dy = rand(rows, k, dtype=dtype), rand(wide, k, dtype=dtype, scale=k ** -0.5), rand(rows, n, dtype=dtype)
+    y, pre = (ra.gated_ffn if gated else ra.linear)(x, w, act="silu", save_pre=True)
+    z = x.double() @ w.double().T
+    act = R.act64("silu", z[:, :n]) * z[:, n:] if gated else R.act64("silu", z)
+    assert distance(pre, z) <= ONE_ROUNDING * R.UNIT[dtype]
+    assert distance(y, act) <= ONE_ROUNDING * R.UNIT[dtype]
+    dx, dw, _ = (ra.gated_ffn_backward if gated else ra.linear_backward)(dy, x, w, pre, act="silu")
+    pre, dy = pre.double(), dy.double()
+    slope = R.act64_grad("silu", pre[:, :n])
+    dz = torch.cat((dy * pre[:, n:] * slope, dy * R.act64("silu", pre[:, :n])), 1) if gated else dy * slope
+    assert distance(dx, dz @ w.double()) <= TWO_ROUNDINGS * R.UNIT[dtype]
+    assert distance(dw, dz.T @ x.double()) <= TWO_ROUNDINGS * R.UNIT[dtype]
