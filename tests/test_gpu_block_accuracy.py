@@ -75,3 +75,29 @@ def test_products_sum_in_fp32(rows, k, n, gated, dtype):
     dz = torch.cat((dy * pre[:, n:] * slope, dy * R.act64("silu", pre[:, :n])), 1) if gated else dy * slope
     assert distance(dx, dz @ w.double()) <= TWO_ROUNDINGS * R.UNIT[dtype]
     assert distance(dw, dz.T @ x.double()) <= TWO_ROUNDINGS * R.UNIT[dtype]
+
+
+def _gelu_error(dtype, z):
+    """Relative: the 16-bit types' polynomial (2.2e-5 beyond |z| = 4), the
+    exponential's and erfc's argument, rounded to fp32 (a relative u32 of it is
+    z^2 u32 of them), and a few operations."""
+    poly = 2.0 ** -15 if dtype != F32 else 0.0
+    return poly + (8 + 4 * z * z) * R.U32
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_gelu_in_its_lower_tail(dtype):
+    """Values and slopes relative to themselves, down to z = -12, where the
+    distribution is 1e-33."""
+    _gen("gelu tail", dtype)
+    z = torch.cat((torch.linspace(-12, 12, 961), torch.linspace(-1, 1, 801))).to(dtype).cuda().reshape(1, -1)
+    z64 = z.double().cpu()
+    # erfc: torch.special.ndtr cancels, to nothing at -8.3
+    cdf, density = 0.5 * torch.special.erfc(-z64 * 0.5 ** 0.5), torch.exp(-z64 * z64 / 2) / (2 * torch.pi) ** 0.5
+    err = _gelu_error(dtype, z64)
+    y = ra.linear(torch.ones(1, 1, dtype=dtype, device="cuda"), z.T.contiguous(), act="gelu")
+    want = z64 * cdf
+    R.assert_within(y, want, R.rounded(dtype, want, err * want.abs()), "gelu")
+    _, _, slope = ra.linear_backward(torch.ones_like(z), None, None, z, act="gelu", dx=False, dweight=False)
+    want = cdf + z64 * density
+    R.assert_within(slope, want[0], R.rounded(dtype, want, err * (cdf + (z64 * density).abs()))[0], "slope")
