@@ -137,7 +137,7 @@ template <bool FAST> __device__ inline void activate_grad(int act, float z, floa
       return;
     }
     case kActGeluTanh: {
-      const float zz = z * z;
+      const float zz = fminf(z * z, 1e30f);      // infinite, it would meet the zero of s (1 - s)
       const float s = sigmoid_of<FAST>(kGeluA * z * (1.0f + kGeluB * zz));
       *a = z * s;
       *d = s + z * (s * (1.0f - s)) * (kGeluA * (1.0f + 3.0f * kGeluB * zz));

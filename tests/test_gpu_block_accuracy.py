@@ -101,3 +101,21 @@ def test_gelu_in_its_lower_tail(dtype):
     _, _, slope = ra.linear_backward(torch.ones_like(z), None, None, z, act="gelu", dx=False, dweight=False)
     want = cdf + z64 * density
     R.assert_within(slope, want[0], R.rounded(dtype, want, err * (cdf + (z64 * density).abs()))[0], "slope")
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu", "sigmoid"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_slopes_where_the_square_overflows(act, dtype):
+    """Finite pre-activations far out: the slope is its limit, 0 or 1."""
+    _gen("far slopes", act, dtype)
+    z = torch.tensor([[2e18, 2e19, 1e25, 3e38]], device="cuda").to(dtype)
+    for sign, limit in ((1, 0.0 if act == "sigmoid" else 1.0), (-1, 0.0)):
+        _, _, slope = ra.linear_backward(torch.ones_like(z), None, None, sign * z, act=act, dx=False, dweight=False)
+        assert (slope == limit).all(), (sign, slope)
+        # the gated form, as the products of few rows take it
+        _, _, both = ra.gated_ffn_backward(torch.ones_like(z), None, None, torch.cat((sign * z, torch.ones_like(z)), 1), act=act, dx=False,
+                                           dweight=False)
+        assert (both[:4] == limit).all(), (sign, both)
+    nan = torch.full_like(z, float("nan"))
+    if act != "relu":
+        assert ra.linear_backward(torch.ones_like(z), None, None, nan, act=act, dx=False, dweight=False)[2].isnan().all()
