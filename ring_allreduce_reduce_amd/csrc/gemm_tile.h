@@ -101,7 +101,7 @@ template <typename T, bool ROW, int R, int NW> struct Operand {
   __device__ inline void load(int i, char* lds, int wave) {
     const uint32_t to = (uint32_t)(uintptr_t)(RINGAR_LDS void*)lds + (i * NW + wave) * 1024;
     asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(to), "v"(off[i]), "s"(desc) : "memory");
+                 :: "s"(to), "v"(off[i]), "s"(desc) : "memory", "m0");
   }
 
   // Zeros every value of a step from k = `valid` on.

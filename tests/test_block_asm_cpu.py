@@ -1,0 +1,41 @@
+"""The products' loads into LDS tell the compiler which register they change
+(compiled for gfx950 here, read as assembly)."""
+import os
+import re
+import subprocess
+
+from ring_allreduce_reduce_amd import _build
+
+SOURCE = r"""
+#include "gemm_tile.h"
+using namespace ringar;
+// a load of the tile's between two of the compiler's own to one LDS address,
+// which it holds in m0
+extern "C" __global__ void probe(const void* p, float* out) {
+  __shared__ __attribute__((aligned(1024))) char lds[2][1024];
+  Operand<float, true, 8, 1> op;
+  op.start(p, 0, 1024, 128);
+  op.offsets(128, 0, threadIdx.x, [](int r) { return r * 128; });
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p, (RINGAR_LDS void*)lds[1], 4, 0, 0);
+  op.next_step();
+  op.load(0, lds[0], 0);
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p, (RINGAR_LDS void*)lds[1], 4, 256, 0);
+  wait_loads<>();
+  out[threadIdx.x] = *(float*)(lds[0] + threadIdx.x * 4) + *(float*)(lds[1] + threadIdx.x * 4);
+}
+"""
+
+
+def test_m0_is_set_again_after_a_load_into_lds(tmp_path):
+    src, out = tmp_path / "probe.hip", tmp_path / "probe.s"
+    src.write_text(SOURCE)
+    cmd = [_build._hipcc(), *_build.HIPCC_FLAGS, "-I", _build.CSRC, "-I", os.path.join(_build.ROOT, "include"), "-x", "hip",
+           "--cuda-device-only", "-S", str(src), "-o", str(out)]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-3000:]
+    # what sets m0, and what goes by it, in order
+    steps = re.findall(r"^\s+(s_mov\w* m0|s_add\w* m0|s_lshl\w* m0|v_readfirstlane_b32 m0|buffer_load_\S+ .*\blds\b|global_load_lds\S*)", out.read_text(), re.M)
+    kinds = ["set" if "m0" in s else "load" for s in steps]
+    assert kinds.count("load") == 3, steps
+    for i, k in enumerate(kinds):
+        assert k == "set" or kinds[i - 1] == "set", steps
