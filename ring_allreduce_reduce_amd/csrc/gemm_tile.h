@@ -89,7 +89,9 @@ template <typename T, bool ROW, int R, int NW> struct Operand {
   // because the compiler would wait for them before every transposing LDS
   // read that follows, which is what the second buffer is there to avoid;
   // they have no register result, and wait_loads() waits for all of them
-  // before a barrier lets any wave read what they bring.
+  // before a barrier lets any wave read what they bring.  The LDS address is
+  // taken from m0, one instruction at least after it is set: the compiler puts
+  // a wait state there for its own loads, not before asm.
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   u32x4 desc;
   __device__ inline void next_step() {
@@ -100,8 +102,7 @@ template <typename T, bool ROW, int R, int NW> struct Operand {
   }
   __device__ inline void load(int i, char* lds, int wave) {
     const uint32_t to = (uint32_t)(uintptr_t)(RINGAR_LDS void*)lds + (i * NW + wave) * 1024;
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(to), "v"(off[i]), "s"(desc) : "memory", "m0");
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" :: "{m0}"(to), "v"(off[i]), "s"(desc) : "memory");
   }
 
   // Zeros every value of a step from k = `valid` on.

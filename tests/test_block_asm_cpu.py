@@ -26,16 +26,36 @@ extern "C" __global__ void probe(const void* p, float* out) {
 """
 
 
-def test_m0_is_set_again_after_a_load_into_lds(tmp_path):
+def _listing(tmp_path):
     src, out = tmp_path / "probe.hip", tmp_path / "probe.s"
     src.write_text(SOURCE)
     cmd = [_build._hipcc(), *_build.HIPCC_FLAGS, "-I", _build.CSRC, "-I", os.path.join(_build.ROOT, "include"), "-x", "hip",
            "--cuda-device-only", "-S", str(src), "-o", str(out)]
     r = subprocess.run(cmd, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[-3000:]
-    # what sets m0, and what goes by it, in order
-    steps = re.findall(r"^\s+(s_mov\w* m0|s_add\w* m0|s_lshl\w* m0|v_readfirstlane_b32 m0|buffer_load_\S+ .*\blds\b|global_load_lds\S*)", out.read_text(), re.M)
-    kinds = ["set" if "m0" in s else "load" for s in steps]
-    assert kinds.count("load") == 3, steps
+    # the instructions, without labels, directives and comments
+    lines = [line.split(";")[0].strip() for line in out.read_text().splitlines() if line.startswith("\t")]
+    return [line for line in lines if line and not line.startswith(".")]
+
+
+def _sets_m0(line):
+    return bool(re.match(r"\S+ m0,", line))
+
+
+def _loads_to_lds(line):
+    return bool(re.match(r"buffer_load_\S+ .*\blds\b|global_load_lds", line))
+
+
+def test_m0_is_set_again_after_a_load_into_lds(tmp_path):
+    kinds = ["set" if _sets_m0(line) else "load" for line in _listing(tmp_path) if _sets_m0(line) or _loads_to_lds(line)]
+    assert kinds.count("load") == 3
     for i, k in enumerate(kinds):
-        assert k == "set" or kinds[i - 1] == "set", steps
+        assert k == "set" or kinds[i - 1] == "set", kinds
+
+
+def test_an_instruction_lies_between_m0_and_the_load_that_takes_it(tmp_path):
+    """The hardware needs a wait state there, which the compiler adds before
+    its own loads only."""
+    lines = _listing(tmp_path)
+    after = [lines[i + 1] for i, line in enumerate(lines) if _sets_m0(line)]
+    assert after and not any(_loads_to_lds(line) for line in after), after
