@@ -4,6 +4,8 @@ import os
 import re
 import subprocess
 
+import pytest
+
 from ring_allreduce_reduce_amd import _build
 
 SOURCE = r"""
@@ -26,9 +28,11 @@ extern "C" __global__ void probe(const void* p, float* out) {
 """
 
 
-def _listing(tmp_path):
-    src, out = tmp_path / "probe.hip", tmp_path / "probe.s"
-    src.write_text(SOURCE)
+def _listing(tmp_path, src=None):
+    out = tmp_path / "listing.s"
+    if src is None:
+        src = tmp_path / "probe.hip"
+        src.write_text(SOURCE)
     cmd = [_build._hipcc(), *_build.HIPCC_FLAGS, "-I", _build.CSRC, "-I", os.path.join(_build.ROOT, "include"), "-x", "hip",
            "--cuda-device-only", "-S", str(src), "-o", str(out)]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -59,3 +63,34 @@ def test_an_instruction_lies_between_m0_and_the_load_that_takes_it(tmp_path):
     lines = _listing(tmp_path)
     after = [lines[i + 1] for i, line in enumerate(lines) if _sets_m0(line)]
     assert after and not any(_loads_to_lds(line) for line in after), after
+
+
+@pytest.mark.parametrize("unit", ["gemm_nt_f32.hip", "gemm_nn_bf16.hip", "gemm_tn_bf16.hip"])
+def test_loads_into_lds_of_the_products(unit, tmp_path):
+    """In the kernels as built: a wait state after m0, and no scalar that a
+    load takes written by a vector instruction within five wait states (the
+    compiler looks after neither before asm)."""
+    lines = _listing(tmp_path, os.path.join(_build.CSRC, unit))
+    loads = [i for i, line in enumerate(lines) if _loads_to_lds(line)]
+    assert loads
+    for at in loads:
+        first, last = map(int, re.search(r"s\[(\d+):(\d+)\]", lines[at]).groups())
+        taken = {"m0"} | {f"s{i}" for i in range(first, last + 1)}
+        waited, i = 0, at - 1
+        while i >= 0 and waited < 5:
+            line = lines[i]
+            written = _scalars(line.split(None, 1)[1].split(",")[0]) if " " in line or "\t" in line else set()
+            if line.startswith("s_nop"):
+                waited += int(line.split()[1], 0) + 1
+            else:
+                assert not (line.startswith("v_") and written & taken), (line, lines[at])
+                assert not ("m0" in written and waited == 0), (line, lines[at])
+                waited += 1
+            i -= 1
+
+
+def _scalars(operand):
+    m = re.match(r"s\[(\d+):(\d+)\]$", operand.strip())
+    if m:
+        return {f"s{i}" for i in range(int(m[1]), int(m[2]) + 1)}
+    return {operand.strip()} if re.match(r"(s\d+|m0)$", operand.strip()) else set()
