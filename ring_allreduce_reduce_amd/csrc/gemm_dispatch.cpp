@@ -99,6 +99,25 @@ Choice cheapest(int variant, int epi, int es, const GemmArgs& a) {
   return best;
 }
 
+// Rows up to which the forward product streams the weight (kRows), `direct`:
+// the tiles could load both operands as they lie.  Measured over 1 .. 16 rows, k of
+// 64 .. 8192 and 1024 .. 65536 weight rows (gated: both), us of the tiles and of the
+// stream:
+//   fp32: the stream wins everywhere but at k = 64 with 32768 rows or more (6.0,
+//     7.3): 16 x 4096 x 4096 24.3, 19.3; x 16384 74.5, 64.4; 8 x 4095 x 16384 81, 62.
+//   16 bits, few weight rows: the stream (16 x 2048 x 4096: 10.6, 6.2; 16 x 1024 x
+//     8192: 7.2, 6.3).
+//   many of them, 9 rows and more: the tiles, which read the rows once for 128
+//     columns (16 x 4096 x 20480: 37.6, 42.6; at 9 rows equal, 37.2, 36.0).
+//   many of them, a short k: the stream's blocks end as soon as they have
+//     started (4 x 1024 x 16384: 7.7, 8.7; 8 x 256 x 65536: 8.8, 14.3; 8 x 2048 x
+//     65536: 59.7, 54.4); not where the tiles would need a copy (4 x 1023 x 16384: 16.2, 11.5).
+int most_rows(int es, int64_t k, int64_t wide, bool direct) {
+  if (es == 4 || wide < 12288) return 16;
+  if (k <= 1024 && direct) return 0;
+  return wide < 16384 ? 16 : 8;
+}
+
 }  // namespace
 
 // `only`: the one tiled kernel to consider, or -1.
@@ -113,10 +132,10 @@ static GemmPlan plan_tiles(int dtype, int epi, const GemmArgs& given, int only, 
   if (a.m == 0 || a.n == 0) return p;
   const int es = dtype == kF32 ? 4 : 2;
   const int64_t wide = epi == kEpiGated ? 2 * (int64_t)a.n : a.n;
-  // Up to 16 rows of 16 bytes or more; where the weight is large the tiles, which read the rows
-  // once for 128 columns, win from 9 on (16 x 4096 x 20480 bf16: 36 us, not
-  // 43; 16 x 4096 x 4096: 16 us, not 10).
-  if (epi != kEpiStore && a.k >= 16 / es && a.m <= (wide >= 16384 ? 8 : 16)) {
+  const bool arow = a.sak == 1, brow = a.sbk == 1;
+  const bool ok_a = operand_ok(a.a, arow ? a.sam : a.sak, arow, es, 0);
+  const bool ok_b = operand_ok(a.b, brow ? a.sbn : a.sbk, brow, es, epi == kEpiGated ? a.n : 0);
+  if (epi != kEpiStore && a.k >= 16 / es && a.m <= most_rows(es, a.k, wide, ok_a && ok_b)) {
     a.variant = kRows;
     // k over several blocks until there are two for every CU, each with
     // two steps for each of its 8 waves or more
@@ -131,9 +150,6 @@ static GemmPlan plan_tiles(int dtype, int epi, const GemmArgs& given, int only, 
     p.bytes = a.splits > 1 ? (size_t)tiles * a.splits * a.m * 16 * 4 : 0;
     return p;
   }
-  const bool arow = a.sak == 1, brow = a.sbk == 1;
-  const bool ok_a = operand_ok(a.a, arow ? a.sam : a.sak, arow, es, 0);
-  const bool ok_b = operand_ok(a.b, brow ? a.sbn : a.sbk, brow, es, epi == kEpiGated ? a.n : 0);
   // the operands as stored, and copies with padded rows
   const int64_t rows_a = arow ? a.m : a.k, cols_a = arow ? a.k : a.m, rows_b = brow ? wide : a.k, cols_b = brow ? a.k : wide;
   const int64_t pad = 128 / es;

@@ -108,8 +108,8 @@ def test_launches_of_the_largest_sizes(fake):
 
         big = 1 << 27
         # a few rows, 16 (gated: 8) columns a block
-        assert blocks_of("ringar_linear", product("linear", 1, 8, big + 20), "gemm_rows") == big // 16 + 2
-        assert blocks_of("ringar_gated_ffn", product("gated", 2, 8, big // 2 + 20, big + 40), "gemm_rows") == big // 16 + 3
+        assert blocks_of("ringar_linear", product("linear", 1, 8, big + 20, dtype=4), "gemm_rows") == big // 16 + 2
+        assert blocks_of("ringar_gated_ffn", product("gated", 2, 8, big // 2 + 20, big + 40, dtype=4), "gemm_rows") == big // 16 + 3
         # tiles of 64 x 64
         for k in (8, 7):
             got = blocks_of("ringar_linear", product("linear", 1 << 30, k, 8), "gemm_tile")
@@ -131,4 +131,24 @@ def test_launches_of_the_largest_sizes(fake):
         for rows, cols in ((rows, cols), (3, 1 << 29)):
             blocks_of("ringar_layer_norm_backward", norm_back(rows=rows, cols=cols, ldx=cols, lddy=cols, lddx=cols, dy=far["dy"], dx=far["dx"],
                       dweight=far["dweight"], dbias=far["dbias"], **norms), "col_sum")
+    """)
+
+
+def test_which_products_of_few_rows_stream_the_weight(fake):
+    """The rule's corners, as measured: 16-bit tiles take many weight rows
+    with a short k or with more than 8 rows; fp32 streams all of them."""
+    host_runtime.run(fake, """
+        far = {k: (i + 1) << 46 for i, k in enumerate(("x", "weight", "y", "bias"))}
+        def streams(dtype, rows, k, n, gated=False, pad=0):
+            fake.fake_reset()
+            args = lin(dtype=dtype, rows=rows, in_features=k, out_features=n, ldx=k + pad, ldw=k + pad, ldy=n, pre=None, **far)
+            assert on("ringar_gated_ffn" if gated else "ringar_linear", args, 0x1000) == 0
+            return any("gemm_rows" in l[0] for l in launches())
+        for rows, k, n, pad, want in ((1, 4096, 4096, 0, 1), (16, 4096, 4096, 0, 1), (17, 4096, 4096, 0, 0), (16, 1024, 8192, 0, 1),
+                                      (16, 2048, 12288, 0, 1), (4, 1024, 12288, 0, 0), (4, 1032, 16384, 0, 1), (8, 4096, 20480, 0, 1),
+                                      (9, 4096, 20480, 0, 0), (4, 1023, 16384, 0, 1), (4, 1024, 16384, 1, 1), (1, 7, 4096, 0, 0)):
+            assert streams(3, rows, k, n, pad=pad) == bool(want), (rows, k, n, pad)
+            assert streams(2, rows, k, n // 2, True, pad) == bool(want), (rows, k, n, pad)
+        for rows, k, n, want in ((16, 4096, 65536, 1), (16, 512, 65536, 1), (17, 512, 65536, 0), (9, 4095, 20480, 1), (1, 3, 64, 0), (1, 4, 64, 1)):
+            assert streams(4, rows, k, n) == bool(want), (rows, k, n)
     """)

@@ -7,20 +7,21 @@ import block_refs as R
 import ring_allreduce_reduce_amd as ra
 
 pytestmark = pytest.mark.gpu
-BF16 = torch.bfloat16
+BF16, F32 = torch.bfloat16, torch.float32
 
 
-def _rand(seed, *shape):
-    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(BF16).cuda()
+def _rand(seed, *shape, dtype=BF16):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dtype).cuda()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("gated", [False, True])
-def test_more_columns_than_one_launch(gated):
-    print("case columns", gated, flush=True)
+def test_more_columns_than_one_launch(gated, dtype):
+    print("case columns", gated, dtype, flush=True)
     n = (1 << 26 if gated else 1 << 27) + 20
     at = [0, 15, 77777, (1 << 26) - 9, n - 21, n - 20, n - 1]
-    x, some = _rand(1, 1, 8), _rand(2, 2 * len(at) if gated else len(at), 8)
-    w = torch.zeros(2 * n if gated else n, 8, dtype=BF16, device="cuda")
+    x, some = _rand(1, 1, 8, dtype=dtype), _rand(2, 2 * len(at) if gated else len(at), 8, dtype=dtype)
+    w = torch.zeros(2 * n if gated else n, 8, dtype=dtype, device="cuda")
     w[at] = some[:len(at)]
     if gated:
         w[[n + i for i in at]] = some[len(at):]
