@@ -92,7 +92,7 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 // p and c fitted to erfcx over 0 .. 13.5 by linear programming on the largest
 // weighted relative error: 4e-7 up to a = 0.5, 2.3e-6 at 2, 2.3e-5 from 4 on, where
 // a rounding of fp16 is 4.9e-4.  Its exponential is the density's.  (333 x 1024 x
-// 2048 fp16: 8.0 us, with erff 9.0.)
+// 2048 fp16: 7.6 us, with silu 7.3.)
 template <bool FAST> __device__ inline void normal(float z, float* cdf, float* density) {
   const float e = act_exp<FAST>(-0.5f * z * z);
   *density = e * kInvSqrt2Pi;

@@ -6,7 +6,7 @@
 // it twice; the sums are taken of the unrounded values.  Memory bound: each
 // thread moves 16-byte packs of one column group down its block's rows, and
 // the groups of rows leave a partial sum each (8192 x 2 * 10240 bf16 gated: 145
-// us, 5.8 TB/s; 4096 x 16384 with sums: 72 us, 5.6 TB/s).
+// us, 5.8 TB/s; 4096 x 16384 with sums: 71 us, 5.7 TB/s).
 #include "block_types.h"
 
 namespace ringar {

@@ -157,11 +157,14 @@ template <typename T, int V, int M> hipError_t launch(const FewArgs& a, hipStrea
 }  // namespace
 
 // Where the one pass wins over the products of the matrix kernels.  Its
-// multiply-adds are 2 a row and value on the vector units, so rows end it: at
-// 4096 x 4096 bf16 the call took 17.4, 23.9 and 33 us for 1, 4 and 8 rows
-// where the products took 30.6, 30.2 and 30.7; at 8 rows of fp32 39 against
-// 58.  Small weights are near each other (512 x 512: 9.2 and 12.6 us, 192 x
-// 384: 10.1 and 9.4), without dx the pass has one launch (5.4 and 8 us).
+// multiply-adds are 2 a row and value on the vector units, so rows end it.  us
+// of the call, one pass and products:
+//   4096 x 4096 bf16, 1, 2, 4 rows: 15.8, 17.8, 22.5 and 28.1, 28.1, 28.4 (8
+//     rows: 33 and 31); fp32, 1, 4, 8 rows: 30.6, 33.3, 38.2 and 50.6, 50.7, 51.5;
+//   4096 in, 16384 out, bf16, 1 and 4 rows: 50.7, 57.2 and 74.9, 75.0;
+//   small weights with dx: 512 x 512 bf16 7.1, 8.2, 11.0 and 8.0, 8.0, 8.1 (its
+//     second launch waits for the first); 8 rows of fp32 11.9 and 10.7;
+//   without dx one launch: 512 x 512 bf16, 1 and 4 rows 3.4, 4.9 and 6.6, 6.9.
 // The launch that adds the parts takes a block for every 64 values of dx.
 bool few_rows(int dtype, int64_t rows, int64_t wide, int64_t k) {
   return (rows * k + 63) / 64 <= most_blocks(1024) && rows >= 1 && rows <= (dtype == kF32 ? 8 : 4) && k >= 8 && wide >= 1 && wide <= 65535ll * kMostN;

@@ -9,8 +9,8 @@
 // added, in wave order.
 // The step after the next is on its way while one is multiplied.  Where the
 // blocks are too few to fill the GPU, k is split over several; the last of
-// them to arrive adds the parts, in their order.  1 x 4096 x 4096 bf16: 8.4 us,
-// 4.0 TB/s; 16 rows cost as one (one matrix instruction holds them all).
+// them to arrive adds the parts, in their order.  1 x 4096 x 4096 bf16: 8.1 us,
+// 4.2 TB/s, 16 rows 9.8; fp32 17.8 and 20.8 (one matrix instruction holds them all).
 #pragma once
 
 #include "gemm_kernel.h"

@@ -7,9 +7,9 @@
 // to arrive.  Within a step the fragments of one half are read while the
 // other half's matrix instructions run, and the next step's first half is
 // read across the barrier, so the matrix units wait for LDS only where a
-// wave waits for the slowest one.  8192 x 4096 x 16384 bf16: 776 us (1417
-// TFLOP/s) forward without an epilogue, 838 .. 910 with bias, gelu and the kept
-// pre-activation; the matrix units are busy 67 .. 70% of the time at the 1.9 GHz
+// wave waits for the slowest one.  8192 x 4096 x 16384 bf16: 763 us (1441
+// TFLOP/s; a library's plain product 672) forward without an epilogue, 832 with
+// bias, gelu and the kept pre-activation (884 over three sets of operands); the matrix units are busy 67 .. 70% of the time at the 1.9 GHz
 // that the power leaves.
 //
 // LDS holds an operand as it lies in memory:
