@@ -68,12 +68,14 @@ def log(msg):
 
 
 def kernel_source_hash():
-    """Hash of the device code: the kernel sources (`.hip` files and the
-    headers they include) with comments and whitespace removed, so that a
-    comment edit or a host-side change leaves a counter record valid."""
+    """Hash of the collectives' device code: their kernel sources (`.hip` files
+    and the headers they include) with comments and whitespace removed, so that
+    a comment edit, a host-side change or another operator's kernel leaves a
+    counter record valid."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "ring_allreduce_reduce_amd", "csrc")
-    for p in sorted(glob.glob(os.path.join(csrc, "*.hip")) + glob.glob(os.path.join(csrc, "*.h"))):
+    sources = ("ring_*.hip", "tree_*.hip", "captured_*.hip", "ring_*.h")
+    for p in sorted(p for s in sources for p in glob.glob(os.path.join(csrc, s))):
         with open(p) as f:
             text = f.read()
         text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)

@@ -15,7 +15,6 @@
 
 #include "block_types.h"
 #include "op_host.h"
-#include "ring_kernel.h"
 #include "ringar.h"
 
 using namespace ringar;
@@ -99,7 +98,7 @@ ringar_result_t workspace(hipStream_t st, size_t bytes, char** out) {
     w.captured_ever = false;
     const size_t want = (bytes + (4u << 20) - 1) / (4u << 20) * (4u << 20);
     HIP_TRY(hipMalloc((void**)&w.p, want));
-    const hipError_t e = launch_fill((uint64_t*)w.p, kCounterBytes / 8, 0, st);
+    const hipError_t e = launch_clear((uint32_t*)w.p, kCounters, st);
     if (e != hipSuccess) {                   // counters unset: the next call starts over
       (void)hipFree(w.p);
       w.p = nullptr;

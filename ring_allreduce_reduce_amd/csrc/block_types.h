@@ -386,5 +386,6 @@ bool few_rows(int dtype, int64_t rows, int64_t wide, int64_t k);
 size_t plan_few(int dtype, FewArgs& a);       // returns the bytes of parts
 hipError_t launch_few(int dtype, const FewArgs& a, hipStream_t st);
 hipError_t launch_pack(int dtype, PackArgs a, hipStream_t st);
+hipError_t launch_clear(uint32_t* words, unsigned count, hipStream_t st);
 
 }  // namespace ringar

@@ -133,7 +133,17 @@ template <typename T> hipError_t pack(PackArgs& a, hipStream_t st) {
   return total ? launch_kernel(pack_rows<T, V>, dim3((unsigned)total), 256, st, a) : hipSuccess;
 }
 
+// Zeros in a workspace's counters (a kernel, as every other access to them).
+__global__ __launch_bounds__(256) void clear_words(uint32_t* words, unsigned count) {
+  const unsigned i = blockIdx.x * 256 + threadIdx.x;
+  if (i < count) words[i] = 0;
+}
+
 }  // namespace
+
+hipError_t launch_clear(uint32_t* words, unsigned count, hipStream_t st) {
+  return launch_kernel(clear_words, dim3((count + 255) / 256), 256, st, words, count);
+}
 
 // Row groups: enough blocks to fill the GPU (about 2048 with the column
 // groups); a few rows stay in one, whose sums are then final.

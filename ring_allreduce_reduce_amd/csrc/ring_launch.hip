@@ -109,8 +109,8 @@ hipError_t launch_fill(uint64_t* p, uint64_t words, uint64_t value, hipStream_t 
   if (words == 0) return hipSuccess;
   uint64_t blocks = div_up(words, 256);
   if (blocks > 4096) blocks = 4096;
-  void* params[] = {&p, &words, &value};
-  return hipLaunchKernel((const void*)fill_u64_kernel, dim3((unsigned)blocks), dim3(256), params, 0, stream);
+  hipLaunchKernelGGL(fill_u64_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, p, words, value);
+  return hipGetLastError();
 }
 
 }  // namespace ringar

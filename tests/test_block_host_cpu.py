@@ -44,13 +44,13 @@ def test_a_workspace_whose_counters_were_not_cleared_is_not_used(fake):
     allocates and clears again."""
     host_runtime.run(fake, """
         args = lin(rows=4, in_features=8192, out_features=64, ldx=8192, ldw=8192, ldy=64)
-        fake.fake_fail(b"fill_u64")
+        fake.fake_fail(b"clear_words")
         assert on("ringar_linear", args, 0x1000) == ra.DEVICE
         assert launches() == []
         fake.fake_stale_error(0)
         assert on("ringar_linear", args, 0x1000) == 0
         names = [l[0] for l in launches()]
-        assert len(names) == 2 and "fill_u64" in names[0] and "gemm_rows" in names[1], names
+        assert len(names) == 2 and "clear_words" in names[0] and "gemm_rows" in names[1], names
         assert fake.fake_mallocs() == 2 and fake.fake_frees() == 1
     """)
 
