@@ -583,6 +583,161 @@ typedef struct {
 ringar_result_t ringar_linear_backward(const ringar_linear_backward_t* args, ringar_stream_t stream);
 ringar_result_t ringar_gated_ffn_backward(const ringar_linear_backward_t* args, ringar_stream_t stream);
 
+/* Root-mean-square norm over the last dimension, joined to the residual
+ * stream: s = x + residual, rounded to dtype (x itself without a residual),
+ *   y = s rstd weight,  rstd = 1 / sqrt(mean(s^2) + eps).
+ * The norm reads s as it is stored, so the backward pass, which reads it
+ * again, differentiates what ran.  sum: where s is stored, needed with a
+ * residual.  y and sum may each be x or the residual itself (same row stride).
+ * In 8 bits (4 of exponent, 3 of mantissa, largest value 448, no infinity): y is one byte a value, and
+ *   scale = max(max |y| / 448, 2^-126)
+ * over a row, or over every 128 columns of it (the last group may be
+ * shorter); the byte holds y times the scale's reciprocal, rounded to nearest
+ * even.  A row that holds NaN has a NaN scale. */
+typedef enum {
+  RINGAR_OUT_SAME = 0,       /* y has x's dtype */
+  RINGAR_OUT_FP8_ROW = 1,    /* one scale a row */
+  RINGAR_OUT_FP8_GROUP = 2   /* one scale for every 128 columns of a row */
+} ringar_out_t;
+
+typedef struct {
+  ringar_dtype_t dtype;        /* x, residual, sum; y with RINGAR_OUT_SAME */
+  ringar_dtype_t param_dtype;  /* weight: dtype or RINGAR_FLOAT32 */
+  ringar_out_t out;
+  int64_t rows, cols;          /* cols >= 1 */
+  const void* x;
+  int64_t ldx;
+  const void* residual;        /* or NULL */
+  int64_t ldr;
+  const void* weight;          /* cols values, or NULL = ones */
+  float eps;
+  void* sum;
+  int64_t lds;
+  void* y;
+  int64_t ldy;
+  float* scale;                /* 8 bits: rows x (1 or ceil(cols / 128)) values */
+  float* rstd;                 /* rows values, or NULL */
+} ringar_rms_norm_t;
+
+ringar_result_t ringar_rms_norm(const ringar_rms_norm_t* args, ringar_stream_t stream);
+
+/* Its gradients (of the norm as fp32 values: the rounding to 8 bits has
+ * none); x is the forward pass's s, with g = dy weight and h = x rstd:
+ *   dx = rstd (g - h mean(g h)) + dsum,  dweight = sum over rows of dy h.
+ * dsum: the gradient that reaches s on the residual stream's own way, or NULL.
+ * dx is the gradient of x and of the residual alike; it may be dsum itself
+ * (same row stride).  dx and dweight may be NULL (not wanted). */
+typedef struct {
+  ringar_dtype_t dtype;        /* dy, x, dsum, dx */
+  ringar_dtype_t param_dtype;  /* weight, dweight */
+  int64_t rows, cols;
+  const void* dy;
+  int64_t lddy;
+  const void* x;
+  int64_t ldx;
+  const float* rstd;
+  const void* weight;          /* or NULL = ones */
+  const void* dsum;
+  int64_t ldds;
+  void* dx;
+  int64_t lddx;
+  void* dweight;
+} ringar_rms_norm_backward_t;
+
+ringar_result_t ringar_rms_norm_backward(const ringar_rms_norm_backward_t* args, ringar_stream_t stream);
+
+/* Dropout: y = (keep ? x / (1 - p) : 0) + residual.  The mask is never
+ * stored: the gradient is the same call on dy, without a residual.
+ * Value (i, j) is kept where its 16-bit number is not below p 2^16 (p is
+ * rounded to 16 bits, and 1 - p goes by what it is rounded to).  Its number is
+ * half-word j % 8, low half first, of Philox4x32-10 (Salmon et al., "Parallel
+ * random numbers: as easy as 1, 2, 3", 2011) with the key (seed's low word,
+ * high word) and the counter (column / 8, row, offset's low word, high word),
+ * where row = first_row + i and column = first_col + j: a rank that holds some
+ * rows or columns of a larger array draws that array's mask.  Calls that
+ * shall differ take another offset (or seed); more_offset, a value in device
+ * memory that is added to it, lets a captured call draw another mask at every
+ * replay.  y may be x or the residual itself (same row stride). */
+typedef struct {
+  ringar_dtype_t dtype;
+  int64_t rows, cols;
+  const void* x;
+  int64_t ldx;
+  const void* residual;        /* or NULL */
+  int64_t ldr;
+  double p;                    /* 0 .. 1 */
+  uint64_t seed, offset;
+  const int64_t* more_offset;  /* or NULL */
+  int64_t first_row;           /* first_row + rows at most 2^32 */
+  int64_t first_col;           /* a multiple of 8 */
+  void* y;
+  int64_t ldy;
+} ringar_dropout_t;
+
+ringar_result_t ringar_dropout(const ringar_dropout_t* args, ringar_stream_t stream);
+
+/* Attention to an encoder's states: queries and keys of unlike lengths, every
+ * query to every key of its sequence,
+ *   P = softmax over keys of (scale q k^T),  y = P v,
+ * for each sequence and head; heads / kv_heads neighbouring query heads share a key head.
+ * Arrays have three strides, in elements: of the sequence (batch), the row and the head; the
+ * head_dim values of a row are contiguous.
+ *   key_lengths: keys of each sequence (device memory, limited to 0 .. keys),
+ *     or NULL: keys.  What lies past them is never read into a result.
+ *   lse: log sum exp(scale q k^T) of every row, batch x heads x queries, or NULL.
+ * A row without keys gives zeros, and an lse of -infinity.
+ * head_dim is a multiple of 8 (fp32: 4) up to 128; rows start at 16-byte
+ * boundaries; row strides are below 2^25 bytes; scale is above zero.  16-bit
+ * types round P to their type before it meets v.  An output's span must not
+ * overlap another operand's. */
+typedef struct {
+  ringar_dtype_t dtype;
+  int64_t batch, queries, keys, heads, kv_heads, head_dim;
+  const void* q;               /* batch x queries x heads x head_dim */
+  int64_t q_strides[3];
+  const void* k;               /* batch x keys x kv_heads x head_dim */
+  int64_t k_strides[3];
+  const void* v;
+  int64_t v_strides[3];
+  const int32_t* key_lengths;
+  float scale;
+  void* y;                     /* like q */
+  int64_t y_strides[3];
+  float* lse;
+} ringar_cross_attention_t;
+
+ringar_result_t ringar_cross_attention(const ringar_cross_attention_t* args, ringar_stream_t stream);
+
+/* Its gradients, from the forward pass's y and lse.  With dP = dy v^T,
+ * delta = sum over head_dim of dy y and dS = P (dP - delta), rounded to a
+ * 16-bit dtype before the products that read it:
+ *   dq = scale dS k,  dk = scale dS^T q,  dv = P^T dy,
+ * summed over the query heads that share a key head; keys past a sequence's
+ * length get zeros.  dq (like q), dk and dv (like k) are contiguous; any of
+ * them may be NULL (not wanted). */
+typedef struct {
+  ringar_dtype_t dtype;
+  int64_t batch, queries, keys, heads, kv_heads, head_dim;
+  const void* dy;
+  int64_t dy_strides[3];
+  const void* q;
+  int64_t q_strides[3];
+  const void* k;
+  int64_t k_strides[3];
+  const void* v;
+  int64_t v_strides[3];
+  const void* y;
+  int64_t y_strides[3];
+  const float* lse;
+  const int32_t* key_lengths;
+  float scale;
+  void* dq;
+  void* dk;
+  void* dv;
+} ringar_cross_attention_backward_t;
+
+ringar_result_t ringar_cross_attention_backward(const ringar_cross_attention_backward_t* args, ringar_stream_t stream);
+
 /* Asynchronous errors ([BOOK] §1.4: ncclCommGetAsyncError reports what went
  * wrong after the call returned; [ARCH] §九.5: a kernel only leaves its wait
  * loops through the abort flag).  Waits for `stream`, then returns (and

@@ -398,5 +398,6 @@ def all_gather(sends, recvs, nchannels=0, proto="auto", stream=None, **cfg_kwarg
 
 
 # ------------------------------------------------------------------ block operators
-from .block import (gated_ffn, gated_ffn_backward, layer_norm, layer_norm_backward, linear,  # noqa: E402,F401
-                    linear_backward)
+from .attention import cross_attention, cross_attention_backward  # noqa: E402,F401
+from .block import (dropout, dropout_backward, gated_ffn, gated_ffn_backward, layer_norm,  # noqa: E402,F401
+                    layer_norm_backward, linear, linear_backward, rms_norm, rms_norm_backward, rms_norm_fp8)

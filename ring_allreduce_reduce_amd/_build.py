@@ -18,7 +18,9 @@ _TYPES = ("i8", "i32", "f16", "bf16", "f32", "f64")
 SOURCES = ([f"tree_{t}.hip" for t in _TYPES] + [f"ring_kernel_{t}.hip" for t in _TYPES] +
            [f"ring_rs_{t}.hip" for t in _TYPES] + [f"captured_{t}.hip" for t in _TYPES] +
            ["ring_ag.hip", "ring_launch.hip", "ringar.cpp"] +
-           ["norm_kernels.hip", "dz_kernels.hip", "few_kernels.hip", "gemm_dispatch.cpp", "block_ops.cpp"] +
+           ["norm_kernels.hip", "dz_kernels.hip", "few_kernels.hip", "gemm_dispatch.cpp", "block_ops.cpp",
+            "rms_kernels.hip", "dropout_kernels.hip", "layer_ops.cpp", "attn_common.hip", "attention_ops.cpp"] +
+           [f"attn_{way}_{t}.hip" for way in ("fwd", "bwd") for t in ("f16", "bf16", "f32")] +
            [f"gemm_{lay}_{t}.hip" for lay in ("nt", "nn", "tn", "pair") for t in ("f16", "bf16", "f32")])
 
 HIPCC_FLAGS = [
@@ -54,12 +56,12 @@ def build_ext() -> str:
            "/opt/rocm/include", sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
-           *[a for i in inc for a in ("-isystem", i)], os.path.join(CSRC, "torch_block.cpp"), "-o", EXT + ".tmp",
+           *[a for i in inc for a in ("-isystem", i)], os.path.join(CSRC, "torch_block.cpp"), os.path.join(CSRC, "torch_layer.cpp"), "-o", EXT + ".tmp",
            "-L", HERE, "-lringar", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(base, "lib"), "-Wl,-rpath," + os.path.join(base, "lib"),
            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on torch_block.cpp:\n{r.stderr}")
+        raise RuntimeError(f"g++ failed on the torch binding:\n{r.stderr}")
     os.replace(EXT + ".tmp", EXT)
     return EXT
 

@@ -1,0 +1,305 @@
+// Cross attention, backward.
+//
+//   P = exp(s - lse),  dP = dy v^T,  delta = sum dy y,  dS = P (dP - delta)
+//   dq = scale dS k,  dk = scale dS^T q,  dv = P^T dy
+//
+// Two kernels, each of which computes S and dP again for what it sums over, so
+// that every gradient is added up in one block's registers, in an order that
+// is always the same (no atomics): 7 products in place of 5.
+//   dq: a wave holds 32 query rows (Q, dy in fragments, dq^T in result
+//   registers) and goes along the keys; S^T and dP^T have a row a lane.
+//   dk, dv: a wave holds 32 keys (K, V in fragments, dk^T and dv^T in result
+//   registers) and goes along the query rows of every head that shares them;
+//   S and dP have a key a lane.
+// P and dS are the next product's operand as they stand (attn_tile.h), rounded
+// to the operands' type: what the matrix instructions take.  fp16 holds P times
+// 2^10 where it meets dy, so that the small P of long rows keep their bits.
+#pragma once
+
+#include "attn_tile.h"
+
+namespace ringar {
+
+template <typename T> struct Shift {
+  static constexpr float kLog2 = sizeof(T) == 2 && !std::is_same_v<T, __bf16> ? 10.0f : 0.0f;
+  static constexpr float kBack = kLog2 > 0.0f ? 0x1p-10f : 1.0f;
+};
+
+// lse in powers of two (+infinity where a row has no keys, so that its P are
+// 0), and delta.  16 lanes a row, 8 values each at head_dim 128.
+template <typename T> __global__ __launch_bounds__(256) void attn_delta(AttnArgs a) {
+  constexpr int kChunk = 16 / sizeof(T);
+  const int t = threadIdx.x & 15;
+  const int64_t rows = (int64_t)a.batch * a.heads * a.queries;
+  for (int64_t i = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); i < rows; i += (int64_t)gridDim.x * 16) {
+    const int64_t query = i % a.queries, bh = i / a.queries, head = bh % a.heads, batch = bh / a.heads;
+    const T* dy = row_at<T>(a.dy, batch, head, query);
+    const T* y = row_at<T>(a.y, batch, head, query);
+    float s = 0.0f;
+    for (int d = t * kChunk; d < a.dim; d += 16 * kChunk) {
+      const Pack<T, kChunk> u = load_pack<T, kChunk>(dy + d), v = load_pack<T, kChunk>(y + d);
+#pragma unroll
+      for (int j = 0; j < kChunk; j++) s = fmaf((float)u.v[j], (float)v.v[j], s);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    if (t == 0) {
+      const float lse = a.lse[i];
+      a.lse2[i] = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+      a.delta[i] = s;
+    }
+  }
+}
+
+// ------------------------------------------------------------------------ dq
+template <typename T, int D, int KT> struct AttnDq {
+  using M = Mma32<T>;
+  using Frag = typename M::Frag;
+  static constexpr int NW = 4, kThreads = 64 * NW;
+  using Tile = RowTile<T, D, KT, NW>;
+  static constexpr int kSteps = D / M::kK, kDims = D / 32;
+  static constexpr int kShared = 4 * Tile::kBytes;
+  static constexpr int kBlocksPerCu = D * sizeof(T) > 256 ? 1 : 2;     // registers
+
+  static __device__ inline void run(const AttnArgs& a, char* smem) {
+    const AttnPlace at(a);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = (at.tile * NW + wave) * 32 + (lane & 31);
+    const bool exists = r < a.rows;
+    const int r_in = exists ? r : a.rows - 1;
+    const int head = at.head(a, r_in), query = r_in % a.queries;
+    RowFrags<T, D> q, dy;
+    q.load(row_at<T>(a.q, at.batch, head, query), exists, a.dim, lane);
+    dy.load(row_at<T>(a.dy, at.batch, head, query), exists, a.dim, lane);
+    const int64_t stat = ((int64_t)at.batch * a.heads + head) * a.queries + query;
+    const float lse2 = a.lse2[stat], delta = a.delta[stat];
+
+    const int all = (at.length + KT - 1) / KT, per = (all + a.splits - 1) / a.splits;
+    const int first = at.split * per, last = first + per < all ? first + per : all;
+    const int64_t pitch_k = a.k.row * (int64_t)sizeof(T), pitch_v = a.v.row * (int64_t)sizeof(T);
+    const char* keys = (const char*)row_at<T>(a.k, at.batch, at.kv_head, 0);
+    const char* values = (const char*)row_at<T>(a.v, at.batch, at.kv_head, 0);
+    Tile tk, tv;
+    tk.start(pitch_k, a.dim, wave, lane);
+    tv.start(pitch_v, a.dim, wave, lane);
+    auto issue = [&](int t, int buf) {
+      const int64_t row = (int64_t)t * KT, left = at.length - 1 - row;
+      char* lds = smem + buf * 2 * Tile::kBytes;
+      tk.load(buffer_of(keys + row * pitch_k, left * pitch_k + a.dim * (int)sizeof(T)), lds, wave);
+      tv.load(buffer_of(values + row * pitch_v, left * pitch_v + a.dim * (int)sizeof(T)), lds + Tile::kBytes, wave);
+    };
+    f32x16 acc[kDims];
+#pragma unroll
+    for (int i = 0; i < kDims; i++) acc[i] = zero16();
+    if (first < last) issue(first, 0);
+    for (int tile = first, buf = 0; tile < last; tile++, buf ^= 1) {
+      wait_lds();
+      block_barrier();
+      if (tile + 1 < last) issue(tile + 1, buf ^ 1);
+      const char* lk = smem + buf * 2 * Tile::kBytes;
+      const char* lv = lk + Tile::kBytes;
+      const int left = at.length - tile * KT;
+#pragma unroll
+      for (int b = 0; b < KT / 32; b++) {
+        f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+        for (int i = 0; i < kSteps; i++) {
+          s = M::run(Tile::rows(lk, b * 32, i, lane), q.f[i], s);
+          dp = M::run(Tile::rows(lv, b * 32, i, lane), dy.f[i], dp);
+        }
+        float ds[16];
+#pragma unroll
+        for (int i = 0; i < 16; i++) ds[i] = fast_exp2(fmaf(s[i], a.scale2, -lse2)) * (dp[i] - delta);
+        if (left < KT) {
+#pragma unroll
+          for (int i = 0; i < 16; i++)
+            if (b * 32 + result_row(i, lane) >= left) ds[i] = 0.0f;
+        }
+        constexpr int kValues = 16 / sizeof(T);
+#pragma unroll
+        for (int f = 0; f < 32 / M::kK; f++) {
+          const Frag frag = result_frag<T>(ds + f * kValues);
+#pragma unroll
+          for (int i = 0; i < kDims; i++) acc[i] = M::run(Tile::cols(lk, b * 32 + f * M::kK, i * 32, lane), frag, acc[i]);
+        }
+      }
+    }
+    if (!exists) return;
+    const int64_t out = (((int64_t)at.batch * a.queries + query) * a.heads + head) * a.dim;
+#pragma unroll
+    for (int i = 0; i < kDims; i++)
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        const int d = i * 32 + result_row(j, lane);
+        if (d >= a.dim) continue;
+        if (a.splits > 1) {
+          const float v[4] = {acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]};
+          put4<float>(a.part + at.split * ((int64_t)a.batch * a.queries * a.heads * a.dim) + out + d, v);
+        } else {
+          const float v[4] = {acc[i][j] * a.scale, acc[i][j + 1] * a.scale, acc[i][j + 2] * a.scale, acc[i][j + 3] * a.scale};
+          put4<T>((T*)a.dq + out + d, v);
+        }
+      }
+  }
+};
+
+// -------------------------------------------------------------------- dk, dv
+template <typename T, int D, int QT> struct AttnDkv {
+  using M = Mma32<T>;
+  using Frag = typename M::Frag;
+  static constexpr int NW = 4, kThreads = 64 * NW;
+  using Tile = RowTile<T, D, QT, NW>;
+  static constexpr int kSteps = D / M::kK, kDims = D / 32;
+  // Q and dy, and a tile's lse2 and delta (64 floats each)
+  static constexpr int kStage = 2 * Tile::kBytes + 512;
+  static constexpr int kShared = 2 * kStage;
+  static constexpr int kBlocksPerCu = D * sizeof(T) > 256 ? 1 : 2;     // registers
+  static_assert(QT <= 64, "one load brings a tile's statistics");
+
+  static __device__ inline void run(const AttnArgs& a, char* smem) {
+    const AttnPlace at(a);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int key = (at.tile * NW + wave) * 32 + (lane & 31);
+    const bool exists = key < at.length;
+    const int key_in = exists ? key : 0;
+    const int64_t out = (((int64_t)at.batch * a.keys + key) * a.kv_heads + at.kv_head) * a.dim;
+    const int64_t part_size = (int64_t)a.batch * a.keys * a.kv_heads * a.dim;
+
+    RowFrags<T, D> k, v;
+    k.load(row_at<T>(a.k, at.batch, at.kv_head, key_in), exists, a.dim, lane);
+    v.load(row_at<T>(a.v, at.batch, at.kv_head, key_in), exists, a.dim, lane);
+
+    // tiles of query rows: of every query head, one after the other
+    const int tiles = (a.queries + QT - 1) / QT;
+    const int64_t all = at.tile * (NW * 32) < at.length ? (int64_t)a.group * tiles : 0;
+    const int64_t per = (all + a.splits - 1) / a.splits;
+    const int64_t first = at.split * per, last = first + per < all ? first + per : all;
+    const int64_t pitch_q = a.q.row * (int64_t)sizeof(T), pitch_dy = a.dy.row * (int64_t)sizeof(T);
+    Tile tq, tdy;
+    tq.start(pitch_q, a.dim, wave, lane);
+    tdy.start(pitch_dy, a.dim, wave, lane);
+    int head = at.kv_head * a.group, next = 0;          // of the tile that is issued next
+    int row_now = 0;                                    // first row of the tile in work
+    if (first < last) {
+      head += (int)(first / tiles);
+      next = (int)(first % tiles);
+      row_now = next * QT;
+    }
+    auto issue = [&](int buf) {
+      const int64_t row = (int64_t)next * QT, left = a.queries - 1 - row;
+      char* lds = smem + buf * kStage;
+      tq.load(buffer_of((const char*)row_at<T>(a.q, at.batch, head, row), left * pitch_q + a.dim * (int)sizeof(T)), lds, wave);
+      tdy.load(buffer_of((const char*)row_at<T>(a.dy, at.batch, head, row), left * pitch_dy + a.dim * (int)sizeof(T)), lds + Tile::kBytes, wave);
+      if (wave < 2) {
+        const float* stats = (wave ? a.delta : a.lse2) + ((int64_t)at.batch * a.heads + head) * a.queries + row;
+        const u32x4 buffer = buffer_of((const char*)stats, (left + 1) * 4);
+        const uint32_t to = (uint32_t)(uintptr_t)(RINGAR_LDS void*)lds + 2 * Tile::kBytes + wave * 256;
+        asm volatile("s_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" :: "{m0}"(to), "v"(lane * 4), "s"(buffer) : "memory");
+      }
+      if (++next == tiles) {
+        next = 0;
+        head++;
+      }
+    };
+
+    f32x16 dk[kDims], dv[kDims];
+#pragma unroll
+    for (int i = 0; i < kDims; i++) dk[i] = dv[i] = zero16();
+    if (first < last) issue(0);
+    int buf = 0;
+    for (int64_t tile = first; tile < last; tile++, buf ^= 1) {
+      wait_lds();
+      block_barrier();
+      if (tile + 1 < last) issue(buf ^ 1);
+      const char* lq = smem + buf * kStage;
+      const char* ldy = lq + Tile::kBytes;
+      const float* lse2 = (const float*)(ldy + Tile::kBytes);
+      const int rows_left = a.queries - row_now;        // of the tile that exist
+      row_now = row_now + QT < a.queries ? row_now + QT : 0;
+#pragma unroll
+      for (int b = 0; b < QT / 32; b++) {
+        f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+        for (int i = 0; i < kSteps; i++) {
+          s = M::run(Tile::rows(lq, b * 32, i, lane), k.f[i], s);
+          dp = M::run(Tile::rows(ldy, b * 32, i, lane), v.f[i], dp);
+        }
+        float p[16], ds[16];
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const f32x4 l = *(const f32x4*)(lse2 + b * 32 + result_row(j, lane)), delta = *(const f32x4*)(lse2 + 64 + b * 32 + result_row(j, lane));
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            p[j + e] = fast_exp2(fmaf(s[j + e], a.scale2, Shift<T>::kLog2 - l[e]));
+            ds[j + e] = p[j + e] * ((dp[j + e] - delta[e]) * Shift<T>::kBack);
+          }
+        }
+        if (rows_left < QT) {
+#pragma unroll
+          for (int j = 0; j < 16; j++)
+            if (b * 32 + result_row(j, lane) >= rows_left) p[j] = ds[j] = 0.0f;
+        }
+        constexpr int kValues = 16 / sizeof(T);
+#pragma unroll
+        for (int f = 0; f < 32 / M::kK; f++) {
+          const Frag pf = result_frag<T>(p + f * kValues), df = result_frag<T>(ds + f * kValues);
+#pragma unroll
+          for (int i = 0; i < kDims; i++) {
+            dv[i] = M::run(Tile::cols(ldy, b * 32 + f * M::kK, i * 32, lane), pf, dv[i]);
+            dk[i] = M::run(Tile::cols(lq, b * 32 + f * M::kK, i * 32, lane), df, dk[i]);
+          }
+        }
+      }
+    }
+    if (key >= a.keys) return;
+#pragma unroll
+    for (int i = 0; i < kDims; i++)
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        const int d = i * 32 + result_row(j, lane);
+        if (d >= a.dim) continue;
+        // keys past the length: zeros, whatever their columns have added up
+        float vk[4], vv[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          vk[e] = exists ? dk[i][j + e] * (a.splits > 1 ? 1.0f : a.scale) : 0.0f;
+          vv[e] = exists ? dv[i][j + e] * Shift<T>::kBack : 0.0f;
+        }
+        if (a.splits > 1) {
+          put4<float>(a.part + (2 * at.split) * part_size + out + d, vk);
+          put4<float>(a.part + (2 * at.split + 1) * part_size + out + d, vv);
+        } else {
+          if (a.dk) put4<T>((T*)a.dk + out + d, vk);
+          if (a.dv) put4<T>((T*)a.dv + out + d, vv);
+        }
+      }
+  }
+};
+
+template <typename K> __global__ __launch_bounds__(K::kThreads, K::kBlocksPerCu) void attn_dq(AttnArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[K::kShared];
+  K::run(a, smem);
+}
+template <typename K> __global__ __launch_bounds__(K::kThreads, K::kBlocksPerCu) void attn_dkv(AttnArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[K::kShared];
+  K::run(a, smem);
+}
+
+template <typename T> hipError_t attn_delta_of(const AttnArgs& a, hipStream_t st) {
+  const int64_t blocks = ((int64_t)a.batch * a.heads * a.queries + 15) / 16;
+  return launch_kernel(attn_delta<T>, dim3((unsigned)(blocks < most_blocks(256) ? blocks : most_blocks(256))), 256, st, a);
+}
+
+template <typename T> hipError_t attn_dq_of(const AttnArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)attn_blocks(a));
+  if (a.dim <= 64) return launch_kernel(attn_dq<AttnDq<T, 64, 64>>, grid, 256, st, a);
+  return launch_kernel(attn_dq<AttnDq<T, 128, sizeof(T) == 2 ? 64 : 32>>, grid, 256, st, a);
+}
+
+template <typename T> hipError_t attn_dkv_of(const AttnArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)attn_blocks(a));
+  if (a.dim <= 64) return launch_kernel(attn_dkv<AttnDkv<T, 64, 64>>, grid, 256, st, a);
+  return launch_kernel(attn_dkv<AttnDkv<T, 128, 32>>, grid, 256, st, a);
+}
+
+}  // namespace ringar

@@ -1,0 +1,5 @@
+#include "attn_forward.h"
+
+namespace ringar {
+template hipError_t attn_forward_of<_Float16>(const AttnArgs& a, hipStream_t st);
+}

@@ -1,0 +1,218 @@
+// What the attention kernels share: 32 x 32 matrix instructions, tiles of key
+// or query rows in LDS, and their fragments.
+//
+// Every product here puts the index that belongs to a lane (a row of softmax
+// statistics, or a key) into the columns of the matrix instruction's result:
+//   S^T = K Q^T   (columns: query rows)       S = Q K^T    (columns: keys)
+// A result's lane l holds column l % 32 and of the 32 rows those that
+// result_row() names, four neighbours at a time.  The product that follows
+// contracts over just these rows, and a contraction may take its terms in any
+// order, the same on both sides: a lane's result values, rounded to the
+// operands' type, are the second operand of the next product as they stand, no
+// exchange between lanes.  The first operand follows that order: 16-bit ones
+// through the transposing LDS read, which returns four rows at a time, fp32
+// ones value by value.
+#pragma once
+
+#include "attn_types.h"
+
+namespace ringar {
+
+#define RINGAR_LDS __attribute__((address_space(3)))
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// kK: terms of the contraction a step takes; a lane's fragment is the 16-byte
+// chunk of its half (lane / 32), so a step takes two chunks of a row.
+template <typename T> struct Mma32;
+template <> struct Mma32<_Float16> {
+  typedef _Float16 Frag __attribute__((ext_vector_type(8)));
+  static constexpr int kK = 16;
+  static __device__ inline f32x16 run(Frag a, Frag b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+};
+template <> struct Mma32<__bf16> {
+  typedef __bf16 Frag __attribute__((ext_vector_type(8)));
+  static constexpr int kK = 16;
+  static __device__ inline f32x16 run(Frag a, Frag b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
+};
+template <> struct Mma32<float> {
+  typedef float Frag __attribute__((ext_vector_type(4)));
+  static constexpr int kK = 8;
+  static __device__ inline f32x16 run(Frag a, Frag b, f32x16 c) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
+    return c;
+  }
+};
+
+__device__ inline int result_row(int reg, int lane) { return (reg & 3) + 8 * (reg >> 2) + 4 * (lane >> 5); }
+
+// Values first .. of a result as a fragment of the contraction over its rows.
+template <typename T> __device__ inline typename Mma32<T>::Frag result_frag(const float* v) {
+  typename Mma32<T>::Frag f;
+#pragma unroll
+  for (int i = 0; i < 16 / (int)sizeof(T); i++) f[i] = (T)v[i];
+  return f;
+}
+
+__device__ inline f32x16 zero16() { return f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0}; }
+
+__device__ inline float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Waits until the wave's loads into LDS have landed and its reads are done;
+// the empty asm keeps memory accesses from moving over it.
+__device__ inline void wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x70);
+  asm volatile("" ::: "memory");
+}
+__device__ inline void block_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// A buffer from `base` on, of `bytes` (what lies beyond reads as zero).
+__device__ inline u32x4 buffer_of(const char* base, int64_t bytes) {
+  const uint32_t size = bytes <= 0 ? 0u : bytes > 0x7fffffff ? 0x7fffffffu : (uint32_t)bytes;
+  return u32x4{(uint32_t)(uintptr_t)base, (uint32_t)((uintptr_t)base >> 32), size, 0x00027000u};
+}
+
+// R rows of D values in LDS, brought by NW waves straight from memory: lines of
+// 128 bytes, R of them for each 128 bytes of a row, the eight 16-byte chunks of
+// a line in the order c ^ turn(row).  turn() lets both kinds of reads spread
+// over all banks: eight rows of one chunk (rows of like parity lie in one half
+// of the banks, four turns keep them apart there), and four rows of 64 bytes
+// (rows k and k + 2 in different halves of their lines).
+template <typename T, int D, int R, int NW> struct RowTile {
+  static constexpr int kChunk = 16 / sizeof(T);
+  static constexpr int kLines = D * (int)sizeof(T) / 128;
+  static constexpr int kBytes = R * D * (int)sizeof(T);
+  static constexpr int kLoads = kBytes / 1024 / NW;
+  static_assert(kLoads * NW * 1024 == kBytes && R % 32 == 0, "every wave loads the same share");
+  static constexpr uint32_t kOutside = 0x80000000u;   // past the end of any buffer
+
+  static __device__ inline int turn(int row) { return (row & 2) << 1 | (row & 4) >> 1; }
+
+  uint32_t off[kLoads];
+
+  // `pitch`: bytes from row to row; chunks from `dim` on read as zero
+  __device__ inline void start(int64_t pitch, int dim, int wave, int lane) {
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) {
+      const int idx = i * NW + wave;
+      const int row = idx % (R / 8) * 8 + (lane >> 3), chunk = idx / (R / 8) * 8 + ((lane & 7) ^ turn(lane >> 3));
+      off[i] = chunk * kChunk < dim ? (uint32_t)(row * pitch) + chunk * 16 : kOutside;
+    }
+  }
+  // Starts the loads.  They are asm because the compiler would wait for them
+  // before every LDS read that follows; wait_lds() and a barrier come before
+  // anything reads what they bring.  The LDS address is taken from m0, one
+  // instruction at least after it is set.
+  __device__ inline void load(u32x4 buffer, char* lds, int wave) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) {
+      const uint32_t to = (uint32_t)(uintptr_t)(RINGAR_LDS void*)lds + (i * NW + wave) * 1024;
+      asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" :: "{m0}"(to), "v"(off[i]), "s"(buffer) : "memory");
+    }
+  }
+
+  using Frag = typename Mma32<T>::Frag;
+  // Rows r0 .. r0 + 31 as the lanes' index, step s of the contraction over D.
+  static __device__ inline Frag rows(const char* lds, int r0, int s, int lane) {
+    const int t = lane & 31, c = 2 * s + (lane >> 5);
+    return *(const Frag*)(lds + c / 8 * (R * 128) + (r0 + t) * 128 + (((c & 7) ^ turn(t)) << 4));
+  }
+  // Columns c0 .. c0 + 31 as the lanes' index, contraction over rows r0 .. in the
+  // order of a result's values (r0: a multiple of kK).
+  static __device__ inline Frag cols(const char* lds, int r0, int c0, int lane) {
+    if constexpr (sizeof(T) == 2) {
+      // source lane t of 16 gives row t / 4 and four columns; after the
+      // transposing read lane t holds column t of the four rows
+      typedef short s16x4 __attribute__((ext_vector_type(4)));
+      typedef short s16x8 __attribute__((ext_vector_type(8)));
+      const int t = lane & 15, col = c0 + (lane & 16) + (t & 3) * 4;
+      s16x4 v[2];
+#pragma unroll
+      for (int q = 0; q < 2; q++) {
+        const int row = r0 + 8 * q + 4 * (lane >> 5) + (t >> 2), chunk = col / 8;
+        const char* p = lds + chunk / 8 * (R * 128) + row * 128 + (((chunk & 7) ^ turn(row)) << 4) + (col & 7) * 2;
+        v[q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((RINGAR_LDS s16x4*)(RINGAR_LDS void*)p);
+      }
+      const s16x8 w = {v[0][0], v[0][1], v[0][2], v[0][3], v[1][0], v[1][1], v[1][2], v[1][3]};
+      return __builtin_bit_cast(Frag, w);
+    } else {
+      const int col = c0 + (lane & 31), chunk = col / 4;
+      Frag f;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int row = r0 + 4 * (lane >> 5) + i;
+        f[i] = *(const float*)(lds + chunk / 8 * (R * 128) + row * 128 + (((chunk & 7) ^ turn(row)) << 4) + (col & 3) * 4);
+      }
+      return f;
+    }
+  }
+};
+
+// 32 rows straight into fragments (their lane index), zeros past `dim` and
+// where the lane's row does not exist.
+template <typename T, int D> struct RowFrags {
+  using Frag = typename Mma32<T>::Frag;
+  static constexpr int kSteps = D / Mma32<T>::kK;
+  Frag f[kSteps];
+
+  __device__ inline void load(const T* row, bool exists, int dim, int lane) {
+    constexpr int kChunk = 16 / sizeof(T);
+#pragma unroll
+    for (int s = 0; s < kSteps; s++) {
+      const int at = (2 * s + (lane >> 5)) * kChunk;
+      Frag v = {};
+      if (exists && at < dim) v = *(const Frag*)(row + at);
+      f[s] = v;
+    }
+  }
+};
+
+// Blocks go round the 8 XCDs in turn: each XCD gets a run of neighbours, which
+// share keys and values in its L2.
+__device__ inline int64_t xcd_run(unsigned block, unsigned total) {
+  const unsigned q = total >> 3, rest = total & 7, xcd = block & 7;
+  return xcd * q + (xcd < rest ? xcd : rest) + (block >> 3);
+}
+
+// Where block `id` works.
+struct AttnPlace {
+  int tile, split, kv_head, batch, length;
+  __device__ inline AttnPlace(const AttnArgs& a) {
+    unsigned id = (unsigned)xcd_run(blockIdx.x, gridDim.x);
+    tile = id % a.tiles;
+    id /= a.tiles;
+    split = id % a.splits;
+    id /= a.splits;
+    kv_head = id % a.kv_heads;
+    batch = id / a.kv_heads;
+    length = a.keys;
+    if (a.lengths) {
+      const int n = __builtin_amdgcn_readfirstlane(a.lengths[batch]);
+      length = n < 0 ? 0 : n < a.keys ? n : a.keys;
+    }
+  }
+  // row r of the group's: its query head and query
+  __device__ inline int head(const AttnArgs& a, int r) const { return kv_head * a.group + r / a.queries; }
+};
+
+template <typename T> __device__ inline const T* row_at(const HeadRows& v, int64_t batch, int64_t head, int64_t row) {
+  return (const T*)v.p + batch * v.batch + head * v.head + row * v.row;
+}
+
+// Four neighbouring values of a result.
+template <typename T> __device__ inline void put4(T* p, const float* v) {
+  Pack<T, 4> o;
+#pragma unroll
+  for (int i = 0; i < 4; i++) o.v[i] = (T)v[i];
+  store_pack<T, 4>(p, o);
+}
+
+}  // namespace ringar

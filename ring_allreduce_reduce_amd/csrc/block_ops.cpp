@@ -6,7 +6,6 @@
 #include <atomic>
 #include <cstdint>
 #include <cstring>
-#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <string>
@@ -14,37 +13,12 @@
 #include <vector>
 
 #include "block_types.h"
-#include "op_host.h"
+#include "op_checks.h"
 #include "ringar.h"
 
 using namespace ringar;
 
 namespace {
-
-// The call's result tells of the error: nothing of it is left for
-// hipGetLastError().
-ringar_result_t hip_fail(hipError_t e, const char* what) {
-  (void)hipGetLastError();
-  last_error_text() = std::string(what) + ": " + hipGetErrorString(e);
-  return RINGAR_ERR_DEVICE;
-}
-
-ringar_result_t refuse(ringar_result_t code, const std::string& why) {
-  last_error_text() = why;
-  return code;
-}
-
-#define HIP_TRY(call)                                   \
-  do {                                                  \
-    hipError_t e_ = (call);                             \
-    if (e_ != hipSuccess) return hip_fail(e_, #call);   \
-  } while (0)
-
-#define TRY(call)                                       \
-  do {                                                  \
-    ringar_result_t r_ = (call);                        \
-    if (r_ != RINGAR_SUCCESS) return r_;                \
-  } while (0)
 
 // ------------------------------------------------------------- workspaces
 // One buffer per (device, stream), grown as calls need it and reused in
@@ -67,12 +41,58 @@ uint64_t thread_of(hipStream_t st) {
   return mine;
 }
 
-std::mutex g_ws_mu;
 std::map<std::tuple<int, hipStream_t, uint64_t>, Workspace> g_ws;
 
-// The buffer starts with kCounters zeroed words, which every kernel that uses
-// one leaves at zero; *out is what follows them.
-constexpr size_t kCounterBytes = kCounters * sizeof(uint32_t);
+// ---------------------------------------------------------------- checks
+// Null where something is to be read or written, misalignment, a row stride
+// below the row's length (inputs may repeat one row: stride 0).
+ringar_result_t check_mat(const Mat& m) {
+  if (m.rows == 0 || m.cols == 0) return RINGAR_SUCCESS;
+  if (!m.p) return refuse(RINGAR_ERR_INVALID_ARGUMENT, std::string(m.name) + " is null");
+  if ((uintptr_t)m.p % m.es) return refuse(RINGAR_ERR_INVALID_ARGUMENT, std::string(m.name) + " is not aligned to its element size");
+  if (m.rows > 1 && m.ld < m.cols && !(m.ld == 0 && !m.output))
+    return refuse(RINGAR_ERR_INVALID_ARGUMENT, std::string(m.name) + ": row stride below the row's length");
+  if (m.ld > kMaxPitch) return refuse(RINGAR_ERR_INVALID_ARGUMENT, std::string(m.name) + ": row stride beyond 2^31 - 1 elements");
+  return RINGAR_SUCCESS;
+}
+
+bool overlap(const Mat& a, const Mat& b) {
+  if (!a.p || !b.p || !a.rows || !b.rows || !a.cols || !b.cols) return false;
+  const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
+  const uintptr_t ea = pa + ((uint64_t)(a.rows - 1) * a.ld + a.cols) * a.es;
+  const uintptr_t eb = pb + ((uint64_t)(b.rows - 1) * b.ld + b.cols) * b.es;
+  if (pa >= eb || pb >= ea) return false;
+  // columns of one array: same row stride (a single row goes by the other's),
+  // column ranges apart
+  const uint64_t pitch_a = a.rows > 1 ? (uint64_t)a.ld * a.es : 0, pitch_b = b.rows > 1 ? (uint64_t)b.ld * b.es : 0;
+  const uint64_t pitch = pitch_a ? pitch_a : pitch_b;
+  if (pitch && (a.rows == 1 || pitch_a == pitch) && (b.rows == 1 || pitch_b == pitch)) {
+    const uint64_t d = pb >= pa ? (pb - pa) % pitch : (pitch - (pa - pb) % pitch) % pitch;
+    if (d >= a.cols * a.es && d + b.cols * b.es <= pitch) return false;
+  }
+  return true;
+}
+
+bool same_place(const Mat& a, const Mat& b) { return a.p == b.p && (a.ld == b.ld || a.rows <= 1) && a.es == b.es; }
+
+}  // namespace
+
+namespace ringar {
+
+std::mutex g_ws_mu;
+
+// The call's result tells of the error: nothing of it is left for
+// hipGetLastError().
+ringar_result_t hip_fail(hipError_t e, const char* what) {
+  (void)hipGetLastError();
+  last_error_text() = std::string(what) + ": " + hipGetErrorString(e);
+  return RINGAR_ERR_DEVICE;
+}
+
+ringar_result_t refuse(ringar_result_t code, const std::string& why) {
+  last_error_text() = why;
+  return code;
+}
 
 ringar_result_t workspace(hipStream_t st, size_t bytes, char** out) {
   *out = nullptr;
@@ -110,74 +130,17 @@ ringar_result_t workspace(hipStream_t st, size_t bytes, char** out) {
   return RINGAR_SUCCESS;
 }
 
-// Parts of one workspace, each 256-byte aligned.
-struct Layout {
-  size_t bytes = 0;
-  size_t add(size_t n) {
-    const size_t at = bytes;
-    bytes += (n + 255) / 256 * 256;
-    return at;
-  }
-};
-
-// ---------------------------------------------------------------- checks
-size_t size_of(int dtype) { return dtype == kF32 ? 4 : 2; }
-bool type_ok(int dtype) { return dtype == kF16 || dtype == kBF16 || dtype == kF32; }
-constexpr int64_t kMaxPitch = 0x7fffffff;
-constexpr int64_t kMaxDim = kMaxPitch - 1024;   // sizes rounded up to tiles stay 32-bit
-
-// A matrix operand: rows x cols elements, row i at p + i * ld elements.
-struct Mat {
-  const char* name;
-  const void* p;
-  int64_t rows, cols, ld;
-  size_t es;
-  bool output;
-  bool in_place = false;   // an input that may be y's very place
-};
-
-// Null where something is to be read or written, misalignment, a row stride
-// below the row's length (inputs may repeat one row: stride 0).
-ringar_result_t check_mat(const Mat& m) {
-  if (m.rows == 0 || m.cols == 0) return RINGAR_SUCCESS;
-  if (!m.p) return refuse(RINGAR_ERR_INVALID_ARGUMENT, std::string(m.name) + " is null");
-  if ((uintptr_t)m.p % m.es) return refuse(RINGAR_ERR_INVALID_ARGUMENT, std::string(m.name) + " is not aligned to its element size");
-  if (m.rows > 1 && m.ld < m.cols && !(m.ld == 0 && !m.output))
-    return refuse(RINGAR_ERR_INVALID_ARGUMENT, std::string(m.name) + ": row stride below the row's length");
-  if (m.ld > kMaxPitch) return refuse(RINGAR_ERR_INVALID_ARGUMENT, std::string(m.name) + ": row stride beyond 2^31 - 1 elements");
-  return RINGAR_SUCCESS;
-}
-
-bool overlap(const Mat& a, const Mat& b) {
-  if (!a.p || !b.p || !a.rows || !b.rows || !a.cols || !b.cols) return false;
-  const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
-  const uintptr_t ea = pa + ((uint64_t)(a.rows - 1) * a.ld + a.cols) * a.es;
-  const uintptr_t eb = pb + ((uint64_t)(b.rows - 1) * b.ld + b.cols) * b.es;
-  if (pa >= eb || pb >= ea) return false;
-  // columns of one array: same row stride (a single row goes by the other's),
-  // column ranges apart
-  const uint64_t pitch_a = a.rows > 1 ? (uint64_t)a.ld * a.es : 0, pitch_b = b.rows > 1 ? (uint64_t)b.ld * b.es : 0;
-  const uint64_t pitch = pitch_a ? pitch_a : pitch_b;
-  if (pitch && (a.rows == 1 || pitch_a == pitch) && (b.rows == 1 || pitch_b == pitch)) {
-    const uint64_t d = pb >= pa ? (pb - pa) % pitch : (pitch - (pa - pb) % pitch) % pitch;
-    if (d >= a.cols * a.es && d + b.cols * b.es <= pitch) return false;
-  }
-  return true;
-}
-
-bool same_place(const Mat& a, const Mat& b) { return a.p == b.p && (a.ld == b.ld || a.rows <= 1) && a.es == b.es; }
-
 // Every operand's own checks, and no output over another operand.  The one
-// exception is the operand marked `in_place` (its elements are read before y's
-// are written, by the same thread); another one that lies at the same address,
-// say a square product's x that is the residual too, is refused.
+// exception is an operand marked `in_place` or `any_place` (its elements are read
+// before the output's are written, by the same thread); another one that lies at the
+// same address, say a square product's x that is the residual too, is refused.
 ringar_result_t check_mats(std::initializer_list<Mat> all) {
   for (const Mat& m : all) TRY(check_mat(m));
   for (const Mat* o = all.begin(); o != all.end(); o++) {
     if (!o->output) continue;
     for (const Mat* m = all.begin(); m != all.end(); m++) {
       if (m == o || (m->output && m < o)) continue;
-      if (m->in_place && !strcmp(o->name, "y") && same_place(*m, *o)) continue;
+      if ((m->any_place || (m->in_place && !strcmp(o->name, "y"))) && same_place(*m, *o)) continue;
       if (overlap(*o, *m))
         return refuse(RINGAR_ERR_INVALID_USAGE, std::string(o->name) + " overlaps " + m->name);
     }
@@ -185,13 +148,9 @@ ringar_result_t check_mats(std::initializer_list<Mat> all) {
   return RINGAR_SUCCESS;
 }
 
-bool dims_ok(std::initializer_list<int64_t> d) {
-  for (int64_t v : d)
-    if (v < 0 || v > kMaxDim) return false;
-  return true;
-}
+}  // namespace ringar
 
-#define VEC(name, p, n, es, out) Mat{name, p, (p) ? 1 : 0, n, n, es, out}
+namespace {
 
 // --------------------------------------------------------------- products
 // `ws`: p.bytes at `at` in the stream's workspace (null where nothing of it
@@ -204,15 +163,6 @@ ringar_result_t run_gemm(int dtype, const GemmPlan& p, char* ws, size_t at, hipS
 ringar_result_t check_plan(const GemmPlan& p) {
   if (p.too_many) return refuse(RINGAR_ERR_INVALID_USAGE, "the product has more tiles than one launch takes");
   return RINGAR_SUCCESS;
-}
-
-// No C++ exception leaves a C entry (allocation of a map node or a text).
-template <typename F> ringar_result_t guarded(F f) {
-  try {
-    return f();
-  } catch (...) {
-    return RINGAR_ERR_INTERNAL;
-  }
 }
 
 }  // namespace

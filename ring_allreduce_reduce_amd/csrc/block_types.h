@@ -369,12 +369,10 @@ int norm_backward_groups(int64_t rows, int cols);
 hipError_t launch_col_sum(int out_dtype, const ColSumArgs& a, hipStream_t st);
 hipError_t launch_dz(int dtype, const DzArgs& a, hipStream_t st);
 int dz_groups(int dtype, int64_t rows, int64_t n);
-// Counters at the start of every workspace, zero between calls.
-constexpr int kCounters = 4096;
 // Chooses the kernel, the split of k and the copies from sizes, strides and
 // alignment alone.
 GemmPlan plan_gemm(int dtype, int epi, const GemmArgs& a);
-// `ws`: p.bytes of workspace; `counters`: kCounters zeros.
+// `ws`: p.bytes of workspace; `counters`: its kCounters zeros.
 hipError_t launch_gemm(int dtype, const GemmPlan& p, char* ws, uint32_t* counters, hipStream_t st);
 // dx and dweight in one launch (their workspaces apart), where both run the
 // same tile: a launch less, and the one fills what the other leaves idle.

@@ -1,5 +1,6 @@
 // Products by element type, and the rules that choose their kernel.
 #include "block_types.h"
+#include "op_checks.h"
 
 namespace ringar {
 

@@ -14,29 +14,10 @@
 //
 // Memory bound: forward 16384 x 8192 bf16 92 us (5.8 TB/s), backward 16384 x
 // 4096 bf16 73 us and 5 us of column sums (5.5 TB/s).
-#include "block_types.h"
+#include "norm_rows.h"
 
 namespace ringar {
 namespace {
-
-constexpr int kBlock = 256;
-
-// Sum of `v` over the TPR threads that share a row.
-template <int TPR> __device__ inline float row_sum(float v, float* smem) {
-#pragma unroll
-  for (int o = (TPR < 64 ? TPR : 64) / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  if constexpr (TPR > 64) {
-    const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) smem[wave] = v;
-    __syncthreads();
-    const float* row = smem + wave / (TPR / 64) * (TPR / 64);
-    v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < TPR / 64; i++) v += row[i];
-    __syncthreads();
-  }
-  return v;
-}
 
 template <int TPR> __device__ inline void row_sum2(float& u, float& v, float* smem) {
 #pragma unroll
@@ -61,91 +42,6 @@ template <int TPR> __device__ inline void row_sum2(float& u, float& v, float* sm
     __syncthreads();
   }
 }
-
-// E elements of a row: thread t of TPR holds the packs of V elements that
-// start at (i * TPR + t) * V.  A pack that would pass the row's end starts V
-// before the end instead, and its first `skip` elements, which belong to
-// other packs, are held as zeros and not stored: loads never branch, so all
-// of them are in flight together, at any width of at least V.
-template <typename T, int TPR, int E, int V> struct Row {
-  static constexpr int P = E / V;
-  int col[P], skip[P];
-
-  __device__ inline Row(int cols, int t) {
-#pragma unroll
-    for (int i = 0; i < P; i++) {
-      const int c = (i * TPR + t) * V;
-      col[i] = c < cols - V ? c : cols - V;
-      skip[i] = c - col[i];
-    }
-  }
-  // the row as it lies in memory
-  template <typename U> struct Raw {
-    Pack<U, V> q[P];
-  };
-  template <typename U> __device__ inline void load(const U* p, Raw<U>& r) const {
-#pragma unroll
-    for (int i = 0; i < P; i++) r.q[i] = load_pack<U, V>(p + col[i]);
-  }
-  template <typename U> __device__ inline void widen(const Raw<U>& r, float* out) const {
-#pragma unroll
-    for (int i = 0; i < P; i++)
-#pragma unroll
-      for (int j = 0; j < V; j++) out[i * V + j] = (float)r.q[i].v[j];
-    clear(out);
-  }
-  __device__ inline void clear(float* v) const {
-#pragma unroll
-    for (int i = 0; i < P; i++)
-      if (skip[i] > 0)
-#pragma unroll
-        for (int j = 0; j < V; j++)
-          if (j < skip[i]) v[i * V + j] = 0.0f;
-  }
-  template <typename F> __device__ inline void each(F f) const {
-#pragma unroll
-    for (int i = 0; i < P; i++)
-#pragma unroll
-      for (int j = 0; j < V; j++)
-        if (j >= skip[i]) f(i * V + j, col[i] + j);
-  }
-  // fp32 sums, 16 bytes at a time (value by value the partial rows of 8192 x
-  // 8192 bf16 cost 10 us more: 83, not 73)
-  __device__ inline void sums(float* p, const float* in) const {
-    constexpr int S = V < 4 ? V : 4;
-#pragma unroll
-    for (int i = 0; i < P; i++)
-#pragma unroll
-      for (int h = 0; h < V; h += S) {
-        if (skip[i] <= h) {
-          Pack<float, S> q;
-#pragma unroll
-          for (int j = 0; j < S; j++) q.v[j] = in[i * V + h + j];
-          store_pack<float, S>(p + col[i] + h, q);
-        } else {
-#pragma unroll
-          for (int j = 0; j < S; j++)
-            if (h + j >= skip[i]) p[col[i] + h + j] = in[i * V + h + j];
-        }
-      }
-  }
-  template <bool STREAM> __device__ inline void store(T* p, const float* in) const {
-#pragma unroll
-    for (int i = 0; i < P; i++) {
-      if (skip[i] == 0) {
-        Pack<T, V> q;
-#pragma unroll
-        for (int j = 0; j < V; j++) q.v[j] = (T)in[i * V + j];
-        if constexpr (STREAM) stream_pack<T, V>(p + col[i], q);
-        else store_pack<T, V>(p + col[i], q);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; j++)
-          if (j >= skip[i]) p[col[i] + j] = (T)in[i * V + j];
-      }
-    }
-  }
-};
 
 template <typename T, typename W, int TPR, int E, int V, bool STREAM>
 __global__ __launch_bounds__(TPR < kBlock ? kBlock : TPR) void norm_forward(NormArgs a) {
@@ -367,9 +263,6 @@ template <typename O> __global__ __launch_bounds__(1024) void col_sum(ColSumArgs
   }
 }
 
-// Blocks of a kernel that loops over what it has too few of.
-unsigned capped(int64_t blocks, int threads) { return (unsigned)(blocks < most_blocks(threads) ? blocks : most_blocks(threads)); }
-
 // Threads and elements per thread of a row: the smallest shape that holds it.
 template <typename T, typename W> hipError_t forward(const NormArgs& a, hipStream_t st) {
   auto go = [&](auto kernel, int tpr) {
@@ -431,14 +324,9 @@ int norm_backward_groups(int64_t rows, int cols) {
   return (int)(blocks < most ? blocks : most);
 }
 
-// Outputs that the XCDs' L2s (32 MB together) cannot hold anyway go past them
-// (16384 x 8192 bf16 forward: 87 us, not 115; 16384 x 4096 backward: 70, not
-// 82); smaller ones stay for whoever reads them next.
-static bool beyond_l2(int dtype, const NormArgs& a) { return a.rows * a.cols * (dtype == kF32 ? 4 : 2) > 32ll << 20; }
-
 hipError_t launch_norm_forward(int dtype, int wdtype, const NormArgs& given, hipStream_t st) {
   NormArgs a = given;
-  a.stream = beyond_l2(dtype, a);
+  a.stream = beyond_l2(dtype, a.rows, a.cols);
   if (dtype == kF32) return forward<float, float>(a, st);
   if (dtype == kF16) return wdtype == kF32 ? forward<_Float16, float>(a, st) : forward<_Float16, _Float16>(a, st);
   return wdtype == kF32 ? forward<__bf16, float>(a, st) : forward<__bf16, __bf16>(a, st);
@@ -446,7 +334,7 @@ hipError_t launch_norm_forward(int dtype, int wdtype, const NormArgs& given, hip
 
 hipError_t launch_norm_backward(int dtype, int wdtype, const NormArgs& given, hipStream_t st) {
   NormArgs a = given;
-  a.stream = beyond_l2(dtype, a);
+  a.stream = beyond_l2(dtype, a.rows, a.cols);
   if (dtype == kF32) return backward<float, float>(a, st);
   if (dtype == kF16) return wdtype == kF32 ? backward<_Float16, float>(a, st) : backward<_Float16, _Float16>(a, st);
   return wdtype == kF32 ? backward<__bf16, float>(a, st) : backward<__bf16, __bf16>(a, st);
