@@ -91,21 +91,20 @@ template <typename T, int D, int KT> struct AttnDq {
     f32x16 acc[kDims];
 #pragma unroll
     for (int i = 0; i < kDims; i++) acc[i] = zero16();
+    FragReader<T, KT> read(smem, lane);
     if (first < last) issue(first, 0);
-    for (int tile = first, buf = 0; tile < last; tile++, buf ^= 1) {
+    for (int tile = first, buf = 0; tile < last; tile++, buf ^= 1, read.other(2 * Tile::kBytes)) {
       wait_lds();
       block_barrier();
       if (tile + 1 < last) issue(tile + 1, buf ^ 1);
-      const char* lk = smem + buf * 2 * Tile::kBytes;
-      const char* lv = lk + Tile::kBytes;
       const int left = at.length - tile * KT;
 #pragma unroll
       for (int b = 0; b < KT / 32; b++) {
         f32x16 s = zero16(), dp = zero16();
 #pragma unroll
         for (int i = 0; i < kSteps; i++) {
-          s = M::run(Tile::rows(lk, b * 32, i, lane), q.f[i], s);
-          dp = M::run(Tile::rows(lv, b * 32, i, lane), dy.f[i], dp);
+          s = M::run(read.rows(0, b * 32, i), q.f[i], s);
+          dp = M::run(read.rows(Tile::kBytes, b * 32, i), dy.f[i], dp);
         }
         float ds[16];
 #pragma unroll
@@ -120,7 +119,7 @@ template <typename T, int D, int KT> struct AttnDq {
         for (int f = 0; f < 32 / M::kK; f++) {
           const Frag frag = result_frag<T>(ds + f * kValues);
 #pragma unroll
-          for (int i = 0; i < kDims; i++) acc[i] = M::run(Tile::cols(lk, b * 32 + f * M::kK, i * 32, lane), frag, acc[i]);
+          for (int i = 0; i < kDims; i++) acc[i] = M::run(read.cols(0, b * 32 + f * M::kK, i * 32), frag, acc[i]);
         }
       }
     }
@@ -150,9 +149,9 @@ template <typename T, int D, int QT> struct AttnDkv {
   static constexpr int NW = 4, kThreads = 64 * NW;
   using Tile = RowTile<T, D, QT, NW>;
   static constexpr int kSteps = D / M::kK, kDims = D / 32;
-  // Q and dy, and a tile's lse2 and delta (64 floats each)
-  static constexpr int kStage = 2 * Tile::kBytes + 512;
-  static constexpr int kShared = 2 * kStage;
+  // two buffers of Q and dy, and of the tile's lse2 and delta (64 floats each)
+  static constexpr int kStage = 2 * Tile::kBytes;
+  static constexpr int kShared = 2 * kStage + 2 * 512;
   static constexpr int kBlocksPerCu = D * sizeof(T) > 256 ? 1 : 2;     // registers
   static_assert(QT <= 64, "one load brings a tile's statistics");
 
@@ -193,8 +192,8 @@ template <typename T, int D, int QT> struct AttnDkv {
       if (wave < 2) {
         const float* stats = (wave ? a.delta : a.lse2) + ((int64_t)at.batch * a.heads + head) * a.queries + row;
         const u32x4 buffer = buffer_of((const char*)stats, (left + 1) * 4);
-        const uint32_t to = (uint32_t)(uintptr_t)(RINGAR_LDS void*)lds + 2 * Tile::kBytes + wave * 256;
-        asm volatile("s_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" :: "{m0}"(to), "v"(lane * 4), "s"(buffer) : "memory");
+        const uint32_t to = (uint32_t)(uintptr_t)(RINGAR_LDS void*)smem + 2 * kStage + buf * 512 + wave * 256;
+        load_lds_word(lane * 4, buffer, to);
       }
       if (++next == tiles) {
         next = 0;
@@ -205,15 +204,14 @@ template <typename T, int D, int QT> struct AttnDkv {
     f32x16 dk[kDims], dv[kDims];
 #pragma unroll
     for (int i = 0; i < kDims; i++) dk[i] = dv[i] = zero16();
+    FragReader<T, QT> read(smem, lane);
     if (first < last) issue(0);
     int buf = 0;
-    for (int64_t tile = first; tile < last; tile++, buf ^= 1) {
+    for (int64_t tile = first; tile < last; tile++, buf ^= 1, read.other(kStage)) {
       wait_lds();
       block_barrier();
       if (tile + 1 < last) issue(buf ^ 1);
-      const char* lq = smem + buf * kStage;
-      const char* ldy = lq + Tile::kBytes;
-      const float* lse2 = (const float*)(ldy + Tile::kBytes);
+      const float* lse2 = (const float*)(smem + 2 * kStage + buf * 512);
       const int rows_left = a.queries - row_now;        // of the tile that exist
       row_now = row_now + QT < a.queries ? row_now + QT : 0;
 #pragma unroll
@@ -221,8 +219,9 @@ template <typename T, int D, int QT> struct AttnDkv {
         f32x16 s = zero16(), dp = zero16();
 #pragma unroll
         for (int i = 0; i < kSteps; i++) {
-          s = M::run(Tile::rows(lq, b * 32, i, lane), k.f[i], s);
-          dp = M::run(Tile::rows(ldy, b * 32, i, lane), v.f[i], dp);
+          s = M::run(read.rows(0, b * 32, i), k.f[i], s);
+          dp = M::run(read.rows(Tile::kBytes, b * 32, i), v.f[i], dp);
+          if (i % 2) __builtin_amdgcn_sched_barrier(0);
         }
         float p[16], ds[16];
 #pragma unroll
@@ -239,14 +238,16 @@ template <typename T, int D, int QT> struct AttnDkv {
           for (int j = 0; j < 16; j++)
             if (b * 32 + result_row(j, lane) >= rows_left) p[j] = ds[j] = 0.0f;
         }
+        __builtin_amdgcn_sched_barrier(0);
         constexpr int kValues = 16 / sizeof(T);
 #pragma unroll
         for (int f = 0; f < 32 / M::kK; f++) {
           const Frag pf = result_frag<T>(p + f * kValues), df = result_frag<T>(ds + f * kValues);
 #pragma unroll
           for (int i = 0; i < kDims; i++) {
-            dv[i] = M::run(Tile::cols(ldy, b * 32 + f * M::kK, i * 32, lane), pf, dv[i]);
-            dk[i] = M::run(Tile::cols(lq, b * 32 + f * M::kK, i * 32, lane), df, dk[i]);
+            dv[i] = M::run(read.cols(Tile::kBytes, b * 32 + f * M::kK, i * 32), pf, dv[i]);
+            dk[i] = M::run(read.cols(0, b * 32 + f * M::kK, i * 32), df, dk[i]);
+            __builtin_amdgcn_sched_barrier(0);
           }
         }
       }

@@ -77,20 +77,19 @@ __device__ inline void AttnForward<T, D, KT, NW, FEW>::run(const AttnArgs& a, ch
   for (int i = 0; i < kDims; i++) o[i] = zero16();
   float top = -INFINITY, sum = 0.0f;          // sum: of this lane's half of the keys
 
+  FragReader<T, KT> read(mine, lane);
   if (tile < last) issue(tile, 0);
-  for (int buf = 0; tile < last; tile += kTurn, buf ^= 1) {
+  for (int buf = 0; tile < last; tile += kTurn, buf ^= 1, read.other(2 * Tile::kBytes)) {
     // the tile has landed, and every wave is done with the other buffer
     wait_lds();
     if constexpr (!FEW) block_barrier();
     if (tile + kTurn < last) issue(tile + kTurn, buf ^ 1);
-    const char* lk = mine + buf * 2 * Tile::kBytes;
-    const char* lv = lk + Tile::kBytes;
     f32x16 s[kBlocks];
 #pragma unroll
     for (int b = 0; b < kBlocks; b++) {
       s[b] = zero16();
 #pragma unroll
-      for (int i = 0; i < kSteps; i++) s[b] = M::run(Tile::rows(lk, b * 32, i, lane), q.f[i], s[b]);
+      for (int i = 0; i < kSteps; i++) s[b] = M::run(read.rows(0, b * 32, i), q.f[i], s[b]);
     }
     const int left = at.length - tile * KT;   // keys of the tile that exist
     if (left < KT) {
@@ -123,12 +122,11 @@ __device__ inline void AttnForward<T, D, KT, NW, FEW>::run(const AttnArgs& a, ch
         p[b * 16 + i] = e;
         sum += e;
       }
-    constexpr int kValues = 16 / sizeof(T);
 #pragma unroll
     for (int f = 0; f < KT / M::kK; f++) {
-      const Frag pf = result_frag<T>(p + f * kValues);
+      const Frag pf = result_frag<T>(p + f * (16 / (int)sizeof(T)));
 #pragma unroll
-      for (int i = 0; i < kDims; i++) o[i] = M::run(Tile::cols(lv, f * M::kK, i * 32, lane), pf, o[i]);
+      for (int i = 0; i < kDims; i++) o[i] = M::run(read.cols(Tile::kBytes, f * M::kK, i * 32), pf, o[i]);
     }
   }
   sum += __shfl_xor(sum, 32);

@@ -80,12 +80,34 @@ __device__ inline u32x4 buffer_of(const char* base, int64_t bytes) {
   return u32x4{(uint32_t)(uintptr_t)base, (uint32_t)((uintptr_t)base >> 32), size, 0x00027000u};
 }
 
+// Loads into LDS, 16 bytes a lane, to `to` and (load_lds2) APART bytes on.  The
+// LDS address is taken from m0, one instruction at least after it is set, and
+// what a vector instruction has put into a scalar register (the compiler keeps
+// scalars in lanes where it has too many) five later: asm gets neither wait
+// from the compiler.
+__device__ inline void load_lds(uint32_t off, u32x4 buffer, uint32_t to) {
+  asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" :: "{m0}"(to), "v"(off), "s"(buffer) : "memory");
+}
+template <int APART> __device__ inline void load_lds2(uint32_t off, uint32_t off2, u32x4 buffer, uint32_t to) {
+  asm volatile(
+      "s_nop 4\n\tbuffer_load_dwordx4 %1, %3, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds"
+      : "+{m0}"(to) : "v"(off), "v"(off2), "s"(buffer), "n"(APART) : "memory", "scc");
+}
+// 4 bytes a lane.
+__device__ inline void load_lds_word(uint32_t off, u32x4 buffer, uint32_t to) {
+  asm volatile("s_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" :: "{m0}"(to), "v"(off), "s"(buffer) : "memory");
+}
+
 // R rows of D values in LDS, brought by NW waves straight from memory: lines of
 // 128 bytes, R of them for each 128 bytes of a row, the eight 16-byte chunks of
 // a line in the order c ^ turn(row).  turn() lets both kinds of reads spread
-// over all banks: eight rows of one chunk (rows of like parity lie in one half
-// of the banks, four turns keep them apart there), and four rows of 64 bytes
-// (rows k and k + 2 in different halves of their lines).
+// over all 64 banks in every cycle's 256 bytes: sixteen rows of one chunk (rows
+// of like parity lie in one half of the banks, eight turns keep them apart
+// there), and four rows of 64 bytes (rows k and k + 2 in different halves of
+// their lines).
+__device__ inline int turn(int row) { return (row & 2) << 1 | (row & 4) >> 1 | (row & 8) >> 3; }
+
 template <typename T, int D, int R, int NW> struct RowTile {
   static constexpr int kChunk = 16 / sizeof(T);
   static constexpr int kLines = D * (int)sizeof(T) / 128;
@@ -94,8 +116,6 @@ template <typename T, int D, int R, int NW> struct RowTile {
   static_assert(kLoads * NW * 1024 == kBytes && R % 32 == 0, "every wave loads the same share");
   static constexpr uint32_t kOutside = 0x80000000u;   // past the end of any buffer
 
-  static __device__ inline int turn(int row) { return (row & 2) << 1 | (row & 4) >> 1; }
-
   uint32_t off[kLoads];
 
   // `pitch`: bytes from row to row; chunks from `dim` on read as zero
@@ -103,54 +123,80 @@ template <typename T, int D, int R, int NW> struct RowTile {
 #pragma unroll
     for (int i = 0; i < kLoads; i++) {
       const int idx = i * NW + wave;
-      const int row = idx % (R / 8) * 8 + (lane >> 3), chunk = idx / (R / 8) * 8 + ((lane & 7) ^ turn(lane >> 3));
+      const int row = idx % (R / 8) * 8 + (lane >> 3), chunk = idx / (R / 8) * 8 + ((lane & 7) ^ turn(row));
       off[i] = chunk * kChunk < dim ? (uint32_t)(row * pitch) + chunk * 16 : kOutside;
     }
   }
   // Starts the loads.  They are asm because the compiler would wait for them
   // before every LDS read that follows; wait_lds() and a barrier come before
-  // anything reads what they bring.  The LDS address is taken from m0, one
-  // instruction at least after it is set.
+  // anything reads what they bring.
   __device__ inline void load(u32x4 buffer, char* lds, int wave) const {
+    const uint32_t to = (uint32_t)(uintptr_t)(RINGAR_LDS void*)lds + wave * 1024;
+    if constexpr (kLoads == 1) load_lds(off[0], buffer, to);
+    else
 #pragma unroll
-    for (int i = 0; i < kLoads; i++) {
-      const uint32_t to = (uint32_t)(uintptr_t)(RINGAR_LDS void*)lds + (i * NW + wave) * 1024;
-      asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" :: "{m0}"(to), "v"(off[i]), "s"(buffer) : "memory");
-    }
+      for (int i = 0; i < kLoads; i += 2) load_lds2<NW * 1024>(off[i], off[i + 1], buffer, to + i * NW * 1024);
   }
+};
 
+// The lanes' part of the addresses in LDS at which fragments of a RowTile are
+// read; what is left, the tile's place and the rows and columns in it, are
+// constants of the instruction (a chunk's turn folds into four addresses each).
+template <typename T, int R> struct FragReader {
   using Frag = typename Mma32<T>::Frag;
-  // Rows r0 .. r0 + 31 as the lanes' index, step s of the contraction over D.
-  static __device__ inline Frag rows(const char* lds, int r0, int s, int lane) {
-    const int t = lane & 31, c = 2 * s + (lane >> 5);
-    return *(const Frag*)(lds + c / 8 * (R * 128) + (r0 + t) * 128 + (((c & 7) ^ turn(t)) << 4));
-  }
-  // Columns c0 .. c0 + 31 as the lanes' index, contraction over rows r0 .. in the
-  // order of a result's values (r0: a multiple of kK).
-  static __device__ inline Frag cols(const char* lds, int r0, int c0, int lane) {
+  uint32_t row[4], col[4];
+
+  __device__ inline FragReader(const char* smem, int lane) {
+    const uint32_t base = (uint32_t)(uintptr_t)(RINGAR_LDS const void*)smem;
+    const int half = lane >> 5, t = lane & 31;
+    const uint32_t by_row = base + t * 128 + ((half ^ turn(t)) << 4);
+    uint32_t by_col;
     if constexpr (sizeof(T) == 2) {
       // source lane t of 16 gives row t / 4 and four columns; after the
       // transposing read lane t holds column t of the four rows
+      const int u = lane & 15, r = 4 * half + (u >> 2);
+      by_col = base + r * 128 + ((((lane >> 4 & 1) * 2 + (u >> 1 & 1)) ^ turn(r)) << 4) + (u & 1) * 8;
+    } else {
+      by_col = base + 4 * half * 128 + (((t >> 2) ^ turn(4 * half)) << 4) + (t & 3) * 4;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      row[i] = by_row ^ (i << 5);
+      col[i] = by_col ^ ((i & 1) << 4 | (i & 2) << 5);
+    }
+  }
+
+  // On to the other of two buffers, `apart` bytes (a power of two) away.
+  __device__ inline void other(int apart) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      row[i] ^= apart;
+      col[i] ^= apart;
+    }
+  }
+
+  // Rows r0 .. r0 + 31 as the lanes' index, step s of the contraction over D.
+  __device__ inline Frag rows(int tile, int r0, int s) const {
+    return *(const RINGAR_LDS Frag*)(uintptr_t)(row[s & 3] + tile + s / 4 * (R * 128) + r0 * 128);
+  }
+  // Columns c0 .. c0 + 31 as the lanes' index, contraction over rows r0 .. in the
+  // order of a result's values (r0: a multiple of kK).
+  __device__ inline Frag cols(int tile, int r0, int c0) const {
+    if constexpr (sizeof(T) == 2) {
       typedef short s16x4 __attribute__((ext_vector_type(4)));
       typedef short s16x8 __attribute__((ext_vector_type(8)));
-      const int t = lane & 15, col = c0 + (lane & 16) + (t & 3) * 4;
       s16x4 v[2];
 #pragma unroll
-      for (int q = 0; q < 2; q++) {
-        const int row = r0 + 8 * q + 4 * (lane >> 5) + (t >> 2), chunk = col / 8;
-        const char* p = lds + chunk / 8 * (R * 128) + row * 128 + (((chunk & 7) ^ turn(row)) << 4) + (col & 7) * 2;
-        v[q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((RINGAR_LDS s16x4*)(RINGAR_LDS void*)p);
-      }
+      for (int q = 0; q < 2; q++)
+        v[q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (RINGAR_LDS s16x4*)(uintptr_t)(col[(c0 / 32 & 1) * 2 + q] + tile + c0 / 64 * (R * 128) + (r0 + 8 * q) * 128));
       const s16x8 w = {v[0][0], v[0][1], v[0][2], v[0][3], v[1][0], v[1][1], v[1][2], v[1][3]};
       return __builtin_bit_cast(Frag, w);
     } else {
-      const int col = c0 + (lane & 31), chunk = col / 4;
       Frag f;
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int row = r0 + 4 * (lane >> 5) + i;
-        f[i] = *(const float*)(lds + chunk / 8 * (R * 128) + row * 128 + (((chunk & 7) ^ turn(row)) << 4) + (col & 3) * 4);
-      }
+      for (int i = 0; i < 4; i++)
+        f[i] = *(const RINGAR_LDS float*)(uintptr_t)(col[(i & 2) + (r0 >> 3 & 1)] + tile + c0 / 32 * (R * 128) + (r0 + i) * 128);
       return f;
     }
   }
