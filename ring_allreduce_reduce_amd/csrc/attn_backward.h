@@ -77,26 +77,27 @@ template <typename T, int D, int KT> struct AttnDq {
     const int all = (at.length + KT - 1) / KT, per = (all + a.splits - 1) / a.splits;
     const int first = at.split * per, last = first + per < all ? first + per : all;
     const int64_t pitch_k = a.k.row * (int64_t)sizeof(T), pitch_v = a.v.row * (int64_t)sizeof(T);
-    const char* keys = (const char*)row_at<T>(a.k, at.batch, at.kv_head, 0);
-    const char* values = (const char*)row_at<T>(a.v, at.batch, at.kv_head, 0);
+    const int row_bytes = a.dim * (int)sizeof(T);
+    RowStream keys, values;
+    keys.start(row_at<T>(a.k, at.batch, at.kv_head, 0), pitch_k, (int64_t)first * KT, at.length, KT, row_bytes);
+    values.start(row_at<T>(a.v, at.batch, at.kv_head, 0), pitch_v, (int64_t)first * KT, at.length, KT, row_bytes);
     Tile tk, tv;
     tk.start(pitch_k, a.dim, wave, lane);
     tv.start(pitch_v, a.dim, wave, lane);
-    auto issue = [&](int t, int buf) {
-      const int64_t row = (int64_t)t * KT, left = at.length - 1 - row;
+    auto issue = [&](int buf) {
       char* lds = smem + buf * 2 * Tile::kBytes;
-      tk.load(buffer_of(keys + row * pitch_k, left * pitch_k + a.dim * (int)sizeof(T)), lds, wave);
-      tv.load(buffer_of(values + row * pitch_v, left * pitch_v + a.dim * (int)sizeof(T)), lds + Tile::kBytes, wave);
+      tk.load(keys.next(), lds, wave);
+      tv.load(values.next(), lds + Tile::kBytes, wave);
     };
     f32x16 acc[kDims];
 #pragma unroll
     for (int i = 0; i < kDims; i++) acc[i] = zero16();
     FragReader<T, KT> read(smem, lane);
-    if (first < last) issue(first, 0);
+    if (first < last) issue(0);
     for (int tile = first, buf = 0; tile < last; tile++, buf ^= 1, read.other(2 * Tile::kBytes)) {
       wait_lds();
       block_barrier();
-      if (tile + 1 < last) issue(tile + 1, buf ^ 1);
+      if (tile + 1 < last) issue(buf ^ 1);
       const int left = at.length - tile * KT;
 #pragma unroll
       for (int b = 0; b < KT / 32; b++) {
@@ -179,22 +180,30 @@ template <typename T, int D, int QT> struct AttnDkv {
     tdy.start(pitch_dy, a.dim, wave, lane);
     int head = at.kv_head * a.group, next = 0;          // of the tile that is issued next
     int row_now = 0;                                    // first row of the tile in work
+    bool fresh = true;
     if (first < last) {
       head += (int)(first / tiles);
       next = (int)(first % tiles);
       row_now = next * QT;
     }
+    const int row_bytes = a.dim * (int)sizeof(T);
+    RowStream queries, grads, lse2s, deltas;
     auto issue = [&](int buf) {
-      const int64_t row = (int64_t)next * QT, left = a.queries - 1 - row;
-      char* lds = smem + buf * kStage;
-      tq.load(buffer_of((const char*)row_at<T>(a.q, at.batch, head, row), left * pitch_q + a.dim * (int)sizeof(T)), lds, wave);
-      tdy.load(buffer_of((const char*)row_at<T>(a.dy, at.batch, head, row), left * pitch_dy + a.dim * (int)sizeof(T)), lds + Tile::kBytes, wave);
-      if (wave < 2) {
-        const float* stats = (wave ? a.delta : a.lse2) + ((int64_t)at.batch * a.heads + head) * a.queries + row;
-        const u32x4 buffer = buffer_of((const char*)stats, (left + 1) * 4);
-        const uint32_t to = (uint32_t)(uintptr_t)(RINGAR_LDS void*)smem + 2 * kStage + buf * 512 + wave * 256;
-        load_lds_word(lane * 4, buffer, to);
+      if (next == 0 || fresh) {             // a head's rows
+        const int64_t row = (int64_t)next * QT, stat = ((int64_t)at.batch * a.heads + head) * a.queries;
+        queries.start(row_at<T>(a.q, at.batch, head, 0), pitch_q, row, a.queries, QT, row_bytes);
+        grads.start(row_at<T>(a.dy, at.batch, head, 0), pitch_dy, row, a.queries, QT, row_bytes);
+        lse2s.start(a.lse2 + stat, 4, row, a.queries, QT, 4);
+        deltas.start(a.delta + stat, 4, row, a.queries, QT, 4);
+        fresh = false;
       }
+      char* lds = smem + buf * kStage;
+      tq.load(queries.next(), lds, wave);
+      tdy.load(grads.next(), lds + Tile::kBytes, wave);
+      const uint32_t to = (uint32_t)(uintptr_t)(RINGAR_LDS void*)smem + 2 * kStage + buf * 512;
+      const u32x4 l = lse2s.next(), d = deltas.next();
+      if (wave == 0) load_lds_word(lane * 4, l, to);
+      else if (wave == 1) load_lds_word(lane * 4, d, to + 256);
       if (++next == tiles) {
         next = 0;
         head++;

@@ -1,5 +1,7 @@
 // Cross attention: how a call is cut into blocks, and the join of gradients
 // whose sums were split.
+#include <initializer_list>
+
 #include "attn_types.h"
 
 namespace ringar {
@@ -14,10 +16,43 @@ static int splits_for(int64_t blocks, int64_t along, int64_t least) {
 
 int64_t attn_blocks(const AttnArgs& a) { return (int64_t)a.tiles * a.splits * a.kv_heads * a.batch; }
 
-void plan_attn_forward(int, AttnArgs& a) {
-  a.few = a.rows <= 32;
-  a.tiles = (int)(((int64_t)a.rows + (a.few ? 31 : 127)) / (a.few ? 32 : 128));
-  a.splits = splits_for((int64_t)a.tiles * a.kv_heads * a.batch, a.keys, 256);
+// The forward pass's form and its parts along the keys: the one whose time, put
+// together from what was measured over 1 .. 1024 queries, 500 .. 65536 keys, 1
+// .. 64 sequences and 1 .. 20 heads, is the least.  In us:
+//   a turn of one wave (32 rows, 32 keys): 0.33 at head_dim 64, 0.46 at 128, fp32
+//   2.0 and 4.5 (one wave a SIMD and two cost the same a turn: the clock drops);
+//   of few rows, each wave's tiles on its own: 0.45 at least where other blocks
+//   read them too, 0.75 where they come from memory;
+//   start and end 5; a second launch 3.5 and 0.3 a part, and the parts' bytes;
+//   keys and values from memory once at 5 TB/s, and to every block at 18.
+void plan_attn_forward(int dtype, AttnArgs& a) {
+  const bool wide = dtype == kF32, far = a.dim > 64;
+  const double bytes = 2.0 * a.keys * a.kv_heads * a.batch * a.dim * (wide ? 4 : 2);
+  const double turn = wide ? (far ? 4.5 : 2.0) : far ? 0.46 : 0.33;
+  double best = 0;
+  for (int form = a.rows <= 32 ? kFewRows : kManyRows; form <= kFewRows; form++) {
+    const int rows = form == kFewRows ? 32 : 128;
+    const int groups = form == kManyRows ? 1 : form == kSomeRows ? 2 : wide && far ? 2 : 4;       // along the keys
+    const int64_t tiles = ((int64_t)a.rows + rows - 1) / rows, units = tiles * a.kv_heads * a.batch;
+    for (int splits : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+      if (splits > 1 && (int64_t)splits * 128 > a.keys) break;
+      const double turns = (double)(((int64_t)a.keys + 32 * groups * splits - 1) / (32 * groups * splits));
+      const double rounds = (double)((units * splits + 255) / 256);      // blocks of a CU
+      double work = rounds * turns;
+      if (form == kSomeRows) work *= rounds > 1 ? 2.0 : 1.8;
+      const double wait = (form != kFewRows ? 0.0 : tiles > 1 ? 0.45 : 0.75) / rounds;
+      work *= wait > turn ? wait : turn;
+      const double memory = bytes / 5e6 > bytes * tiles / 18e6 ? bytes / 5e6 : bytes * tiles / 18e6;
+      double us = 5 + (work > memory ? work : memory);
+      if (splits > 1) us += 3.5 + 0.3 * splits + (double)splits * a.rows * a.kv_heads * a.batch * a.dim * 8 / 4e6;
+      if (best == 0 || us < 0.97 * best) {
+        best = us;
+        a.form = form;
+        a.tiles = (int)tiles;
+        a.splits = splits;
+      }
+    }
+  }
 }
 
 void plan_attn_dq(int, AttnArgs& a) {

@@ -9,42 +9,54 @@
 // Query heads that share a key head lie behind each other in one run of rows.
 // Tiles of keys and values come straight into LDS, two buffers in turn, one
 // barrier a tile.  P is rounded to the operands' type before it meets v (the
-// matrix instruction's operand; l sums what was not rounded).  m is raised only where
-// a row passes it by 8 (a factor of 256 in P, which fp32 sums and either type
-// hold): most tiles then scale nothing.
+// matrix instruction's operand; l sums what was not rounded).
 //
-// Rows in plenty: a block's 4 waves take 32 rows each and share the tiles.
-// Few rows (one tile): its waves share the rows and take the tiles in turn,
-// each its own from memory, joined over LDS at the end; more blocks along the
-// keys where the GPU has room, joined by a second launch.
+// The first tile gives m.  A later one is taken at the m there is, without a
+// look for its maximum: m is raised, and the tile taken again, only where a
+// lane's exponentials add up to more than 2^12 (every type and the fp32 sums
+// hold those).  So most tiles cost an fma, an exponential, an addition and half
+// a conversion a score.  And these take the vector units while the products take
+// the matrix units: a wave works on three tiles at once, instruction by
+// instruction, P v of tile t - 1, q k^T of tile t + 1 and the exponentials of t.
+//
+// A block's NQ x NK waves are NQ runs of 32 rows, which share tiles, and NK
+// groups that take the tiles in turn, each from buffers of its own; the groups'
+// sums meet in LDS at the end.  More blocks along the keys where the GPU has
+// room, joined by a second launch.
 #pragma once
 
 #include "attn_tile.h"
 
 namespace ringar {
 
-constexpr float kRaise = 8.0f;
+constexpr float kMostSum = 4096.0f;
 
-// NW waves.  FEW: they share the rows and have tiles of their own.
-template <typename T, int D, int KT, int NW, bool FEW> struct AttnForward {
+template <typename T, int D, int KT, int NQ, int NK> struct AttnForward {
   using M = Mma32<T>;
   using Frag = typename M::Frag;
-  using Tile = RowTile<T, D, KT, FEW ? 1 : NW>;
-  static constexpr int kThreads = 64 * NW;
+  using Tile = RowTile<T, D, KT, NQ>;
+  static constexpr int kThreads = 64 * NQ * NK;
   static constexpr int kSteps = D / M::kK, kBlocks = KT / 32, kDims = D / 32;
-  static constexpr int kSets = FEW ? NW : 1;              // tiles in work at a time
-  static constexpr int kShared = kSets * 4 * Tile::kBytes;
-  static constexpr int kJoinRow = D + 4;                  // FEW: floats of a row, shifted over the banks
-  static_assert(!FEW || kShared >= NW * 32 * (kJoinRow + 2) * 4, "the waves' sums fit");
+  static constexpr int kGroup = 4 * Tile::kBytes;         // a group's buffers: two of keys, two of values
+  static constexpr int kLaneSums = (kDims * 16 + 4) * 4;  // bytes of a lane's sums, its maximum and sum
+  static constexpr int kJoin = (NK - 1) * NQ * 64 * kLaneSums;
+  static constexpr int kShared = NK * kGroup > kJoin ? NK * kGroup : kJoin;
+  static constexpr int kBlocksPerCu = kThreads <= 256 && kShared <= 80 * 1024 ? 2 : 1;
+  // waves that read a tile must all have it, and be done with it, together
+  static __device__ inline void arrive() {
+    wait_lds();
+    if constexpr (NQ > 1) block_barrier();
+  }
 
   static __device__ inline void run(const AttnArgs& a, char* smem);
 };
 
-template <typename T, int D, int KT, int NW, bool FEW>
-__device__ inline void AttnForward<T, D, KT, NW, FEW>::run(const AttnArgs& a, char* smem) {
+template <typename T, int D, int KT, int NQ, int NK>
+__device__ inline void AttnForward<T, D, KT, NQ, NK>::run(const AttnArgs& a, char* smem) {
   const AttnPlace at(a);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = at.tile * (FEW ? 32 : 32 * NW) + (FEW ? 0 : wave * 32) + (lane & 31);
+  const int wq = wave % NQ, group = wave / NQ;
+  const int r = (at.tile * NQ + wq) * 32 + (lane & 31);
   const bool exists = r < a.rows;
   const int r_in = exists ? r : a.rows - 1;
   const int head = at.head(a, r_in), query = r_in % a.queries;
@@ -52,46 +64,81 @@ __device__ inline void AttnForward<T, D, KT, NW, FEW>::run(const AttnArgs& a, ch
   RowFrags<T, D> q;
   q.load(row_at<T>(a.q, at.batch, head, query), exists, a.dim, lane);
 
-  // this block's tiles of keys
+  // this block's tiles of keys, and of them this group's
   const int all = (at.length + KT - 1) / KT, per = (all + a.splits - 1) / a.splits;
   const int first = at.split * per, last = first + per < all ? first + per : all;
-  constexpr int kTurn = FEW ? NW : 1;
-  int tile = first + (FEW ? wave : 0);
+  const int turns = (last - first + NK - 1) / NK, mine = (last - first - group + NK - 1) / NK;
 
   const int64_t pitch_k = a.k.row * (int64_t)sizeof(T), pitch_v = a.v.row * (int64_t)sizeof(T);
-  const char* keys = (const char*)row_at<T>(a.k, at.batch, at.kv_head, 0);
-  const char* values = (const char*)row_at<T>(a.v, at.batch, at.kv_head, 0);
+  const int row_bytes = a.dim * (int)sizeof(T), from = (first + group) * KT;
+  RowStream keys, values;
+  keys.start(row_at<T>(a.k, at.batch, at.kv_head, 0), pitch_k, from, at.length, NK * KT, row_bytes);
+  values.start(row_at<T>(a.v, at.batch, at.kv_head, 0), pitch_v, from, at.length, NK * KT, row_bytes);
   Tile tk, tv;
-  tk.start(pitch_k, a.dim, FEW ? 0 : wave, lane);
-  tv.start(pitch_v, a.dim, FEW ? 0 : wave, lane);
-  char* mine = smem + (FEW ? wave * 4 * Tile::kBytes : 0);
-  auto issue = [&](int t, int buf) {
-    const int64_t row = (int64_t)t * KT, left = at.length - 1 - row;
-    char* lds = mine + buf * 2 * Tile::kBytes;
-    tk.load(buffer_of(keys + row * pitch_k, left * pitch_k + a.dim * (int)sizeof(T)), lds, FEW ? 0 : wave);
-    tv.load(buffer_of(values + row * pitch_v, left * pitch_v + a.dim * (int)sizeof(T)), lds + Tile::kBytes, FEW ? 0 : wave);
+  tk.start(pitch_k, a.dim, wq, lane);
+  tv.start(pitch_v, a.dim, wq, lane);
+  char* buffers = smem + group * kGroup;
+  // of the turns in order
+  auto issue_k = [&](int turn) {
+    if (turn < mine) tk.load(keys.next(), buffers + (turn & 1) * Tile::kBytes, wq);
+  };
+  auto issue_v = [&](int turn) {
+    if (turn < mine) tv.load(values.next(), buffers + (2 + (turn & 1)) * Tile::kBytes, wq);
   };
 
+  // fragments of keys (b: 32 of them, s: step) and of values (f: step, i: 32 columns)
+  FragReader<T, KT> read(buffers, lane);
+  constexpr int kAhead = 3;                   // fragments read before they are used
+  constexpr int kMmaS = kBlocks * kSteps, kMmaV = KT / M::kK * kDims;
+  auto key_frag = [&](int m) { return read.rows(0, m % kBlocks * 32, m / kBlocks); };
+  auto value_frag = [&](int m) { return read.cols(2 * Tile::kBytes, m / kDims * M::kK, m % kDims * 32); };
+
+  constexpr int kFrags = KT / M::kK, kValues = kBlocks * 16;      // P's fragments; a lane's scores
   f32x16 o[kDims];
 #pragma unroll
   for (int i = 0; i < kDims; i++) o[i] = zero16();
-  float top = -INFINITY, sum = 0.0f;          // sum: of this lane's half of the keys
+  float top = -INFINITY, sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};      // of this lane's half of the keys
 
-  FragReader<T, KT> read(mine, lane);
-  if (tile < last) issue(tile, 0);
-  for (int buf = 0; tile < last; tile += kTurn, buf ^= 1, read.other(2 * Tile::kBytes)) {
-    // the tile has landed, and every wave is done with the other buffer
-    wait_lds();
-    if constexpr (!FEW) block_barrier();
-    if (tile + kTurn < last) issue(tile + kTurn, buf ^ 1);
-    f32x16 s[kBlocks];
+  // The products of a turn, one matrix instruction after the other: P v of the
+  // reader's values (0 .. kMmaV - 1), then q k^T of its keys but for the last step
+  // of the contraction, which end_scores() adds.  before(), then with() after each
+  // instruction, run beside them; each reads the fragment kAhead later.
+  constexpr int kMma = kMmaV + kMmaS;
+  Frag kf[kAhead];
+  f32x16 begun[kBlocks];
+  auto frag = [&](int m) { return m < kMmaV ? value_frag(m) : key_frag(m - kMmaV); };
+  auto products = [&](int from, int to, const Frag* p, auto before, auto with) {
 #pragma unroll
-    for (int b = 0; b < kBlocks; b++) {
-      s[b] = zero16();
+    for (int m = 0; m < kAhead; m++) kf[(from + m) % kAhead] = frag(from + m);
+    before();
+    if (to > kMmaV)
 #pragma unroll
-      for (int i = 0; i < kSteps; i++) s[b] = M::run(read.rows(0, b * 32, i), q.f[i], s[b]);
+      for (int b = 0; b < kBlocks; b++) begun[b] = zero16();
+#pragma unroll
+    for (int m = from; m < to; m++) {
+      if (m < kMmaV) o[m % kDims] = M::run(kf[m % kAhead], p[m / kDims], o[m % kDims]);
+      else begun[(m - kMmaV) % kBlocks] = M::run(kf[m % kAhead], q.f[(m - kMmaV) / kBlocks], begun[(m - kMmaV) % kBlocks]);
+      if (m + kAhead < kMma && (to > kMmaV || m + kAhead < kMmaV)) kf[m % kAhead] = frag(m + kAhead);
+      with(m);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    const int left = at.length - tile * KT;   // keys of the tile that exist
+  };
+  auto end_scores = [&](f32x16* s) {
+#pragma unroll
+    for (int m = kMma - kBlocks; m < kMma; m++)
+      s[(m - kMmaV) % kBlocks] = M::run(kf[m % kAhead], q.f[(m - kMmaV) / kBlocks], begun[(m - kMmaV) % kBlocks]);
+  };
+  // the i-th of a lane's scores: its exponential into P's fragments and a sum
+  auto exponential = [&](const f32x16* s, Frag* p, float* sum, int i) {
+    constexpr int kEach = 16 / sizeof(T);
+    const float e = fast_exp2(fmaf(s[i / 16][i % 16], a.scale2, -top));
+    sum[i & 3] += e;
+    p[i / kEach][i % kEach] = (T)e;
+    // (converted here, not where it is used: half the registers)
+    if (i % kEach == kEach - 1) asm volatile("" : "+v"(p[i / kEach]));
+  };
+  // a tile taken with a look for its maximum; `left` of its keys exist
+  auto raise = [&](f32x16* s, Frag* p, int left) {
     if (left < KT) {
 #pragma unroll
       for (int b = 0; b < kBlocks; b++)
@@ -101,150 +148,192 @@ __device__ inline void AttnForward<T, D, KT, NW, FEW>::run(const AttnArgs& a, ch
     }
     float most = -INFINITY;
 #pragma unroll
-    for (int b = 0; b < kBlocks; b++)
-#pragma unroll
-      for (int i = 0; i < 16; i++) most = fmaxf(most, s[b][i]);
+    for (int i = 0; i < kValues; i++) most = fmaxf(most, s[i / 16][i % 16]);
     most = fmaxf(most, __shfl_xor(most, 32)) * a.scale2;
-    if (__any(most > top + kRaise)) {
-      const float raised = fmaxf(top, most), by = raised == -INFINITY ? 1.0f : fast_exp2(top - raised);
-      top = raised;
-      sum *= by;
+    const float raised = fmaxf(top, most), by = raised == -INFINITY ? 1.0f : fast_exp2(top - raised);
+    top = raised == -INFINITY ? 0.0f : raised;        // (no finite score yet: any m will do)
 #pragma unroll
-      for (int i = 0; i < kDims; i++) o[i] *= by;
-    }
-    const float base = top == -INFINITY ? 0.0f : top;
-    float p[kBlocks * 16];
+    for (int i = 0; i < 4; i++) sums[i] *= by;
 #pragma unroll
-    for (int b = 0; b < kBlocks; b++)
+    for (int i = 0; i < kDims; i++) o[i] *= by;
 #pragma unroll
-      for (int i = 0; i < 16; i++) {
-        const float e = fast_exp2(fmaf(s[b][i], a.scale2, -base));
-        p[b * 16 + i] = e;
-        sum += e;
-      }
-#pragma unroll
-    for (int f = 0; f < KT / M::kK; f++) {
-      const Frag pf = result_frag<T>(p + f * (16 / (int)sizeof(T)));
-#pragma unroll
-      for (int i = 0; i < kDims; i++) o[i] = M::run(read.cols(Tile::kBytes, f * M::kK, i * 32), pf, o[i]);
-    }
-  }
-  sum += __shfl_xor(sum, 32);
-
-  const int64_t place = ((int64_t)at.split * a.batch + at.batch) * a.kv_heads + at.kv_head;
-  // eight values a lane and 32 columns: y^T's columns are rows of y
-  auto put = [&](int row, float top, float sum, auto value) {
-    if (row >= a.rows) return;
-    if (a.splits > 1) {
-      const int64_t to = place * a.rows + row;
-      if ((threadIdx.x & 63) < 32) {
-        a.part_top[2 * to] = top;
-        a.part_top[2 * to + 1] = sum;
-      }
-      value([&](int d, const float* v) { put4<float>(a.part + to * a.dim + d, v); }, 1.0f);
-    } else {
-      const int head = at.head(a, row), query = row % a.queries;
-      if (a.lse && (threadIdx.x & 63) < 32)
-        a.lse[((int64_t)at.batch * a.heads + head) * a.queries + query] = sum > 0.0f || sum != sum ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
-      T* y = (T*)row_at<T>(a.y, at.batch, head, query);
-      value([&](int d, const float* v) { put4<T>(y + d, v); }, sum == 0.0f ? 0.0f : 1.0f / sum);
-    }
+    for (int i = 0; i < kValues; i++) exponential(s, p, sums, i);
   };
-  if constexpr (!FEW) {
-    put(r, top, sum, [&](auto to, float by) {
+
+  constexpr auto kBefore = [] {};
+  constexpr auto kNothing = [](int) {};
+  auto only_scores = [&] { products(kMmaV, kMma - kBlocks, nullptr, kBefore, kNothing); };
+  const int left = at.length - from - (mine - 1) * NK * KT;       // keys of the last tile
+  // Turns between the first and the last, and the last where it is whole, are
+  // the loop's; what is rare in them leaves it, or the compiler would keep a
+  // second place for all sums.
+  const int whole = left < KT ? mine - 1 : mine;
+  f32x16 s[kBlocks];
+  Frag p[kFrags];
+  issue_k(0);
+  arrive();
+  issue_k(1);
+  if (mine > 0) {
+    only_scores();
+    end_scores(s);
+    raise(s, p, mine == 1 ? left : KT);
+  }
+  // A turn's start: the next tile's keys and the last one's values have landed,
+  // and every wave is done with what lies in the other buffers.
+  auto start = [&](int turn) {
+    arrive();
+    issue_k(turn + 2);
+    issue_v(turn);
+    read.other(Tile::kBytes);
+  };
+  if (turns > 0) {
+    start(0);
+    if (mine > 1) {
+      only_scores();
+      end_scores(s);
+    }
+    for (int turn = 1; turn < whole; turn++) {
+      bool over = false;
+      float part[4];
+      Frag p_next[kFrags];
+      for (; turn < whole; turn++) {
+        start(turn);
+        // The exponentials, evenly, up to the last of the scores, which then
+        // need no second place.
+        constexpr int kFirst = kValues / 8;
+#pragma unroll
+        for (int i = 0; i < 4; i++) part[i] = 0.0f;
+        products(0, kMma - kBlocks, p,        // (after the last tile: scores of what lies there, not used)
+                 [&] {
+#pragma unroll
+                   for (int i = 0; i < kFirst; i++) exponential(s, p_next, part, i);
+                 },
+                 [&](int m) {
+#pragma unroll
+                   for (int i = kFirst; i < kValues; i++)
+                     if ((i - kFirst) * (kMma - kBlocks) / (kValues - kFirst) == m) exponential(s, p_next, part, i);
+                 });
+#pragma unroll
+        for (int f = 0; f < kFrags; f++) p[f] = p_next[f];
+        over = __any((part[0] + part[1]) + (part[2] + part[3]) > kMostSum);
+        if (over) break;
+#pragma unroll
+        for (int i = 0; i < 4; i++) sums[i] += part[i];
+        end_scores(s);
+      }
+      if (!over) break;
+      raise(s, p, KT);
+      end_scores(s);
+    }
+    if (mine > 1 && whole < mine) {           // the last tile, with keys that do not exist
+      start(whole);
+      products(0, kMmaV, p, kBefore, kNothing);
+      raise(s, p, left);
+    }
+    // the last tile's values (a group whose last turn is missing keeps the others company)
+    if (NQ > 1 && NK > 1 && mine > 0 && mine < turns) arrive();
+    arrive();
+    read.other(Tile::kBytes);
+    if (mine > 0) products(0, kMmaV, p, kBefore, kNothing);
+  }
+  float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+  sum += __shfl_xor(sum, 32);
+  if (sum == 0.0f) top = -INFINITY;
+
+  if constexpr (NK > 1) {
+    // the groups' sums, through LDS, a lane's own values at a time
+    arrive();
+    block_barrier();
+    typedef float f32x4_lds __attribute__((ext_vector_type(4)));
+    auto slot = [&](int g, int i) { return (f32x4_lds*)(smem + (((g - 1) * NQ + wq) * (kDims * 4 + 1) + i) * 1024) + lane; };
+    if (group > 0) {
 #pragma unroll
       for (int i = 0; i < kDims; i++)
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const int d = i * 32 + result_row(j, lane);
-          const float v[4] = {o[i][j] * by, o[i][j + 1] * by, o[i][j + 2] * by, o[i][j + 3] * by};
-          if (d < a.dim) to(d, v);
-        }
-    });
-  } else {
-    // the waves' sums, through LDS
-    wait_lds();
-    block_barrier();
-    float* all_o = (float*)smem;
-    float* all_top = all_o + NW * 32 * kJoinRow;
-    float* row_o = all_o + (wave * 32 + (lane & 31)) * kJoinRow;
-#pragma unroll
-    for (int i = 0; i < kDims; i++)
-#pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        const f32x4 v = {o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]};
-        *(f32x4*)(row_o + i * 32 + result_row(j, lane)) = v;
-      }
-    if (lane < 32) {
-      all_top[(wave * 32 + lane) * 2] = top;
-      all_top[(wave * 32 + lane) * 2 + 1] = sum;
+        for (int j = 0; j < 4; j++) *slot(group, i * 4 + j) = f32x4_lds{o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]};
+      *slot(group, kDims * 4) = f32x4_lds{top, sum, 0.0f, 0.0f};
     }
     __syncthreads();
-    // wave w finishes rows w, w + NW, .. : lanes take four values of a row each
-    for (int i = wave; i < 32; i += NW) {
-      float most = -INFINITY, total = 0.0f, by[NW];
+    if (group > 0) return;
+    float tops[NK], most = top, total = 0.0f;
+    tops[0] = top;
 #pragma unroll
-      for (int w = 0; w < NW; w++) most = fmaxf(most, all_top[(w * 32 + i) * 2]);
+    for (int g = 1; g < NK; g++) {
+      tops[g] = (*slot(g, kDims * 4))[0];
+      most = fmaxf(most, tops[g]);
+    }
+    // a group that saw no finite score: zeros, or NaN to be kept
+    auto by = [&](int g) { return tops[g] == -INFINITY ? 1.0f : fast_exp2(tops[g] - most); };
+    total = sum * by(0);
 #pragma unroll
-      for (int w = 0; w < NW; w++) {
-        const float t = all_top[(w * 32 + i) * 2];
-        by[w] = t == -INFINITY ? 0.0f : fast_exp2(t - most);
-        const float part = all_top[(w * 32 + i) * 2 + 1];
-        total += t == -INFINITY ? part : part * by[w];       // (no keys: 0, or NaN to be kept)
-      }
-      put(at.tile * 32 + i, most, total, [&](auto to, float scale) {
-        const int d = lane * 4;
-        if (d >= a.dim) return;
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < kDims; i++) o[i] *= by(0);
 #pragma unroll
-        for (int w = 0; w < NW; w++)
+    for (int g = 1; g < NK; g++) {
+      total += (*slot(g, kDims * 4))[1] * by(g);
 #pragma unroll
-          for (int j = 0; j < 4; j++) {
-            const float part = all_o[(w * 32 + i) * kJoinRow + d + j];
-            v[j] += all_top[(w * 32 + i) * 2] == -INFINITY ? part : part * by[w];
-          }
+      for (int i = 0; i < kDims; i++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) v[j] *= scale;
-        to(d, v);
-      });
+        for (int j = 0; j < 16; j++) o[i][j] = fmaf((*slot(g, i * 4 + j / 4))[j % 4], by(g), o[i][j]);
+    }
+    top = most;
+    sum = total;
+  }
+  if (!exists) return;
+  const int64_t part = (((int64_t)at.split * a.batch + at.batch) * a.kv_heads + at.kv_head) * a.rows + r;
+  if (lane < 32) {
+    if (a.splits > 1) {
+      a.part_top[2 * part] = top;
+      a.part_top[2 * part + 1] = sum;
+    } else if (a.lse) {
+      a.lse[((int64_t)at.batch * a.heads + head) * a.queries + query] =
+          sum > 0.0f || sum != sum ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
     }
   }
+  const float by = a.splits > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+  T* y = (T*)row_at<T>(a.y, at.batch, head, query);
+#pragma unroll
+  for (int i = 0; i < kDims; i++)
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      const int d = i * 32 + result_row(j, lane);
+      const float v[4] = {o[i][j] * by, o[i][j + 1] * by, o[i][j + 2] * by, o[i][j + 3] * by};
+      if (d >= a.dim) continue;
+      if (a.splits > 1) put4<float>(a.part + part * a.dim + d, v);
+      else put4<T>(y + d, v);
+    }
 }
 
-template <typename K> __global__ __launch_bounds__(K::kThreads, K::kThreads == 256 && K::kShared <= 80 * 1024 ? 2 : 1) void attn_forward(AttnArgs a) {
+template <typename K> __global__ __launch_bounds__(K::kThreads, K::kBlocksPerCu * K::kThreads / 256) void attn_forward(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[K::kShared];
   K::run(a, smem);
 }
 
-// Rows whose keys were split: the parts' maxima and sums, then the parts.  A
-// wave takes a row.
+// Rows whose keys were split: the parts in order, four values of a row a thread.
 template <typename T> __global__ __launch_bounds__(256) void attn_forward_join(AttnArgs a) {
-  const int lane = threadIdx.x & 63;
   const int64_t rows = (int64_t)a.batch * a.kv_heads * a.rows;
-  for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < rows; i += (int64_t)gridDim.x * 4) {
-    float top = -INFINITY, sum = 0.0f;
+  const int quads = a.dim / 4;
+  for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < rows * quads; at += (int64_t)gridDim.x * 256) {
+    const int64_t i = at / quads;
+    const int d = (int)(at % quads) * 4;
+    float top = -INFINITY, sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int s = 0; s < a.splits; s++) top = fmaxf(top, a.part_top[2 * (s * rows + i)]);
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const int d = lane * 4;
     for (int s = 0; s < a.splits; s++) {
       const float t = a.part_top[2 * (s * rows + i)], part = a.part_top[2 * (s * rows + i) + 1];
       const float by = t == -INFINITY ? 1.0f : fast_exp2(t - top);        // (no keys: zeros, or NaN to be kept)
-      sum += part * by;
-      if (d < a.dim) {
-        const Pack<float, 4> o = load_pack<float, 4>(a.part + (s * rows + i) * a.dim + d);
+      sum = fmaf(part, by, sum);
+      const Pack<float, 4> o = load_pack<float, 4>(a.part + (s * rows + i) * a.dim + d);
 #pragma unroll
-        for (int j = 0; j < 4; j++) v[j] += o.v[j] * by;
-      }
+      for (int j = 0; j < 4; j++) v[j] = fmaf(o.v[j], by, v[j]);
     }
     const int row = (int)(i % a.rows);
     const int64_t bh = i / a.rows;
     const int64_t head = bh % a.kv_heads * a.group + row / a.queries, batch = bh / a.kv_heads, query = row % a.queries;
-    if (a.lse && lane == 0)
+    if (a.lse && d == 0)
       a.lse[(batch * a.heads + head) * a.queries + query] = sum > 0.0f || sum != sum ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
     const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
     for (int j = 0; j < 4; j++) v[j] *= scale;
-    if (d < a.dim) put4<T>((T*)row_at<T>(a.y, batch, head, query) + d, v);
+    put4<T>((T*)row_at<T>(a.y, batch, head, query) + d, v);
   }
 }
 
@@ -253,13 +342,21 @@ template <typename T> hipError_t attn_forward_of(const AttnArgs& a, hipStream_t 
     using K = decltype(k);
     return launch_kernel(attn_forward<K>, dim3((unsigned)attn_blocks(a)), K::kThreads, st, a);
   };
-  constexpr int kFewWaves = sizeof(T) == 2 ? 4 : 2;
+  constexpr bool kWide = sizeof(T) == 4;
   hipError_t e;
-  if (a.dim <= 64) e = a.few ? go(AttnForward<T, 64, 32, 4, true>()) : go(AttnForward<T, 64, 64, 4, false>());
-  else e = a.few ? go(AttnForward<T, 128, 32, kFewWaves, true>()) : go(AttnForward<T, 128, sizeof(T) == 2 ? 64 : 32, 4, false>());
+  if (a.dim <= 64) {
+    if (a.form == kManyRows) e = go(AttnForward<T, 64, kWide ? 32 : 64, 4, 1>());
+    else if (a.form == kSomeRows) e = go(AttnForward<T, 64, kWide ? 32 : 64, 4, 2>());
+    else e = go(AttnForward<T, 64, 32, 1, 4>());
+  } else {
+    if (a.form == kManyRows) e = go(AttnForward<T, 128, kWide ? 32 : 64, 4, 1>());
+    else if (a.form == kSomeRows) e = go(AttnForward<T, 128, kWide ? 32 : 64, 4, 2>());
+    else e = go(AttnForward<T, 128, 32, 1, kWide ? 2 : 4>());
+  }
   if (e != hipSuccess || a.splits == 1) return e;
-  const int64_t rows = (int64_t)a.batch * a.kv_heads * a.rows, blocks = (rows + 3) / 4;
-  return launch_kernel(attn_forward_join<T>, dim3((unsigned)(blocks < most_blocks(256) ? blocks : most_blocks(256))), 256, st, a);
+  // four values a thread
+  const int64_t threads = (int64_t)a.batch * a.kv_heads * a.rows * (a.dim / 4), blocks = (threads + 255) / 256;
+  return launch_kernel(attn_forward_join<T>, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), 256, st, a);
 }
 
 }  // namespace ringar

@@ -74,11 +74,26 @@ __device__ inline void block_barrier() {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// A buffer from `base` on, of `bytes` (what lies beyond reads as zero).
-__device__ inline u32x4 buffer_of(const char* base, int64_t bytes) {
-  const uint32_t size = bytes <= 0 ? 0u : bytes > 0x7fffffff ? 0x7fffffffu : (uint32_t)bytes;
-  return u32x4{(uint32_t)(uintptr_t)base, (uint32_t)((uintptr_t)base >> 32), size, 0x00027000u};
-}
+// Tiles of rows in memory, one after the other: the buffer of each reaches from
+// its first row to the last row's end, and what lies beyond reads as zero.
+struct RowStream {
+  const char* base;
+  int64_t left, step;      // bytes to the last row's end, and from tile to tile
+
+  // from row `row` of `rows`, every `apart` rows
+  __device__ inline void start(const void* p, int64_t pitch, int64_t row, int64_t rows, int64_t apart, int row_bytes) {
+    base = (const char*)p + row * pitch;
+    left = (rows - 1 - row) * pitch + row_bytes;
+    step = apart * pitch;
+  }
+  __device__ inline u32x4 next() {
+    const uint32_t size = left >> 31 ? 0x7fffffffu : (uint32_t)left;
+    const u32x4 buffer = {(uint32_t)(uintptr_t)base, (uint32_t)((uintptr_t)base >> 32), size, 0x00027000u};
+    base += step;
+    left -= step;
+    return buffer;
+  }
+};
 
 // Loads into LDS, 16 bytes a lane, to `to` and (load_lds2) APART bytes on.  The
 // LDS address is taken from m0, one instruction at least after it is set, and

@@ -11,6 +11,10 @@ struct HeadRows {
   int64_t batch, row, head;
 };
 
+// the forward kernel's blocks: 128 rows, 128 rows with two groups of waves along
+// the keys, and 32 rows with all waves along the keys
+enum : int { kManyRows = 0, kSomeRows = 1, kFewRows = 2 };
+
 struct AttnArgs {
   HeadRows q, k, v;
   HeadRows y, dy;          // y: forward's output, backward's input
@@ -24,7 +28,7 @@ struct AttnArgs {
   // set by the plan
   int tiles;               // blocks along the rows (dk, dv: the keys)
   int splits;              // parts of what a block goes along
-  bool few;                // forward: one tile of rows for all of a block's waves
+  int form;                // forward: how a block's waves share rows and keys
   float* part;             // splits > 1: [split][..] sums
   float* part_top;         // forward: [split][batch][kv head][row]: maximum, sum of exponentials
   float* lse2;             // backward: log2 of the rows' sums, and delta, batch x heads x queries
