@@ -201,15 +201,14 @@ static ringar_result_t attention_backward(const ringar_cross_attention_backward_
     aq.lse2 = akv.lse2 = (float*)(ws + at_lse2);
     aq.delta = akv.delta = (float*)(ws + at_delta);
   }
-  if (rows) HIP_TRY(launch_attn_delta(p->dtype, aq, st));
+  if (rows && !want_q) HIP_TRY(launch_attn_delta(p->dtype, aq, st));
   if (want_q) {
     HIP_TRY(launch_attn_dq(p->dtype, aq, st));
-    if (aq.splits > 1) HIP_TRY(launch_attn_join(p->dtype, {aq.part, p->dq, rows * d, rows * d, aq.splits, p->scale}, st));
+    if (aq.splits > 1) HIP_TRY(launch_attn_join(p->dtype, {aq.part, {p->dq, nullptr}, {p->scale, 1.0f}, rows * d, 1, aq.splits}, st));
   }
   if (want_kv) {
     HIP_TRY(launch_attn_dkv(p->dtype, akv, st));
-    if (akv.splits > 1 && p->dk) HIP_TRY(launch_attn_join(p->dtype, {akv.part, p->dk, kv_rows * d, 2 * kv_rows * d, akv.splits, p->scale}, st));
-    if (akv.splits > 1 && p->dv) HIP_TRY(launch_attn_join(p->dtype, {akv.part + kv_rows * d, p->dv, kv_rows * d, 2 * kv_rows * d, akv.splits, 1.0f}, st));
+    if (akv.splits > 1) HIP_TRY(launch_attn_join(p->dtype, {akv.part, {p->dk, p->dv}, {p->scale, 1.0f}, kv_rows * d, 2, akv.splits}, st));
   }
   return RINGAR_SUCCESS;
 }

@@ -25,40 +25,51 @@ template <typename T> struct Shift {
   static constexpr float kBack = kLog2 > 0.0f ? 0x1p-10f : 1.0f;
 };
 
-// lse in powers of two (+infinity where a row has no keys, so that its P are
-// 0), and delta.  16 lanes a row, 8 values each at head_dim 128.
+// lse in powers of two; +infinity where a row has no keys, so that its P are 0
+__device__ inline float powers_of_two(float lse) { return lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f; }
+
+// The lane's half of the sum of dy y over a row, in the order of its fragments.
+template <typename Frag, int N> __device__ inline float half_delta(const Frag (&dy)[N], const Frag (&y)[N]) {
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; i++)
+#pragma unroll
+    for (int j = 0; j < 16 / (int)sizeof(dy[0][0]); j++) s = fmaf((float)dy[i][j], (float)y[i][j], s);
+  return s;
+}
+
+// lse2 and delta where no dq is wanted, whose kernel leaves them otherwise: the
+// same sums, 32 rows a wave.
 template <typename T> __global__ __launch_bounds__(256) void attn_delta(AttnArgs a) {
-  constexpr int kChunk = 16 / sizeof(T);
-  const int t = threadIdx.x & 15;
+  const int lane = threadIdx.x & 63;
   const int64_t rows = (int64_t)a.batch * a.heads * a.queries;
-  for (int64_t i = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); i < rows; i += (int64_t)gridDim.x * 16) {
+  for (int64_t i = (int64_t)blockIdx.x * 128 + (threadIdx.x >> 6) * 32 + (lane & 31); i < rows; i += (int64_t)gridDim.x * 128) {
     const int64_t query = i % a.queries, bh = i / a.queries, head = bh % a.heads, batch = bh / a.heads;
-    const T* dy = row_at<T>(a.dy, batch, head, query);
-    const T* y = row_at<T>(a.y, batch, head, query);
-    float s = 0.0f;
-    for (int d = t * kChunk; d < a.dim; d += 16 * kChunk) {
-      const Pack<T, kChunk> u = load_pack<T, kChunk>(dy + d), v = load_pack<T, kChunk>(y + d);
-#pragma unroll
-      for (int j = 0; j < kChunk; j++) s = fmaf((float)u.v[j], (float)v.v[j], s);
-    }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor(s, o);
-    if (t == 0) {
-      const float lse = a.lse[i];
-      a.lse2[i] = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+    RowFrags<T, 128> dy, y;
+    dy.load(row_at<T>(a.dy, batch, head, query), true, a.dim, lane);
+    y.load(row_at<T>(a.y, batch, head, query), true, a.dim, lane);
+    float s = half_delta(dy.f, y.f);
+    s += __shfl_xor(s, 32);
+    if (lane < 32) {
+      a.lse2[i] = powers_of_two(a.lse[i]);
       a.delta[i] = s;
     }
   }
 }
 
 // ------------------------------------------------------------------------ dq
-template <typename T, int D, int KT> struct AttnDq {
+// As the forward pass, a wave works on three tiles (32 keys) at once: dS k of
+// tile t - 1 and q k^T, dy v^T of tile t + 1 on the matrix units, dS of tile t on
+// the vector units.  Four buffers in turn hold a tile from its loads, two turns
+// ahead, to its last product.  delta comes from y's rows, a lane's half of one
+// each, and is left for the other kernel with lse in powers of two.
+template <typename T, int D> struct AttnDq {
   using M = Mma32<T>;
   using Frag = typename M::Frag;
-  static constexpr int NW = 4, kThreads = 64 * NW;
+  static constexpr int NW = 4, kThreads = 64 * NW, KT = 32;
   using Tile = RowTile<T, D, KT, NW>;
   static constexpr int kSteps = D / M::kK, kDims = D / 32;
-  static constexpr int kShared = 4 * Tile::kBytes;
+  static constexpr int kShared = 8 * Tile::kBytes;
   static constexpr int kBlocksPerCu = D * sizeof(T) > 256 ? 1 : 2;     // registers
 
   static __device__ inline void run(const AttnArgs& a, char* smem) {
@@ -68,61 +79,130 @@ template <typename T, int D, int KT> struct AttnDq {
     const bool exists = r < a.rows;
     const int r_in = exists ? r : a.rows - 1;
     const int head = at.head(a, r_in), query = r_in % a.queries;
-    RowFrags<T, D> q, dy;
-    q.load(row_at<T>(a.q, at.batch, head, query), exists, a.dim, lane);
-    dy.load(row_at<T>(a.dy, at.batch, head, query), exists, a.dim, lane);
-    const int64_t stat = ((int64_t)at.batch * a.heads + head) * a.queries + query;
-    const float lse2 = a.lse2[stat], delta = a.delta[stat];
 
     const int all = (at.length + KT - 1) / KT, per = (all + a.splits - 1) / a.splits;
     const int first = at.split * per, last = first + per < all ? first + per : all;
+    const int turns = last - first, row_bytes = a.dim * (int)sizeof(T);
     const int64_t pitch_k = a.k.row * (int64_t)sizeof(T), pitch_v = a.v.row * (int64_t)sizeof(T);
-    const int row_bytes = a.dim * (int)sizeof(T);
+    RowFrags<T, D> q, dy;
+    q.load(row_at<T>(a.q, at.batch, head, query), exists, a.dim, lane);
+    dy.load(row_at<T>(a.dy, at.batch, head, query), exists, a.dim, lane);
+    float delta = 0.0f;
+    {
+      RowFrags<T, D> y;
+      y.load(row_at<T>(a.y, at.batch, head, query), exists, a.dim, lane);
+      delta = half_delta(dy.f, y.f);
+      delta += __shfl_xor(delta, 32);
+    }
+    const int64_t stat = ((int64_t)at.batch * a.heads + head) * a.queries + query;
+    const float lse2 = powers_of_two(a.lse[stat]);
+    if (exists && lane < 32 && at.split == 0) {
+      a.lse2[stat] = lse2;
+      a.delta[stat] = delta;
+    }
+
     RowStream keys, values;
     keys.start(row_at<T>(a.k, at.batch, at.kv_head, 0), pitch_k, (int64_t)first * KT, at.length, KT, row_bytes);
     values.start(row_at<T>(a.v, at.batch, at.kv_head, 0), pitch_v, (int64_t)first * KT, at.length, KT, row_bytes);
     Tile tk, tv;
     tk.start(pitch_k, a.dim, wave, lane);
     tv.start(pitch_v, a.dim, wave, lane);
-    auto issue = [&](int buf) {
-      char* lds = smem + buf * 2 * Tile::kBytes;
+    auto issue = [&](int turn) {              // of the turns in order
+      if (turn >= turns) return;
+      char* lds = smem + (turn & 3) * Tile::kBytes;
       tk.load(keys.next(), lds, wave);
-      tv.load(values.next(), lds + Tile::kBytes, wave);
+      tv.load(values.next(), lds + 4 * Tile::kBytes, wave);
     };
-    f32x16 acc[kDims];
+
+    FragReader<T, KT> read(smem, lane);
+    read.move_cols(2 * Tile::kBytes);         // rows of the buffer at hand, columns of that two turns back
+    constexpr int kMmaQ = 32 / M::kK * kDims, kMma = kMmaQ + 2 * kSteps, kAhead = 3, kFrags = 32 / M::kK;
+    f32x16 acc[kDims], s, dp, begun_s, begun_dp;
+    Frag kf[kAhead], ds[kFrags], ds_next[kFrags];
 #pragma unroll
     for (int i = 0; i < kDims; i++) acc[i] = zero16();
-    FragReader<T, KT> read(smem, lane);
-    if (first < last) issue(0);
-    for (int tile = first, buf = 0; tile < last; tile++, buf ^= 1, read.other(2 * Tile::kBytes)) {
+    // the turn's matrix instructions: dS k, then q k^T and dy v^T but for their last step
+    auto frag = [&](int m) {
+      if (m < kMmaQ) return read.cols(0, m / kDims * M::kK, m % kDims * 32);
+      return read.rows((m - kMmaQ) & 1 ? 4 * Tile::kBytes : 0, 0, (m - kMmaQ) / 2);
+    };
+    auto products = [&](int from, int to, auto before, auto with) {
+#pragma unroll
+      for (int m = 0; m < kAhead; m++) kf[(from + m) % kAhead] = frag(from + m);
+      before();
+      if (to > kMmaQ) begun_s = begun_dp = zero16();
+#pragma unroll
+      for (int m = from; m < to; m++) {
+        const int n = m - kMmaQ;
+        if (m < kMmaQ) acc[m % kDims] = M::run(kf[m % kAhead], ds[m / kDims], acc[m % kDims]);
+        else if (n & 1) begun_dp = M::run(kf[m % kAhead], dy.f[n / 2], begun_dp);
+        else begun_s = M::run(kf[m % kAhead], q.f[n / 2], begun_s);
+        if (m + kAhead < kMma && (to > kMmaQ || m + kAhead < kMmaQ)) kf[m % kAhead] = frag(m + kAhead);
+        with(m);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    auto end_scores = [&] {
+      s = M::run(kf[(kMma - 2) % kAhead], q.f[kSteps - 1], begun_s);
+      dp = M::run(kf[(kMma - 1) % kAhead], dy.f[kSteps - 1], begun_dp);
+    };
+    constexpr int kEach = 16 / sizeof(T);
+    auto slope = [&](Frag* to, int i) {
+      to[i / kEach][i % kEach] = (T)(fast_exp2(fmaf(s[i], a.scale2, -lse2)) * (dp[i] - delta));
+      if (i % kEach == kEach - 1) asm volatile("" : "+v"(to[i / kEach]));
+    };
+    auto slopes = [&](int left) {             // of a tile with `left` keys
+#pragma unroll
+      for (int i = 0; i < 16; i++) {
+        slope(ds, i);
+        if (result_row(i, lane) >= left) ds[i / kEach][i % kEach] = (T)0.0f;
+      }
+    };
+    auto nothing = [](int) {};
+    auto start = [&](int turn) {
       wait_lds();
       block_barrier();
-      if (tile + 1 < last) issue(buf ^ 1);
-      const int left = at.length - tile * KT;
-#pragma unroll
-      for (int b = 0; b < KT / 32; b++) {
-        f32x16 s = zero16(), dp = zero16();
-#pragma unroll
-        for (int i = 0; i < kSteps; i++) {
-          s = M::run(read.rows(0, b * 32, i), q.f[i], s);
-          dp = M::run(read.rows(Tile::kBytes, b * 32, i), dy.f[i], dp);
-        }
-        float ds[16];
-#pragma unroll
-        for (int i = 0; i < 16; i++) ds[i] = fast_exp2(fmaf(s[i], a.scale2, -lse2)) * (dp[i] - delta);
-        if (left < KT) {
-#pragma unroll
-          for (int i = 0; i < 16; i++)
-            if (b * 32 + result_row(i, lane) >= left) ds[i] = 0.0f;
-        }
-        constexpr int kValues = 16 / sizeof(T);
-#pragma unroll
-        for (int f = 0; f < 32 / M::kK; f++) {
-          const Frag frag = result_frag<T>(ds + f * kValues);
-#pragma unroll
-          for (int i = 0; i < kDims; i++) acc[i] = M::run(read.cols(0, b * 32 + f * M::kK, i * 32), frag, acc[i]);
-        }
+      issue(turn + 2);
+      read.other((turn & 1 ? 3 : 1) * Tile::kBytes);      // on to buffer (turn + 1) % 4
+    };
+    const int left = at.length - (last - 1) * KT, whole = left < KT ? turns - 1 : turns;
+    if (turns > 0) {
+      issue(0);
+      issue(1);
+      if (turns > 1) wait_lds<2 * Tile::kLoads>();
+      else wait_lds();
+      block_barrier();
+      products(kMmaQ, kMma - 2, [] {}, nothing);
+      end_scores();
+      start(0);
+      slopes(turns == 1 ? left : KT);
+      if (turns > 1) {
+        products(kMmaQ, kMma - 2, [] {}, nothing);
+        end_scores();
       }
+      for (int turn = 1; turn < whole; turn++) {
+        start(turn);
+        products(0, kMma - 2,                 // (after the last tile: scores of what lies there, not used)
+                 [&] {
+#pragma unroll
+                   for (int i = 0; i < 2; i++) slope(ds_next, i);
+                 },
+                 [&](int m) {
+#pragma unroll
+                   for (int i = 2; i < 16; i++)
+                     if ((i - 2) * (kMma - 2) / 14 == m) slope(ds_next, i);
+                 });
+#pragma unroll
+        for (int f = 0; f < kFrags; f++) ds[f] = ds_next[f];
+        end_scores();
+      }
+      if (turns > 1 && whole < turns) {
+        start(whole);
+        products(0, kMmaQ, [] {}, nothing);
+        slopes(left);
+      }
+      read.other((turns & 1 ? 3 : 1) * Tile::kBytes);
+      products(0, kMmaQ, [] {}, nothing);
     }
     if (!exists) return;
     const int64_t out = (((int64_t)at.batch * a.queries + query) * a.heads + head) * a.dim;
@@ -144,15 +224,19 @@ template <typename T, int D, int KT> struct AttnDq {
 };
 
 // -------------------------------------------------------------------- dk, dv
-template <typename T, int D, int QT> struct AttnDkv {
+// VLDS: the block's values lie in LDS, not in fragments (head_dim 128 of 16-bit
+// types, whose sums leave no registers for them).
+template <typename T, int D, int QT, bool VLDS> struct AttnDkv {
   using M = Mma32<T>;
   using Frag = typename M::Frag;
-  static constexpr int NW = 4, kThreads = 64 * NW;
+  static constexpr int NW = 4, kThreads = 64 * NW, kKeys = 32 * NW;
   using Tile = RowTile<T, D, QT, NW>;
   static constexpr int kSteps = D / M::kK, kDims = D / 32;
   // two buffers of Q and dy, and of the tile's lse2 and delta (64 floats each)
   static constexpr int kStage = 2 * Tile::kBytes;
-  static constexpr int kShared = 2 * kStage + 2 * 512;
+  using Values = RowTile<T, D, kKeys, NW>;                 // VLDS: the block's values stay in LDS
+  static constexpr int kStats = 2 * kStage, kValues = kStats + 2 * 512;
+  static constexpr int kShared = kValues + (VLDS ? Values::kBytes : 0);
   static constexpr int kBlocksPerCu = D * sizeof(T) > 256 ? 1 : 2;     // registers
   static_assert(QT <= 64, "one load brings a tile's statistics");
 
@@ -161,17 +245,24 @@ template <typename T, int D, int QT> struct AttnDkv {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int key = (at.tile * NW + wave) * 32 + (lane & 31);
     const bool exists = key < at.length;
-    const int key_in = exists ? key : 0;
-    const int64_t out = (((int64_t)at.batch * a.keys + key) * a.kv_heads + at.kv_head) * a.dim;
     const int64_t part_size = (int64_t)a.batch * a.keys * a.kv_heads * a.dim;
 
     RowFrags<T, D> k, v;
-    k.load(row_at<T>(a.k, at.batch, at.kv_head, key_in), exists, a.dim, lane);
-    v.load(row_at<T>(a.v, at.batch, at.kv_head, key_in), exists, a.dim, lane);
+    k.load(row_at<T>(a.k, at.batch, at.kv_head, exists ? key : 0), exists, a.dim, lane);
+    if constexpr (!VLDS) v.load(row_at<T>(a.v, at.batch, at.kv_head, exists ? key : 0), exists, a.dim, lane);
+    FragReader<T, kKeys> read_v(smem + kValues, lane);
+    if (VLDS && at.tile * kKeys < at.length) {
+      const int64_t pitch = a.v.row * (int64_t)sizeof(T);
+      Values values;
+      RowStream stream;
+      stream.start(row_at<T>(a.v, at.batch, at.kv_head, 0), pitch, (int64_t)at.tile * kKeys, at.length, 0, a.dim * (int)sizeof(T));
+      values.start(pitch, a.dim, wave, lane);
+      values.load(stream.next(), smem + kValues, wave);
+    }
 
     // tiles of query rows: of every query head, one after the other
     const int tiles = (a.queries + QT - 1) / QT;
-    const int64_t all = at.tile * (NW * 32) < at.length ? (int64_t)a.group * tiles : 0;
+    const int64_t all = (int64_t)at.tile * kKeys < at.length ? (int64_t)a.group * tiles : 0;
     const int64_t per = (all + a.splits - 1) / a.splits;
     const int64_t first = at.split * per, last = first + per < all ? first + per : all;
     const int64_t pitch_q = a.q.row * (int64_t)sizeof(T), pitch_dy = a.dy.row * (int64_t)sizeof(T);
@@ -200,7 +291,7 @@ template <typename T, int D, int QT> struct AttnDkv {
       char* lds = smem + buf * kStage;
       tq.load(queries.next(), lds, wave);
       tdy.load(grads.next(), lds + Tile::kBytes, wave);
-      const uint32_t to = (uint32_t)(uintptr_t)(RINGAR_LDS void*)smem + 2 * kStage + buf * 512;
+      const uint32_t to = (uint32_t)(uintptr_t)(RINGAR_LDS void*)smem + kStats + buf * 512;
       const u32x4 l = lse2s.next(), d = deltas.next();
       if (wave == 0) load_lds_word(lane * 4, l, to);
       else if (wave == 1) load_lds_word(lane * 4, d, to + 256);
@@ -220,7 +311,7 @@ template <typename T, int D, int QT> struct AttnDkv {
       wait_lds();
       block_barrier();
       if (tile + 1 < last) issue(buf ^ 1);
-      const float* lse2 = (const float*)(smem + 2 * kStage + buf * 512);
+      const float* lse2 = (const float*)(smem + kStats + buf * 512);
       const int rows_left = a.queries - row_now;        // of the tile that exist
       row_now = row_now + QT < a.queries ? row_now + QT : 0;
 #pragma unroll
@@ -229,29 +320,32 @@ template <typename T, int D, int QT> struct AttnDkv {
 #pragma unroll
         for (int i = 0; i < kSteps; i++) {
           s = M::run(read.rows(0, b * 32, i), k.f[i], s);
-          dp = M::run(read.rows(Tile::kBytes, b * 32, i), v.f[i], dp);
+          if constexpr (VLDS) dp = M::run(read.rows(Tile::kBytes, b * 32, i), read_v.rows(wave * 32 * 128, 0, i), dp);
+          else dp = M::run(read.rows(Tile::kBytes, b * 32, i), v.f[i], dp);
+          // (not more fragments ahead than there are registers)
           if (i % 2) __builtin_amdgcn_sched_barrier(0);
         }
         float p[16], ds[16];
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
-          const f32x4 l = *(const f32x4*)(lse2 + b * 32 + result_row(j, lane)), delta = *(const f32x4*)(lse2 + 64 + b * 32 + result_row(j, lane));
+          const int row = b * 32 + result_row(j, lane);
+          const f32x4 l = *(const f32x4*)(lse2 + row), delta = *(const f32x4*)(lse2 + 64 + row);
 #pragma unroll
           for (int e = 0; e < 4; e++) {
             p[j + e] = fast_exp2(fmaf(s[j + e], a.scale2, Shift<T>::kLog2 - l[e]));
             ds[j + e] = p[j + e] * ((dp[j + e] - delta[e]) * Shift<T>::kBack);
           }
         }
-        if (rows_left < QT) {
+        if (rows_left < QT) {                 // rows past the end
 #pragma unroll
           for (int j = 0; j < 16; j++)
             if (b * 32 + result_row(j, lane) >= rows_left) p[j] = ds[j] = 0.0f;
         }
         __builtin_amdgcn_sched_barrier(0);
-        constexpr int kValues = 16 / sizeof(T);
+        constexpr int kEach = 16 / sizeof(T);
 #pragma unroll
         for (int f = 0; f < 32 / M::kK; f++) {
-          const Frag pf = result_frag<T>(p + f * kValues), df = result_frag<T>(ds + f * kValues);
+          const Frag pf = result_frag<T>(p + f * kEach), df = result_frag<T>(ds + f * kEach);
 #pragma unroll
           for (int i = 0; i < kDims; i++) {
             dv[i] = M::run(read.cols(Tile::kBytes, b * 32 + f * M::kK, i * 32), pf, dv[i]);
@@ -262,6 +356,7 @@ template <typename T, int D, int QT> struct AttnDkv {
       }
     }
     if (key >= a.keys) return;
+    const int64_t out = (((int64_t)at.batch * a.keys + key) * a.kv_heads + at.kv_head) * a.dim;
 #pragma unroll
     for (int i = 0; i < kDims; i++)
 #pragma unroll
@@ -296,20 +391,20 @@ template <typename K> __global__ __launch_bounds__(K::kThreads, K::kBlocksPerCu)
 }
 
 template <typename T> hipError_t attn_delta_of(const AttnArgs& a, hipStream_t st) {
-  const int64_t blocks = ((int64_t)a.batch * a.heads * a.queries + 15) / 16;
+  const int64_t blocks = ((int64_t)a.batch * a.heads * a.queries + 127) / 128;
   return launch_kernel(attn_delta<T>, dim3((unsigned)(blocks < most_blocks(256) ? blocks : most_blocks(256))), 256, st, a);
 }
 
 template <typename T> hipError_t attn_dq_of(const AttnArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)attn_blocks(a));
-  if (a.dim <= 64) return launch_kernel(attn_dq<AttnDq<T, 64, 64>>, grid, 256, st, a);
-  return launch_kernel(attn_dq<AttnDq<T, 128, sizeof(T) == 2 ? 64 : 32>>, grid, 256, st, a);
+  if (a.dim <= 64) return launch_kernel(attn_dq<AttnDq<T, 64>>, grid, 256, st, a);
+  return launch_kernel(attn_dq<AttnDq<T, 128>>, grid, 256, st, a);
 }
 
 template <typename T> hipError_t attn_dkv_of(const AttnArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)attn_blocks(a));
-  if (a.dim <= 64) return launch_kernel(attn_dkv<AttnDkv<T, 64, 64>>, grid, 256, st, a);
-  return launch_kernel(attn_dkv<AttnDkv<T, 128, 32>>, grid, 256, st, a);
+  if (a.dim <= 64) return launch_kernel(attn_dkv<AttnDkv<T, 64, 64, false>>, grid, 256, st, a);
+  return launch_kernel(attn_dkv<AttnDkv<T, 128, 32, sizeof(T) == 2>>, grid, 256, st, a);
 }
 
 }  // namespace ringar

@@ -6,12 +6,22 @@
 
 namespace ringar {
 
-// Blocks that keep the GPU busy: two a CU.  A call with fewer is split along
-// what its blocks go along, down to parts of `least`.
-static int splits_for(int64_t blocks, int64_t along, int64_t least) {
-  const int64_t wanted = blocks ? 512 / blocks : 1, most = along / least;
-  const int64_t s = wanted < most ? wanted : most;
-  return s < 1 ? 1 : (int)s;
+// Parts of what the backward kernels' blocks go along, `turns` of 32 rows of
+// `turn` us each: one round of blocks on the 256 CUs after the other, and for
+// parts a second launch and what it reads and writes (`part` bytes each).
+static int splits_for(int64_t blocks, int64_t turns, double turn, double part) {
+  double best = 0;
+  int splits = 1;
+  for (int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+    if (s > 1 && s > turns) break;
+    const double rounds = (double)((blocks * s + 255) / 256);
+    const double us = rounds * (double)((turns + s - 1) / s + 1) * turn + (s > 1 ? 4 + 0.3 * s + s * part * 2 / 4e6 : 0);
+    if (best == 0 || us < 0.97 * best) {
+      best = us;
+      splits = s;
+    }
+  }
+  return splits;
 }
 
 int64_t attn_blocks(const AttnArgs& a) { return (int64_t)a.tiles * a.splits * a.kv_heads * a.batch; }
@@ -55,33 +65,41 @@ void plan_attn_forward(int dtype, AttnArgs& a) {
   }
 }
 
-void plan_attn_dq(int, AttnArgs& a) {
+// (A turn's time as measured: 4 waves of 32 rows.)
+void plan_attn_dq(int dtype, AttnArgs& a) {
+  const bool far = a.dim > 64;
   a.tiles = (int)(((int64_t)a.rows + 127) / 128);
-  a.splits = splits_for((int64_t)a.tiles * a.kv_heads * a.batch, a.keys, 256);
+  a.splits = splits_for((int64_t)a.tiles * a.kv_heads * a.batch, ((int64_t)a.keys + 31) / 32, dtype == kF32 ? (far ? 6.0 : 3.0) : far ? 0.7 : 0.45,
+                        4.0 * a.batch * a.heads * a.queries * a.dim);
 }
 
-void plan_attn_dkv(int, AttnArgs& a) {
+void plan_attn_dkv(int dtype, AttnArgs& a) {
+  const bool far = a.dim > 64;
   a.tiles = (int)(((int64_t)a.keys + 127) / 128);
-  a.splits = splits_for((int64_t)a.tiles * a.kv_heads * a.batch, (int64_t)a.group * ((a.queries + 63) / 64), 2);
+  a.splits = splits_for((int64_t)a.tiles * a.kv_heads * a.batch, (int64_t)a.group * ((a.queries + 31) / 32), dtype == kF32 ? (far ? 8.0 : 4.0) : far ? 1.0 : 0.6,
+                        8.0 * a.batch * a.kv_heads * a.keys * a.dim);
 }
 
 template <typename T> __global__ __launch_bounds__(256) void attn_join(AttnJoinArgs a) {
-  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < a.count; i += (int64_t)gridDim.x * 1024) {
+  for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; at < a.count * a.outs; at += (int64_t)gridDim.x * 1024) {
+    const int which = at >= a.count;
+    T* out = (T*)a.out[which] + (at - which * a.count);
+    if (!a.out[which]) continue;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int s = 0; s < a.splits; s++) {
-      const Pack<float, 4> p = load_pack<float, 4>(a.part + s * a.apart + i);
+      const Pack<float, 4> p = load_pack<float, 4>(a.part + s * (a.count * a.outs) + at);
 #pragma unroll
       for (int j = 0; j < 4; j++) v[j] += p.v[j];
     }
     Pack<T, 4> o;
 #pragma unroll
-    for (int j = 0; j < 4; j++) o.v[j] = (T)(v[j] * a.scale);
-    store_pack<T, 4>((T*)a.out + i, o);
+    for (int j = 0; j < 4; j++) o.v[j] = (T)(v[j] * a.scale[which]);
+    store_pack<T, 4>(out, o);
   }
 }
 
 hipError_t launch_attn_join(int dtype, const AttnJoinArgs& a, hipStream_t st) {
-  const int64_t blocks = (a.count / 4 + 255) / 256;
+  const int64_t blocks = (a.count * a.outs / 4 + 255) / 256;
   const dim3 grid((unsigned)(blocks < 2048 ? blocks : 2048));
   if (dtype == kF32) return launch_kernel(attn_join<float>, grid, 256, st, a);
   if (dtype == kF16) return launch_kernel(attn_join<_Float16>, grid, 256, st, a);

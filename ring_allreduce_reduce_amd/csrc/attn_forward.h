@@ -171,8 +171,12 @@ __device__ inline void AttnForward<T, D, KT, NQ, NK>::run(const AttnArgs& a, cha
   f32x16 s[kBlocks];
   Frag p[kFrags];
   issue_k(0);
-  arrive();
   issue_k(1);
+  issue_v(0);
+  // the first keys; what follows them may still be on its way
+  if (mine > 1) wait_lds<2 * Tile::kLoads>();
+  else wait_lds<Tile::kLoads>();
+  if constexpr (NQ > 1) block_barrier();
   if (mine > 0) {
     only_scores();
     end_scores(s);
@@ -183,7 +187,7 @@ __device__ inline void AttnForward<T, D, KT, NQ, NK>::run(const AttnArgs& a, cha
   auto start = [&](int turn) {
     arrive();
     issue_k(turn + 2);
-    issue_v(turn);
+    if (turn > 0) issue_v(turn);
     read.other(Tile::kBytes);
   };
   if (turns > 0) {

@@ -14,9 +14,17 @@
 // ones value by value.
 #pragma once
 
+#include <utility>
+
 #include "attn_types.h"
 
 namespace ringar {
+
+// f(0), f(1), .. f(N - 1), the number a constant of each call.
+template <typename F, int... I> __device__ inline void each_of(F& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F> __device__ inline void each(F f) { each_of(f, std::make_integer_sequence<int, N>()); }
 
 #define RINGAR_LDS __attribute__((address_space(3)))
 
@@ -59,11 +67,12 @@ __device__ inline f32x16 zero16() { return f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 
 
 __device__ inline float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Waits until the wave's loads into LDS have landed and its reads are done;
-// the empty asm keeps memory accesses from moving over it.
-__device__ inline void wait_lds() {
+// Waits until all but the wave's last N loads into LDS have landed and its reads
+// are done; the empty asm keeps memory accesses from moving over it.
+template <int N = 0> __device__ inline void wait_lds() {
+  static_assert(N < 64, "the counter has six bits");
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x70);
+  __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | (N >> 4 << 14));
   asm volatile("" ::: "memory");
 }
 __device__ inline void block_barrier() {
@@ -181,7 +190,11 @@ template <typename T, int R> struct FragReader {
     }
   }
 
-  // On to the other of two buffers, `apart` bytes (a power of two) away.
+  __device__ inline void move_cols(int by) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) col[i] ^= by;
+  }
+  // On to another buffer: its place differs in the bits of `apart`.
   __device__ inline void other(int apart) {
 #pragma unroll
     for (int i = 0; i < 4; i++) {

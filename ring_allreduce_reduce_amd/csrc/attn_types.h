@@ -36,14 +36,14 @@ struct AttnArgs {
   void *dq, *dk, *dv;      // contiguous
 };
 
-// dq, dk, dv as sums of `splits` parts, in order
+// one gradient, or two side by side, as sums of `splits` parts, in order
 struct AttnJoinArgs {
-  const float* part;
-  void* out;
+  const float* part;       // [split][out][count]
+  void* out[2];            // null: not wanted
+  float scale[2];
   int64_t count;
-  int64_t apart;           // values from part to part
+  int outs;
   int splits;
-  float scale;
 };
 
 int64_t attn_blocks(const AttnArgs& a);
