@@ -69,7 +69,7 @@ template <typename T, int D> struct AttnDq {
   static constexpr int NW = 4, kThreads = 64 * NW, KT = 32;
   using Tile = RowTile<T, D, KT, NW>;
   static constexpr int kSteps = D / M::kK, kDims = D / 32;
-  static constexpr int kShared = 8 * Tile::kBytes;
+  static constexpr int kShared = 8 * Tile::kPlace;
   static constexpr int kBlocksPerCu = D * sizeof(T) > 256 ? 1 : 2;     // registers
 
   static __device__ inline void run(const AttnArgs& a, char* smem) {
@@ -109,13 +109,13 @@ template <typename T, int D> struct AttnDq {
     tv.start(pitch_v, a.dim, wave, lane);
     auto issue = [&](int turn) {              // of the turns in order
       if (turn >= turns) return;
-      char* lds = smem + (turn & 3) * Tile::kBytes;
+      char* lds = smem + (turn & 3) * Tile::kPlace;
       tk.load(keys.next(), lds, wave);
-      tv.load(values.next(), lds + 4 * Tile::kBytes, wave);
+      tv.load(values.next(), lds + 4 * Tile::kPlace, wave);
     };
 
     FragReader<T, KT> read(smem, lane);
-    read.move_cols(2 * Tile::kBytes);         // rows of the buffer at hand, columns of that two turns back
+    read.move_cols(2 * Tile::kPlace);         // rows of the buffer at hand, columns of that two turns back
     constexpr int kMmaQ = 32 / M::kK * kDims, kMma = kMmaQ + 2 * kSteps, kAhead = 3, kFrags = 32 / M::kK;
     f32x16 acc[kDims], s, dp, begun_s, begun_dp;
     Frag kf[kAhead], ds[kFrags], ds_next[kFrags];
@@ -124,7 +124,7 @@ template <typename T, int D> struct AttnDq {
     // the turn's matrix instructions: dS k, then q k^T and dy v^T but for their last step
     auto frag = [&](int m) {
       if (m < kMmaQ) return read.cols(0, m / kDims * M::kK, m % kDims * 32);
-      return read.rows((m - kMmaQ) & 1 ? 4 * Tile::kBytes : 0, 0, (m - kMmaQ) / 2);
+      return read.rows((m - kMmaQ) & 1 ? 4 * Tile::kPlace : 0, 0, (m - kMmaQ) / 2);
     };
     auto products = [&](int from, int to, auto before, auto with) {
 #pragma unroll
@@ -163,7 +163,7 @@ template <typename T, int D> struct AttnDq {
       wait_lds();
       block_barrier();
       issue(turn + 2);
-      read.other((turn & 1 ? 3 : 1) * Tile::kBytes);      // on to buffer (turn + 1) % 4
+      read.other((turn & 1 ? 3 : 1) * Tile::kPlace);      // on to buffer (turn + 1) % 4
     };
     const int left = at.length - (last - 1) * KT, whole = left < KT ? turns - 1 : turns;
     if (turns > 0) {
@@ -201,7 +201,7 @@ template <typename T, int D> struct AttnDq {
         products(0, kMmaQ, [] {}, nothing);
         slopes(left);
       }
-      read.other((turns & 1 ? 3 : 1) * Tile::kBytes);
+      read.other((turns & 1 ? 3 : 1) * Tile::kPlace);
       products(0, kMmaQ, [] {}, nothing);
     }
     if (!exists) return;
@@ -233,7 +233,7 @@ template <typename T, int D, int QT, bool VLDS> struct AttnDkv {
   using Tile = RowTile<T, D, QT, NW>;
   static constexpr int kSteps = D / M::kK, kDims = D / 32;
   // two buffers of Q and dy, and of the tile's lse2 and delta (64 floats each)
-  static constexpr int kStage = 2 * Tile::kBytes;
+  static constexpr int kStage = 2 * Tile::kPlace;
   using Values = RowTile<T, D, kKeys, NW>;                 // VLDS: the block's values stay in LDS
   static constexpr int kStats = 2 * kStage, kValues = kStats + 2 * 512;
   static constexpr int kShared = kValues + (VLDS ? Values::kBytes : 0);
@@ -290,7 +290,7 @@ template <typename T, int D, int QT, bool VLDS> struct AttnDkv {
       }
       char* lds = smem + buf * kStage;
       tq.load(queries.next(), lds, wave);
-      tdy.load(grads.next(), lds + Tile::kBytes, wave);
+      tdy.load(grads.next(), lds + Tile::kPlace, wave);
       const uint32_t to = (uint32_t)(uintptr_t)(RINGAR_LDS void*)smem + kStats + buf * 512;
       const u32x4 l = lse2s.next(), d = deltas.next();
       if (wave == 0) load_lds_word(lane * 4, l, to);
@@ -320,8 +320,8 @@ template <typename T, int D, int QT, bool VLDS> struct AttnDkv {
 #pragma unroll
         for (int i = 0; i < kSteps; i++) {
           s = M::run(read.rows(0, b * 32, i), k.f[i], s);
-          if constexpr (VLDS) dp = M::run(read.rows(Tile::kBytes, b * 32, i), read_v.rows(wave * 32 * 128, 0, i), dp);
-          else dp = M::run(read.rows(Tile::kBytes, b * 32, i), v.f[i], dp);
+          if constexpr (VLDS) dp = M::run(read.rows(Tile::kPlace, b * 32, i), read_v.rows(wave * 32 * 128, 0, i), dp);
+          else dp = M::run(read.rows(Tile::kPlace, b * 32, i), v.f[i], dp);
           // (not more fragments ahead than there are registers)
           if (i % 2) __builtin_amdgcn_sched_barrier(0);
         }
@@ -348,7 +348,7 @@ template <typename T, int D, int QT, bool VLDS> struct AttnDkv {
           const Frag pf = result_frag<T>(p + f * kEach), df = result_frag<T>(ds + f * kEach);
 #pragma unroll
           for (int i = 0; i < kDims; i++) {
-            dv[i] = M::run(read.cols(Tile::kBytes, b * 32 + f * M::kK, i * 32), pf, dv[i]);
+            dv[i] = M::run(read.cols(Tile::kPlace, b * 32 + f * M::kK, i * 32), pf, dv[i]);
             dk[i] = M::run(read.cols(0, b * 32 + f * M::kK, i * 32), df, dk[i]);
             __builtin_amdgcn_sched_barrier(0);
           }
@@ -398,12 +398,18 @@ template <typename T> hipError_t attn_delta_of(const AttnArgs& a, hipStream_t st
 template <typename T> hipError_t attn_dq_of(const AttnArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)attn_blocks(a));
   if (a.dim <= 64) return launch_kernel(attn_dq<AttnDq<T, 64>>, grid, 256, st, a);
+  if constexpr (sizeof(T) == 4) {
+    if (a.dim <= 96) return launch_kernel(attn_dq<AttnDq<T, 96>>, grid, 256, st, a);
+  }
   return launch_kernel(attn_dq<AttnDq<T, 128>>, grid, 256, st, a);
 }
 
 template <typename T> hipError_t attn_dkv_of(const AttnArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)attn_blocks(a));
   if (a.dim <= 64) return launch_kernel(attn_dkv<AttnDkv<T, 64, 64, false>>, grid, 256, st, a);
+  if constexpr (sizeof(T) == 4) {
+    if (a.dim <= 96) return launch_kernel(attn_dkv<AttnDkv<T, 96, 32, false>>, grid, 256, st, a);
+  }
   return launch_kernel(attn_dkv<AttnDkv<T, 128, 32, sizeof(T) == 2>>, grid, 256, st, a);
 }
 

@@ -26,11 +26,14 @@ static int splits_for(int64_t blocks, int64_t turns, double turn, double part) {
 
 int64_t attn_blocks(const AttnArgs& a) { return (int64_t)a.tiles * a.splits * a.kv_heads * a.batch; }
 
+// Columns that a kernel computes for head_dim.
+static int padded(int dtype, int dim) { return dim <= 64 ? 64 : dtype == kF32 && dim <= 96 ? 96 : 128; }
+
 // The forward pass's form and its parts along the keys: the one whose time, put
 // together from what was measured over 1 .. 1024 queries, 500 .. 65536 keys, 1
 // .. 64 sequences and 1 .. 20 heads, is the least.  In us:
 //   a turn of one wave (32 rows, 32 keys): 0.33 at head_dim 64, 0.46 at 128, fp32
-//   2.0 and 4.5 (one wave a SIMD and two cost the same a turn: the clock drops);
+//   0.034 for each of 64, 96 or 128 columns (one wave a SIMD and two cost the same a turn: the clock drops);
 //   of few rows, each wave's tiles on its own: 0.45 at least where other blocks
 //   read them too, 0.75 where they come from memory;
 //   start and end 5; a second launch 3.5 and 0.3 a part, and the parts' bytes;
@@ -38,9 +41,10 @@ int64_t attn_blocks(const AttnArgs& a) { return (int64_t)a.tiles * a.splits * a.
 void plan_attn_forward(int dtype, AttnArgs& a) {
   const bool wide = dtype == kF32, far = a.dim > 64;
   const double bytes = 2.0 * a.keys * a.kv_heads * a.batch * a.dim * (wide ? 4 : 2);
-  const double turn = wide ? (far ? 4.5 : 2.0) : far ? 0.46 : 0.33;
+  const double turn = wide ? 0.034 * padded(dtype, a.dim) : far ? 0.46 : 0.33;
   double best = 0;
   for (int form = a.rows <= 32 ? kFewRows : kManyRows; form <= kFewRows; form++) {
+    if (form == kSomeRows && wide && far) continue;
     const int rows = form == kFewRows ? 32 : 128;
     const int groups = form == kManyRows ? 1 : form == kSomeRows ? 2 : wide && far ? 2 : 4;       // along the keys
     const int64_t tiles = ((int64_t)a.rows + rows - 1) / rows, units = tiles * a.kv_heads * a.batch;
@@ -69,14 +73,14 @@ void plan_attn_forward(int dtype, AttnArgs& a) {
 void plan_attn_dq(int dtype, AttnArgs& a) {
   const bool far = a.dim > 64;
   a.tiles = (int)(((int64_t)a.rows + 127) / 128);
-  a.splits = splits_for((int64_t)a.tiles * a.kv_heads * a.batch, ((int64_t)a.keys + 31) / 32, dtype == kF32 ? (far ? 6.0 : 3.0) : far ? 0.7 : 0.45,
+  a.splits = splits_for((int64_t)a.tiles * a.kv_heads * a.batch, ((int64_t)a.keys + 31) / 32, dtype == kF32 ? 0.047 * padded(dtype, a.dim) : far ? 0.7 : 0.45,
                         4.0 * a.batch * a.heads * a.queries * a.dim);
 }
 
 void plan_attn_dkv(int dtype, AttnArgs& a) {
   const bool far = a.dim > 64;
   a.tiles = (int)(((int64_t)a.keys + 127) / 128);
-  a.splits = splits_for((int64_t)a.tiles * a.kv_heads * a.batch, (int64_t)a.group * ((a.queries + 31) / 32), dtype == kF32 ? (far ? 8.0 : 4.0) : far ? 1.0 : 0.6,
+  a.splits = splits_for((int64_t)a.tiles * a.kv_heads * a.batch, (int64_t)a.group * ((a.queries + 31) / 32), dtype == kF32 ? 0.062 * padded(dtype, a.dim) : far ? 1.0 : 0.6,
                         8.0 * a.batch * a.kv_heads * a.keys * a.dim);
 }
 

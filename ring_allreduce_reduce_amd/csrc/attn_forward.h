@@ -37,11 +37,11 @@ template <typename T, int D, int KT, int NQ, int NK> struct AttnForward {
   using Tile = RowTile<T, D, KT, NQ>;
   static constexpr int kThreads = 64 * NQ * NK;
   static constexpr int kSteps = D / M::kK, kBlocks = KT / 32, kDims = D / 32;
-  static constexpr int kGroup = 4 * Tile::kBytes;         // a group's buffers: two of keys, two of values
+  static constexpr int kGroup = 4 * Tile::kPlace;         // a group's buffers: two of keys, two of values
   static constexpr int kLaneSums = (kDims * 16 + 4) * 4;  // bytes of a lane's sums, its maximum and sum
   static constexpr int kJoin = (NK - 1) * NQ * 64 * kLaneSums;
   static constexpr int kShared = NK * kGroup > kJoin ? NK * kGroup : kJoin;
-  static constexpr int kBlocksPerCu = kThreads <= 256 && kShared <= 80 * 1024 ? 2 : 1;
+  static constexpr int kBlocksPerCu = kThreads <= 256 && kShared <= 80 * 1024 && D * sizeof(T) <= 384 ? 2 : 1;      // LDS, registers
   // waves that read a tile must all have it, and be done with it, together
   static __device__ inline void arrive() {
     wait_lds();
@@ -80,10 +80,10 @@ __device__ inline void AttnForward<T, D, KT, NQ, NK>::run(const AttnArgs& a, cha
   char* buffers = smem + group * kGroup;
   // of the turns in order
   auto issue_k = [&](int turn) {
-    if (turn < mine) tk.load(keys.next(), buffers + (turn & 1) * Tile::kBytes, wq);
+    if (turn < mine) tk.load(keys.next(), buffers + (turn & 1) * Tile::kPlace, wq);
   };
   auto issue_v = [&](int turn) {
-    if (turn < mine) tv.load(values.next(), buffers + (2 + (turn & 1)) * Tile::kBytes, wq);
+    if (turn < mine) tv.load(values.next(), buffers + (2 + (turn & 1)) * Tile::kPlace, wq);
   };
 
   // fragments of keys (b: 32 of them, s: step) and of values (f: step, i: 32 columns)
@@ -91,7 +91,7 @@ __device__ inline void AttnForward<T, D, KT, NQ, NK>::run(const AttnArgs& a, cha
   constexpr int kAhead = 3;                   // fragments read before they are used
   constexpr int kMmaS = kBlocks * kSteps, kMmaV = KT / M::kK * kDims;
   auto key_frag = [&](int m) { return read.rows(0, m % kBlocks * 32, m / kBlocks); };
-  auto value_frag = [&](int m) { return read.cols(2 * Tile::kBytes, m / kDims * M::kK, m % kDims * 32); };
+  auto value_frag = [&](int m) { return read.cols(2 * Tile::kPlace, m / kDims * M::kK, m % kDims * 32); };
 
   constexpr int kFrags = KT / M::kK, kValues = kBlocks * 16;      // P's fragments; a lane's scores
   f32x16 o[kDims];
@@ -188,7 +188,7 @@ __device__ inline void AttnForward<T, D, KT, NQ, NK>::run(const AttnArgs& a, cha
     arrive();
     issue_k(turn + 2);
     if (turn > 0) issue_v(turn);
-    read.other(Tile::kBytes);
+    read.other(Tile::kPlace);
   };
   if (turns > 0) {
     start(0);
@@ -237,7 +237,7 @@ __device__ inline void AttnForward<T, D, KT, NQ, NK>::run(const AttnArgs& a, cha
     // the last tile's values (a group whose last turn is missing keeps the others company)
     if (NQ > 1 && NK > 1 && mine > 0 && mine < turns) arrive();
     arrive();
-    read.other(Tile::kBytes);
+    read.other(Tile::kPlace);
     if (mine > 0) products(0, kMmaV, p, kBefore, kNothing);
   }
   float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
@@ -347,15 +347,19 @@ template <typename T> hipError_t attn_forward_of(const AttnArgs& a, hipStream_t 
     return launch_kernel(attn_forward<K>, dim3((unsigned)attn_blocks(a)), K::kThreads, st, a);
   };
   constexpr bool kWide = sizeof(T) == 4;
-  hipError_t e;
+  hipError_t e = hipSuccess;
+  // (fp32 beyond 64: no registers for eight waves, LDS for two of few rows')
   if (a.dim <= 64) {
     if (a.form == kManyRows) e = go(AttnForward<T, 64, kWide ? 32 : 64, 4, 1>());
     else if (a.form == kSomeRows) e = go(AttnForward<T, 64, kWide ? 32 : 64, 4, 2>());
     else e = go(AttnForward<T, 64, 32, 1, 4>());
+  } else if constexpr (kWide) {
+    if (a.dim <= 96) e = a.form == kManyRows ? go(AttnForward<T, 96, 32, 4, 1>()) : go(AttnForward<T, 96, 32, 1, 2>());
+    else e = a.form == kManyRows ? go(AttnForward<T, 128, 32, 4, 1>()) : go(AttnForward<T, 128, 32, 1, 2>());
   } else {
-    if (a.form == kManyRows) e = go(AttnForward<T, 128, kWide ? 32 : 64, 4, 1>());
-    else if (a.form == kSomeRows) e = go(AttnForward<T, 128, kWide ? 32 : 64, 4, 2>());
-    else e = go(AttnForward<T, 128, 32, 1, kWide ? 2 : 4>());
+    if (a.form == kManyRows) e = go(AttnForward<T, 128, 64, 4, 1>());
+    else if (a.form == kSomeRows) e = go(AttnForward<T, 128, 64, 4, 2>());
+    else e = go(AttnForward<T, 128, 32, 1, 4>());
   }
   if (e != hipSuccess || a.splits == 1) return e;
   // four values a thread

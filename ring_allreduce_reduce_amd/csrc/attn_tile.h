@@ -136,8 +136,10 @@ template <typename T, int D, int R, int NW> struct RowTile {
   static constexpr int kChunk = 16 / sizeof(T);
   static constexpr int kLines = D * (int)sizeof(T) / 128;
   static constexpr int kBytes = R * D * (int)sizeof(T);
+  static constexpr int kPlace = kBytes & (kBytes - 1) ? (kBytes / 3) * 4 : kBytes;      // a buffer: a power of two
   static constexpr int kLoads = kBytes / 1024 / NW;
   static_assert(kLoads * NW * 1024 == kBytes && R % 32 == 0, "every wave loads the same share");
+  static_assert((kPlace & (kPlace - 1)) == 0, "rows of one, or of three, powers of two");
   static constexpr uint32_t kOutside = 0x80000000u;   // past the end of any buffer
 
   uint32_t off[kLoads];
@@ -156,10 +158,9 @@ template <typename T, int D, int R, int NW> struct RowTile {
   // anything reads what they bring.
   __device__ inline void load(u32x4 buffer, char* lds, int wave) const {
     const uint32_t to = (uint32_t)(uintptr_t)(RINGAR_LDS void*)lds + wave * 1024;
-    if constexpr (kLoads == 1) load_lds(off[0], buffer, to);
-    else
 #pragma unroll
-      for (int i = 0; i < kLoads; i += 2) load_lds2<NW * 1024>(off[i], off[i + 1], buffer, to + i * NW * 1024);
+    for (int i = 0; i + 1 < kLoads; i += 2) load_lds2<NW * 1024>(off[i], off[i + 1], buffer, to + i * NW * 1024);
+    if constexpr (kLoads % 2) load_lds(off[kLoads - 1], buffer, to + (kLoads - 1) * NW * 1024);
   }
 };
 
