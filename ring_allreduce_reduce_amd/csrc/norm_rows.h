@@ -113,9 +113,10 @@ template <typename T, int TPR, int E, int V> struct Row {
 // Blocks of a kernel that loops over what it has too few of.
 inline unsigned capped(int64_t blocks, int threads) { return (unsigned)(blocks < most_blocks(threads) ? blocks : most_blocks(threads)); }
 
-// Outputs that the XCDs' L2s (32 MB together) cannot hold anyway go past them
-// (layer norm 16384 x 8192 bf16 forward: 87 us, not 115; 16384 x 4096 backward:
-// 70, not 82); smaller ones stay for whoever reads them next.
+// Outputs (of `cols` values a row, all of them together) that the XCDs' L2s (32
+// MB together) cannot hold anyway go past them (layer norm 16384 x 8192 bf16
+// forward: 87 us, not 115; 16384 x 4096 backward: 70, not 82); smaller ones
+// stay for whoever reads them next.
 inline bool beyond_l2(int dtype, int64_t rows, int64_t cols) { return rows * cols * (dtype == kF32 ? 4 : 2) > 32ll << 20; }
 
 }  // namespace ringar
