@@ -10,7 +10,7 @@ using namespace ringar;
 namespace {
 
 constexpr int kMostDim = 128;
-constexpr int64_t kMostPitch = 1 << 25;       // bytes from row to row: a tile's offsets stay below 2^31
+constexpr int64_t kMostPitch = 1 << 24;       // bytes from row to row: the offsets of 128 rows stay below 2^31
 
 // An array of head rows: [batch][rows][heads][dim].
 struct Array {
@@ -48,7 +48,7 @@ ringar_result_t check_array(Array& a) {
     if (a.stride[i] > (int64_t)1 << 48) return refuse(RINGAR_ERR_INVALID_ARGUMENT, name + ": a stride beyond 2^48 elements");
     if (a.stride[i] * a.es % 16) return refuse(RINGAR_ERR_INVALID_ARGUMENT, name + ": rows must start at 16-byte boundaries");
   }
-  if (a.stride[1] * (int64_t)a.es >= kMostPitch) return refuse(RINGAR_ERR_INVALID_ARGUMENT, name + ": row stride of 2^25 bytes or more");
+  if (a.n[1] > 1 && a.stride[1] * (int64_t)a.es >= kMostPitch) return refuse(RINGAR_ERR_INVALID_ARGUMENT, name + ": row stride of 2^24 bytes or more");
   if (end_of(a) >> 63) return refuse(RINGAR_ERR_INVALID_ARGUMENT, name + " reaches beyond the address space");
   if (!a.output) return RINGAR_SUCCESS;
   // no row of an output over another: from the smallest stride on, each passes all that lies within it

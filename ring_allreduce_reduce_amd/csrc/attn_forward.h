@@ -151,7 +151,7 @@ __device__ inline void AttnForward<T, D, KT, NQ, NK>::run(const AttnArgs& a, cha
     for (int i = 0; i < kValues; i++) most = fmaxf(most, s[i / 16][i % 16]);
     most = fmaxf(most, __shfl_xor(most, 32)) * a.scale2;
     const float raised = fmaxf(top, most), by = raised == -INFINITY ? 1.0f : fast_exp2(top - raised);
-    top = raised == -INFINITY ? 0.0f : raised;        // (no finite score yet: any m will do)
+    top = raised == -INFINITY ? -3e38f : raised;      // (no finite score yet: the first one passes any m of use)
 #pragma unroll
     for (int i = 0; i < 4; i++) sums[i] *= by;
 #pragma unroll

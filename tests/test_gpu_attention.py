@@ -158,6 +158,44 @@ def test_scores_far_apart_and_far_from_zero(dtype):
             assert_within(a, c, e, what)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lq", [1, 150])
+def test_scores_of_minus_infinity_before_very_low_ones(lq, dtype):
+    """The first tiles have no finite score, the later ones scores near -1000:
+    the row is that of the later ones alone."""
+    g = _gen("infinite", lq, dtype)
+    q, k, v = _rand(g, (1, lq, 1, 64), dtype), _rand(g, (1, 400, 1, 64), dtype), _rand(g, (1, 400, 1, 64), dtype)
+    q[..., 0] = 100.0
+    k[..., 0] = -80.0
+    q[..., 1] = 2.0 ** 70
+    k[..., 1] = 0.0
+    k[:, :192, :, 1] = -2.0 ** 70
+    y, lse = ra.cross_attention(q, k, v, stats=True)
+    k = k[:, 192:].contiguous()
+    q[..., 1] = 0.0
+    want, bound = L.attention(q, k, v[:, 192:], None, None)
+    assert_within(y, want[0], bound[0], "y")
+    assert ((lse.double().cpu() - want[1]).abs() <= bound[1]).all() and (lse < -900).all()
+
+
+def test_row_strides_up_to_the_largest():
+    """128 rows of keys 2^24 - 16 bytes apart, and more than that refused."""
+    g = _gen("pitch")
+    for d in (64, 128):
+        pitch = (1 << 23) - 8
+        big = torch.zeros(130 * pitch + 4096, dtype=BF16, device="cuda")
+        k, v = (big.as_strided((1, 130, 1, d), (0, pitch, 0, 1), at) for at in (0, 256))
+        k.copy_(_rand(g, k.shape, BF16))
+        v.copy_(_rand(g, v.shape, BF16))
+        q, dy = _rand(g, (1, 33, 1, d), BF16), _rand(g, (1, 33, 1, d), BF16)
+        y, lse = ra.cross_attention(q, k, v, stats=True)
+        assert torch.equal(y, ra.cross_attention(q, k.contiguous(), v.contiguous()))
+        for a, b in zip(ra.cross_attention_backward(dy, q, k, v, y, lse), ra.cross_attention_backward(dy, q, k.contiguous(), v.contiguous(), y, lse)):
+            assert torch.equal(a, b)
+        with pytest.raises(ra.RingarError):
+            ra.cross_attention(q, big.as_strided((1, 100, 1, d), (0, 1 << 23, 0, 1)), v[:, :100])
+
+
 def test_long_inputs_and_few_sequences():
     """Keys split over blocks, forward and backward."""
     for dtype, n in ((BF16, 20011), (F32, 9001)):

@@ -6,7 +6,6 @@ import os
 import subprocess
 
 import pytest
-import torch
 
 import libutil
 import ring_allreduce_reduce_amd as ra
@@ -113,6 +112,7 @@ def test_nothing_to_do_needs_no_gpu():
 
 
 def test_tensor_calls_refuse_what_is_no_operand():
+    import torch
     libutil.lib()
     t, q, stats = torch.zeros(4, 8), torch.zeros(1, 2, 3, 8), torch.zeros(4)
     z = torch.randn(4, 8, dtype=torch.complex64).conj().imag
