@@ -74,6 +74,7 @@ template <typename T, int D> struct AttnDq {
 
   static __device__ inline void run(const AttnArgs& a, char* smem) {
     const AttnPlace at(a);
+    if (!at.valid) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = (at.tile * NW + wave) * 32 + (lane & 31);
     const bool exists = r < a.rows;
@@ -242,6 +243,7 @@ template <typename T, int D, int QT, bool VLDS> struct AttnDkv {
 
   static __device__ inline void run(const AttnArgs& a, char* smem) {
     const AttnPlace at(a);
+    if (!at.valid) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int key = (at.tile * NW + wave) * 32 + (lane & 31);
     const bool exists = key < at.length;

@@ -6,15 +6,20 @@
 
 namespace ringar {
 
+// Blocks that count: of unlike lengths, which the host does not know, a fourth is
+// taken to be missing (3 x 333 x 1501, 20 heads of 64, lengths 1501, 0 and 1434:
+// 15.5 us, planned for whole ones 18.4).
+static int64_t busy(const AttnArgs& a, int64_t blocks) { return a.lengths ? (blocks * 3 + 3) / 4 : blocks; }
+
 // Parts of what the backward kernels' blocks go along, `turns` of 32 rows of
 // `turn` us each: one round of blocks on the 256 CUs after the other, and for
 // parts a second launch and what it reads and writes (`part` bytes each).
-static int splits_for(int64_t blocks, int64_t turns, double turn, double part) {
+static int splits_for(const AttnArgs& a, int64_t blocks, int64_t turns, double turn, double part) {
   double best = 0;
   int splits = 1;
   for (int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
     if (s > 1 && s > turns) break;
-    const double rounds = (double)((blocks * s + 255) / 256);
+    const double rounds = (double)((busy(a, blocks * s) + 255) / 256);
     const double us = rounds * (double)((turns + s - 1) / s + 1) * turn + (s > 1 ? 4 + 0.3 * s + s * part * 2 / 4e6 : 0);
     if (best == 0 || us < 0.97 * best) {
       best = us;
@@ -24,7 +29,19 @@ static int splits_for(int64_t blocks, int64_t turns, double turn, double part) {
   return splits;
 }
 
-int64_t attn_blocks(const AttnArgs& a) { return (int64_t)a.tiles * a.splits * a.kv_heads * a.batch; }
+// Blocks of the grid: whole rounds of pieces over the XCDs.
+int64_t attn_blocks(const AttnArgs& a) {
+  const int64_t pieces = (int64_t)a.pieces * a.kv_heads * a.batch;
+  return (pieces + 7) / 8 * 8 * a.piece;
+}
+
+// Pieces: a key head's blocks, or less where there are few key heads (64 pieces
+// in all, then).
+static void deal(AttnArgs& a) {
+  const int64_t each = (int64_t)a.tiles * a.splits, piece = each * a.kv_heads * a.batch / 64;
+  a.pieces = (int)(piece < 1 ? each : piece < each ? (each + piece - 1) / piece : 1);
+  a.piece = (int)((each + a.pieces - 1) / a.pieces);       // (of like sizes: neighbours lie on different XCDs)
+}
 
 // Columns that a kernel computes for head_dim.
 static int padded(int dtype, int dim) { return dim <= 64 ? 64 : dtype == kF32 && dim <= 96 ? 96 : 128; }
@@ -40,7 +57,7 @@ static int padded(int dtype, int dim) { return dim <= 64 ? 64 : dtype == kF32 &&
 //   keys and values from memory once at 5 TB/s, and to every block at 18.
 void plan_attn_forward(int dtype, AttnArgs& a) {
   const bool wide = dtype == kF32, far = a.dim > 64;
-  const double bytes = 2.0 * a.keys * a.kv_heads * a.batch * a.dim * (wide ? 4 : 2);
+  const double bytes = (a.lengths ? 1.5 : 2.0) * a.keys * a.kv_heads * a.batch * a.dim * (wide ? 4 : 2);
   const double turn = wide ? 0.034 * padded(dtype, a.dim) : far ? 0.46 : 0.33;
   double best = 0;
   for (int form = a.rows <= 32 ? kFewRows : kManyRows; form <= kFewRows; form++) {
@@ -51,7 +68,7 @@ void plan_attn_forward(int dtype, AttnArgs& a) {
     for (int splits : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
       if (splits > 1 && (int64_t)splits * 128 > a.keys) break;
       const double turns = (double)(((int64_t)a.keys + 32 * groups * splits - 1) / (32 * groups * splits));
-      const double rounds = (double)((units * splits + 255) / 256);      // blocks of a CU
+      const double rounds = (double)((busy(a, units * splits) + 255) / 256);      // blocks of a CU
       double work = rounds * turns;
       if (form == kSomeRows) work *= rounds > 1 ? 2.0 : 1.8;
       const double wait = (form != kFewRows ? 0.0 : tiles > 1 ? 0.45 : 0.75) / rounds;
@@ -67,21 +84,24 @@ void plan_attn_forward(int dtype, AttnArgs& a) {
       }
     }
   }
+  deal(a);
 }
 
 // (A turn's time as measured: 4 waves of 32 rows.)
 void plan_attn_dq(int dtype, AttnArgs& a) {
   const bool far = a.dim > 64;
   a.tiles = (int)(((int64_t)a.rows + 127) / 128);
-  a.splits = splits_for((int64_t)a.tiles * a.kv_heads * a.batch, ((int64_t)a.keys + 31) / 32, dtype == kF32 ? 0.047 * padded(dtype, a.dim) : far ? 0.7 : 0.45,
+  a.splits = splits_for(a, (int64_t)a.tiles * a.kv_heads * a.batch, ((int64_t)a.keys + 31) / 32, dtype == kF32 ? 0.047 * padded(dtype, a.dim) : far ? 0.7 : 0.45,
                         4.0 * a.batch * a.heads * a.queries * a.dim);
+  deal(a);
 }
 
 void plan_attn_dkv(int dtype, AttnArgs& a) {
   const bool far = a.dim > 64;
   a.tiles = (int)(((int64_t)a.keys + 127) / 128);
-  a.splits = splits_for((int64_t)a.tiles * a.kv_heads * a.batch, (int64_t)a.group * ((a.queries + 31) / 32), dtype == kF32 ? 0.062 * padded(dtype, a.dim) : far ? 1.0 : 0.6,
+  a.splits = splits_for(a, (int64_t)a.tiles * a.kv_heads * a.batch, (int64_t)a.group * ((a.queries + 31) / 32), dtype == kF32 ? 0.062 * padded(dtype, a.dim) : far ? 1.0 : 0.6,
                         8.0 * a.batch * a.kv_heads * a.keys * a.dim);
+  deal(a);
 }
 
 template <typename T> __global__ __launch_bounds__(256) void attn_join(AttnJoinArgs a) {

@@ -54,6 +54,7 @@ template <typename T, int D, int KT, int NQ, int NK> struct AttnForward {
 template <typename T, int D, int KT, int NQ, int NK>
 __device__ inline void AttnForward<T, D, KT, NQ, NK>::run(const AttnArgs& a, char* smem) {
   const AttnPlace at(a);
+  if (!at.valid) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wq = wave % NQ, group = wave / NQ;
   const int r = (at.tile * NQ + wq) * 32 + (lane & 31);

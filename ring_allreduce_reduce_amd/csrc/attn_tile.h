@@ -250,26 +250,24 @@ template <typename T, int D> struct RowFrags {
   }
 };
 
-// Blocks go round the 8 XCDs in turn: each XCD gets a run of neighbours, which
-// share keys and values in its L2.
-__device__ inline int64_t xcd_run(unsigned block, unsigned total) {
-  const unsigned q = total >> 3, rest = total & 7, xcd = block & 7;
-  return xcd * q + (xcd < rest ? xcd : rest) + (block >> 3);
-}
-
-// Where block `id` works.
+// Where a block works.  Blocks go round the 8 XCDs in turn; those that share a
+// key head should share an L2, yet sequences of unlike lengths should not lie on
+// XCDs of their own.  So a key head's blocks (tiles x splits) are cut into pieces,
+// and pieces, not blocks, go round the XCDs.
 struct AttnPlace {
   int tile, split, kv_head, batch, length;
+  bool valid;                    // (the last round of pieces may be short, and a key head's last piece)
   __device__ inline AttnPlace(const AttnArgs& a) {
-    unsigned id = (unsigned)xcd_run(blockIdx.x, gridDim.x);
+    const unsigned each = a.tiles * a.splits, of_xcd = blockIdx.x >> 3;
+    const unsigned piece = of_xcd / a.piece * 8 + (blockIdx.x & 7), group = piece / a.pieces;
+    const unsigned id = piece % a.pieces * a.piece + of_xcd % a.piece;
+    valid = id < each && group < (unsigned)a.kv_heads * a.batch;
     tile = id % a.tiles;
-    id /= a.tiles;
-    split = id % a.splits;
-    id /= a.splits;
-    kv_head = id % a.kv_heads;
-    batch = id / a.kv_heads;
+    split = id / a.tiles;
+    kv_head = group % a.kv_heads;
+    batch = group / a.kv_heads;
     length = a.keys;
-    if (a.lengths) {
+    if (a.lengths && valid) {
       const int n = __builtin_amdgcn_readfirstlane(a.lengths[batch]);
       length = n < 0 ? 0 : n < a.keys ? n : a.keys;
     }

@@ -28,6 +28,7 @@ struct AttnArgs {
   // set by the plan
   int tiles;               // blocks along the rows (dk, dv: the keys)
   int splits;              // parts of what a block goes along
+  int piece, pieces;       // blocks of a piece, pieces of a key head's blocks
   int form;                // forward: how a block's waves share rows and keys
   float* part;             // splits > 1: [split][..] sums
   float* part_top;         // forward: [split][batch][kv head][row]: maximum, sum of exponentials
