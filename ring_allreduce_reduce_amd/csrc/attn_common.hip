@@ -36,11 +36,17 @@ int64_t attn_blocks(const AttnArgs& a) {
 }
 
 // Pieces: a key head's blocks, or less where there are few key heads (64 pieces
-// in all, then).
+// in all, then), of like sizes, as neighbours lie on different XCDs; single
+// blocks where whole rounds would pass what a launch takes.
 static void deal(AttnArgs& a) {
-  const int64_t each = (int64_t)a.tiles * a.splits, piece = each * a.kv_heads * a.batch / 64;
-  a.pieces = (int)(piece < 1 ? each : piece < each ? (each + piece - 1) / piece : 1);
-  a.piece = (int)((each + a.pieces - 1) / a.pieces);       // (of like sizes: neighbours lie on different XCDs)
+  const int64_t each = (int64_t)a.tiles * a.splits, groups = (int64_t)a.kv_heads * a.batch;
+  const int64_t pieces = groups ? (64 + groups - 1) / groups : 1;
+  a.pieces = (int)(pieces < each ? pieces : each);
+  a.piece = a.pieces ? (int)((each + a.pieces - 1) / a.pieces) : 0;
+  if (attn_blocks(a) > most_blocks(256)) {
+    a.pieces = (int)each;
+    a.piece = 1;
+  }
 }
 
 // Columns that a kernel computes for head_dim.
