@@ -9,7 +9,10 @@
 // sees every input and output once, one sum over the row's threads a row
 // (8 bits: and a maximum), fp32 throughout.  A group of 128 columns lies in 16
 // (fp32: 32) neighbouring lanes of one wave, so its maximum needs no LDS.
-// Memory bound.
+//
+// Memory bound.  A call takes, forward with a residual 16384 x 8192 bf16 197 us
+// (5.5 TB/s), in 8 bits with a scale for each 128 columns 2053 x 5120 fp16 18 us
+// (4.1 TB/s), backward 16384 x 4096 bf16 with its column sums 100 us (5.4 TB/s).
 #include "layer_types.h"
 #include "norm_rows.h"
 
