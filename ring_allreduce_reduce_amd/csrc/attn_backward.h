@@ -15,8 +15,9 @@
 // to the operands' type: what the matrix instructions take.  fp16 holds P times
 // 2^10 where it meets dy, so that the small P of long rows keep their bits.
 //
-// Times are medians.  8 x 1024 x 2048, 16 heads of 128, bf16: dq 203 us, dk and dv
-// 291 (1017 and 945 TFLOP/s of what they compute).  Tried for dk, dv and not kept:
+// Times are medians, ranges two GPUs.  8 x 1024 x 2048, 16 heads of 128, bf16: dq 203
+// .. 208 us, dk and dv 291 .. 301 (991 .. 1017 and 912 .. 945 TFLOP/s of what they
+// compute).  Tried for dk, dv and not kept:
 // 64 keys a wave with fragments read ahead by hand (408 us), 32 keys with them
 // (321), values in fragments and longer query tiles (289, where the kept form took
 // 281 in the same run; between runs it takes 281 .. 291).

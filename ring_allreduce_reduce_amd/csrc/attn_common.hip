@@ -6,11 +6,6 @@
 
 namespace ringar {
 
-// Blocks that count: of unlike lengths, which the host does not know, a fourth is
-// taken to be missing (3 x 333 x 1501, 20 heads of 64, lengths 1501, 0 and 1434:
-// 15.5 us, planned for whole ones 18.4).
-static int64_t busy(const AttnArgs& a, int64_t blocks) { return a.lengths ? (blocks * 3 + 3) / 4 : blocks; }
-
 // Parts of what the backward kernels' blocks go along, `turns` of 32 rows of
 // `turn` us each: one round of blocks on the 256 CUs after the other, and for
 // parts a second launch and what it reads and writes (`part` bytes each).
@@ -19,7 +14,7 @@ static int splits_for(const AttnArgs& a, int64_t blocks, int64_t turns, double t
   int splits = 1;
   for (int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
     if (s > 1 && s > turns) break;
-    const double rounds = (double)((busy(a, blocks * s) + 255) / 256);
+    const double rounds = (double)((blocks * s + 255) / 256);
     const double us = rounds * (double)((turns + s - 1) / s + 1) * turn + (s > 1 ? 4 + 0.3 * s + s * part * 2 / 4e6 : 0);
     if (best == 0 || us < 0.97 * best) {
       best = us;
@@ -74,7 +69,7 @@ void plan_attn_forward(int dtype, AttnArgs& a) {
     for (int splits : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
       if (splits > 1 && (int64_t)splits * 128 > a.keys) break;
       const double turns = (double)(((int64_t)a.keys + 32 * groups * splits - 1) / (32 * groups * splits));
-      const double rounds = (double)((busy(a, units * splits) + 255) / 256);      // blocks of a CU
+      const double rounds = (double)((units * splits + 255) / 256);      // blocks of a CU
       double work = rounds * turns;
       if (form == kSomeRows) work *= rounds > 1 ? 2.0 : 1.8;
       const double wait = (form != kFewRows ? 0.0 : tiles > 1 ? 0.45 : 0.75) / rounds;
