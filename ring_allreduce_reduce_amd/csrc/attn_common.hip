@@ -54,7 +54,11 @@ static int padded(int dtype, int dim) { return dim <= 64 ? 64 : dtype == kF32 &&
 //   0.034 for each of 64, 96 or 128 columns (one wave a SIMD and two cost the same a turn: the clock drops);
 //   of few rows, each wave's tiles on its own: 0.45 at least where other blocks
 //   read them too, 0.75 where they come from memory;
-//   start and end 5; a second launch 3.5 and 0.3 a part, and the parts' bytes;
+//   start and end 5, of few rows' tiles side by side again for each further round of
+//   blocks, 6 (one block a CU) and 3 at head_dim 64 (two; single tiles wait for
+//   memory, which more blocks hide): 56 x 186 x 330, 4 heads of 64, bf16,
+//   took 19 us in that form, which was chosen without this term, and 12 as
+//   planned now; a second launch 3.5 and 0.3 a part, and the parts' bytes;
 //   keys and values from memory once at 5 TB/s, and to every block at 18.
 void plan_attn_forward(int dtype, AttnArgs& a) {
   const bool wide = dtype == kF32, far = a.dim > 64;
@@ -74,6 +78,7 @@ void plan_attn_forward(int dtype, AttnArgs& a) {
       if (form == kSomeRows) work *= rounds > 1 ? 2.0 : 1.8;
       const double wait = (form != kFewRows ? 0.0 : tiles > 1 ? 0.45 : 0.75) / rounds;
       work *= wait > turn ? wait : turn;
+      if (form == kFewRows && tiles > 1) work += (rounds - 1) * (far ? 6 : 3);
       const double memory = bytes / 5e6 > bytes * tiles / 18e6 ? bytes / 5e6 : bytes * tiles / 18e6;
       double us = 5 + (work > memory ? work : memory);
       if (splits > 1) us += 3.5 + 0.3 * splits + (double)splits * a.rows * a.kv_heads * a.batch * a.dim * 8 / 4e6;
