@@ -95,7 +95,9 @@ template <typename P> ringar_result_t check_sizes(const P* p) {
     return refuse(RINGAR_ERR_INVALID_ARGUMENT, "more than 2^31 - 1025 query rows share a key head");
   if ((unsigned __int128)p->batch * p->heads * p->queries >> 48 || (unsigned __int128)p->batch * p->kv_heads * p->keys >> 48)
     return refuse(RINGAR_ERR_INVALID_ARGUMENT, "more than 2^48 rows");
-  if (!(p->scale > 0.0f) || std::isinf(p->scale)) return refuse(RINGAR_ERR_INVALID_ARGUMENT, "scale must be above zero and finite");
+  // (the kernels' exponentials are base 2)
+  if (!(p->scale > 0.0f) || std::isinf((float)(p->scale * 1.4426950408889634)))
+    return refuse(RINGAR_ERR_INVALID_ARGUMENT, "scale must be above zero and, times log2(e), finite in fp32");
   return RINGAR_SUCCESS;
 }
 
