@@ -710,7 +710,8 @@ ringar_result_t ringar_cross_attention(const ringar_cross_attention_t* args, rin
 
 /* Its gradients, from the forward pass's y and lse.  With dP = dy v^T,
  * delta = sum over head_dim of dy y and dS = P (dP - delta), rounded to a
- * 16-bit dtype before the products that read it:
+ * 16-bit dtype before the products that read it (fp16 holds it times a power of
+ * two that goes by its size, so that small gradients keep their bits):
  *   dq = scale dS k,  dk = scale dS^T q,  dv = P^T dy,
  * summed over the query heads that share a key head; keys past a sequence's
  * length get zeros.  dq (like q), dk and dv (like k) are contiguous; any of

@@ -13,7 +13,8 @@
 //   S and dP have a key a lane.
 // P and dS are the next product's operand as they stand (attn_tile.h), rounded
 // to the operands' type: what the matrix instructions take.  fp16 holds P times
-// 2^10 where it meets dy, so that the small P of long rows keep their bits.
+// 2^10 where it meets dy, so that the small P of long rows keep their bits, and dS
+// times a power of two that goes by its size.
 //
 // Times are medians, ranges two GPUs.  8 x 1024 x 2048, 16 heads of 128, bf16: dq 203
 // .. 208 us, dk and dv 291 .. 301 (991 .. 1017 and 912 .. 945 TFLOP/s of what they
@@ -34,6 +35,20 @@ template <typename T> struct Shift {
 
 // lse in powers of two; +infinity where a row has no keys, so that its P are 0
 __device__ inline float powers_of_two(float lse) { return lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f; }
+
+// dS = P (dP - delta) is as small as P and dy together: in fp16, whose steps below
+// 2^-14 are 2^-24, it would lose most of its bits with dy near 1e-4 and some
+// thousand keys.  So fp16 holds dS times a power of two, which is taken out of the
+// fp32 sums again (both exact).  dq has one for each row, dk one for a wave's 32
+// keys; each kernel says how it is found.  fp16 operands bound dP and delta by 2^39,
+// so dS 2^60 is finite in fp32, and where all dS are 0 the power is that.
+// (8 x 1024 x 2048, 16 heads, fp16, dq and dk with dv, without the powers and with
+// them: head_dim 128 212 / 214 and 327 / 331 us, 64 124 / 124 and 181 / 188.)
+template <typename T> constexpr bool kScaledSlopes = sizeof(T) == 2 && !std::is_same_v<T, __bf16>;
+constexpr int kMostUp = 60;
+__device__ inline float power_of_two(int n) { return __builtin_ldexpf(1.0f, n); }
+// v = m 2^this, m in [1/2, 1); v is finite and not zero
+__device__ inline int exponent_of(float v) { return __builtin_amdgcn_frexp_expf(v); }
 
 // The lane's half of the sum of dy y over a row, in the order of its fragments.
 template <typename Frag, int N> __device__ inline float half_delta(const Frag (&dy)[N], const Frag (&y)[N]) {
@@ -70,6 +85,13 @@ template <typename T> __global__ __launch_bounds__(256) void attn_delta(AttnArgs
 // the vector units.  Four buffers in turn hold a tile from its loads, two turns
 // ahead, to its last product.  delta comes from y's rows, a lane's half of one
 // each, and is left for the other kernel with lse in powers of two.
+//
+// fp16's power of two: P is 1 at most, so a row's dS are bounded by the largest |dP
+// - delta|, which the first tile's 32 keys stand for: below 2^10 there.  A later one
+// 2^6 times as large may overflow, which leaves no column of the row finite: the
+// block then takes its keys again, such rows at 2^-10 of their power, and once more at
+// their natural size.  (Kept out of the loop, where a look for the largest dS and
+// the sums' scaling spilled 116 registers at head_dim 128.)
 template <typename T, int D> struct AttnDq {
   using M = Mma32<T>;
   using Frag = typename M::Frag;
@@ -155,16 +177,47 @@ template <typename T, int D> struct AttnDq {
       dp = M::run(kf[(kMma - 1) % kAhead], dy.f[kSteps - 1], begun_dp);
     };
     constexpr int kEach = 16 / sizeof(T);
+    float times = 1.0f, delta_up = delta;     // what dS is held times, and delta so
     auto slope = [&](Frag* to, int i) {
-      to[i / kEach][i % kEach] = (T)(fast_exp2(fmaf(s[i], a.scale2, -lse2)) * (dp[i] - delta));
+      const float away = kScaledSlopes<T> ? fmaf(dp[i], times, -delta_up) : dp[i] - delta;
+      to[i / kEach][i % kEach] = (T)(fast_exp2(fmaf(s[i], a.scale2, -lse2)) * away);
       if (i % kEach == kEach - 1) asm volatile("" : "+v"(to[i / kEach]));
     };
     auto slopes = [&](int left) {             // of a tile with `left` keys
+      // (computed here: sixteen rows or results kept from before the loop cost registers)
+      int lane_now = lane;
+      asm volatile("" : "+s"(left), "+v"(lane_now));
 #pragma unroll
       for (int i = 0; i < 16; i++) {
         slope(ds, i);
-        if (result_row(i, lane) >= left) ds[i / kEach][i % kEach] = (T)0.0f;
+        if (result_row(i, lane_now) >= left) ds[i / kEach][i % kEach] = (T)0.0f;
       }
+    };
+    auto hold_by_first = [&] {
+      float most = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; i++) most = fmaxf(most, fabsf(dp[i] - delta_up));
+      most = fmaxf(most, __shfl_xor(most, 32));
+      const int up = 10 - (most < INFINITY ? exponent_of(most) : 10);
+      times = power_of_two(most > 0.0f && up < kMostUp ? up : kMostUp);
+      delta_up *= times;
+    };
+    // whether any of the block's lanes says so; what lies in LDS is not needed any more
+    auto any_of_block = [&](bool yes) {
+      uint32_t* said = (uint32_t*)smem;
+      const uint32_t of_wave = __any(yes);
+      wait_lds();
+      block_barrier();
+      if (lane == 0) said[wave] = of_wave;
+      wait_lds();
+      block_barrier();
+      uint32_t all = 0;
+#pragma unroll
+      for (int i = 0; i < NW; i++) all |= said[i];
+      all = __builtin_amdgcn_readfirstlane(all);
+      wait_lds();
+      block_barrier();
+      return all != 0;
     };
     auto nothing = [](int) {};
     auto start = [&](int turn) {
@@ -173,8 +226,15 @@ template <typename T, int D> struct AttnDq {
       issue(turn + 2);
       read.other((turn & 1 ? 3 : 1) * Tile::kPlace);      // on to buffer (turn + 1) % 4
     };
+    // (the lane's row once more: kept over the loop it cost a register)
+    auto row_now = [&] {
+      int lane_now = lane;
+      asm volatile("" : "+v"(lane_now));
+      return (at.tile * NW + wave) * 32 + (lane_now & 31);
+    };
     const int left = at.length - (last - 1) * KT, whole = left < KT ? turns - 1 : turns;
-    if (turns > 0) {
+#pragma unroll 1
+    for (int taken = 0; turns > 0; taken++) {
       issue(0);
       issue(1);
       if (turns > 1) wait_lds<2 * Tile::kLoads>();
@@ -182,6 +242,7 @@ template <typename T, int D> struct AttnDq {
       block_barrier();
       products(kMmaQ, kMma - 2, [] {}, nothing);
       end_scores();
+      if (kScaledSlopes<T> && taken == 0) hold_by_first();
       start(0);
       slopes(turns == 1 ? left : KT);
       if (turns > 1) {
@@ -211,9 +272,29 @@ template <typename T, int D> struct AttnDq {
       }
       read.other((turns & 1 ? 3 : 1) * Tile::kPlace);
       products(0, kMmaQ, [] {}, nothing);
+      if (!kScaledSlopes<T> || taken == 2) break;
+      // (a row whose delta is not finite cannot be helped)
+      const bool over = row_now() < a.rows && fabsf(delta_up) < INFINITY && !(fabsf(acc[0][0]) < INFINITY);
+      if (!any_of_block(over)) break;
+      const float by = !over ? 1.0f : taken == 0 ? 0x1p-10f : times > 1.0f ? power_of_two(1 - exponent_of(times)) : 1.0f;
+      times *= by;
+      delta_up *= by;
+      keys.back(turns);
+      values.back(turns);
+      read.other(((turns + 1) & 3) * Tile::kPlace);         // on to the first buffer
+#pragma unroll
+      for (int i = 0; i < kDims; i++) acc[i] = zero16();
     }
-    if (!exists) return;
-    const int64_t out = (((int64_t)at.batch * a.queries + query) * a.heads + head) * a.dim;
+    const int r_out = row_now();
+    if (r_out >= a.rows) return;
+    if constexpr (kScaledSlopes<T>) {
+      const float down = power_of_two(1 - exponent_of(times));
+#pragma unroll
+      for (int i = 0; i < kDims; i++) acc[i] *= down;
+    }
+    int queries = a.queries;                  // (a divisor of its own, for the same reason)
+    asm volatile("" : "+s"(queries));
+    const int64_t out = (((int64_t)at.batch * queries + r_out % queries) * a.heads + at.kv_head * a.group + r_out / queries) * a.dim;
 #pragma unroll
     for (int i = 0; i < kDims; i++)
 #pragma unroll
@@ -232,6 +313,12 @@ template <typename T, int D> struct AttnDq {
 };
 
 // -------------------------------------------------------------------- dk, dv
+// fp16's power of two: a tile with a dS beyond 2^15 (the first one with any, then)
+// lowers it so that the wave's largest finite one lies below 2^10, and scales what
+// has been added up.  A dS is off by half a step of its own, or by 2^-34 of the largest
+// one that the wave has met.
+constexpr float kMostSlope = 32768.0f;
+
 // VLDS: the block's values lie in LDS, not in fragments (head_dim 128 of 16-bit
 // types, whose sums leave no registers for them).
 template <typename T, int D, int QT, bool VLDS> struct AttnDkv {
@@ -313,6 +400,8 @@ template <typename T, int D, int QT, bool VLDS> struct AttnDkv {
     f32x16 dk[kDims], dv[kDims];
 #pragma unroll
     for (int i = 0; i < kDims; i++) dk[i] = dv[i] = zero16();
+    int up = kMostUp;                                   // fp16 holds dS times 2^up
+    float times = power_of_two(up) * Shift<T>::kBack;
     FragReader<T, QT> read(smem, lane);
     if (first < last) issue(0);
     int buf = 0;
@@ -342,13 +431,36 @@ template <typename T, int D, int QT, bool VLDS> struct AttnDkv {
 #pragma unroll
           for (int e = 0; e < 4; e++) {
             p[j + e] = fast_exp2(fmaf(s[j + e], a.scale2, Shift<T>::kLog2 - l[e]));
-            ds[j + e] = p[j + e] * ((dp[j + e] - delta[e]) * Shift<T>::kBack);
+            ds[j + e] = p[j + e] * (kScaledSlopes<T> ? (dp[j + e] - delta[e]) * times : dp[j + e] - delta[e]);
           }
         }
         if (rows_left < QT) {                 // rows past the end
 #pragma unroll
           for (int j = 0; j < 16; j++)
             if (b * 32 + result_row(j, lane) >= rows_left) p[j] = ds[j] = 0.0f;
+        }
+        if constexpr (kScaledSlopes<T>) {
+          // (a key that does not exist may hold anything)
+          float four[4];
+#pragma unroll
+          for (int j = 0; j < 4; j++) four[j] = fmaxf(fmaxf(fabsf(ds[j]), fabsf(ds[j + 4])), fmaxf(fabsf(ds[j + 8]), fabsf(ds[j + 12])));
+          float most = fmaxf(fmaxf(four[0], four[1]), fmaxf(four[2], four[3]));
+          if (__any(exists && most > kMostSlope)) {
+            most = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 16; j++) most = fabsf(ds[j]) < INFINITY ? fmaxf(most, fabsf(ds[j])) : most;
+            most = exists ? most : 0.0f;
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor(most, o));
+            const int less = __builtin_amdgcn_readfirstlane(most > 1024.0f ? exponent_of(most) - 10 : 0);
+            const float by = power_of_two(-less);
+            up -= less;
+            times *= by;
+#pragma unroll
+            for (int j = 0; j < 16; j++) ds[j] *= by;
+#pragma unroll
+            for (int i = 0; i < kDims; i++) dk[i] *= by;
+          }
         }
         __builtin_amdgcn_sched_barrier(0);
         constexpr int kEach = 16 / sizeof(T);
@@ -365,6 +477,11 @@ template <typename T, int D, int QT, bool VLDS> struct AttnDkv {
       }
     }
     if (key >= a.keys) return;
+    if constexpr (kScaledSlopes<T>) {
+      const float down = power_of_two(-up);
+#pragma unroll
+      for (int i = 0; i < kDims; i++) dk[i] *= down;
+    }
     const int64_t out = (((int64_t)at.batch * a.keys + key) * a.kv_heads + at.kv_head) * a.dim;
 #pragma unroll
     for (int i = 0; i < kDims; i++)

@@ -102,6 +102,10 @@ struct RowStream {
     left -= step;
     return buffer;
   }
+  __device__ inline void back(int tiles) {
+    base -= tiles * step;
+    left += tiles * step;
+  }
 };
 
 // Loads into LDS, 16 bytes a lane, to `to` and (load_lds2) APART bytes on.  The
