@@ -688,7 +688,8 @@ ringar_result_t ringar_dropout(const ringar_dropout_t* args, ringar_stream_t str
  * A row without keys gives zeros, and an lse of -infinity.
  * head_dim is a multiple of 8 (fp32: 4) up to 128; rows start at 16-byte
  * boundaries; row strides are below 2^24 bytes; scale is above zero (and below 2.3e38).  16-bit
- * types round P to their type before it meets v.  An output's span must not
+ * types round P to their type before it meets v (fp16 holds it so that weights of
+ * 2^-24 of the first keys' largest keep their bits).  An output's span must not
  * overlap another operand's. */
 typedef struct {
   ringar_dtype_t dtype;

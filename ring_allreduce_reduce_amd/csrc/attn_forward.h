@@ -13,8 +13,8 @@
 //
 // The first tile gives m.  A later one is taken at the m there is, without a
 // look for its maximum: m is raised, and the tile taken again, only where a
-// lane's exponentials add up to more than 2^12 (every type and the fp32 sums
-// hold those).  So most tiles cost an fma, an exponential, an addition and half
+// lane's exponentials add up to more than 2^12 (fp16: 65504; every type and the fp32
+// sums hold those).  So most tiles cost an fma, an exponential, an addition and half
 // a conversion a score.  And these take the vector units while the products take
 // the matrix units: a wave works on three tiles at once, instruction by
 // instruction, P v of tile t - 1, q k^T of tile t + 1 and the exponentials of t.
@@ -36,7 +36,18 @@
 
 namespace ringar {
 
-constexpr float kMostSum = 4096.0f;
+// fp16 has steps of 2^-24 below 2^-14, and P is 2^-24 of the first tile's largest
+// where a row of a hundred thousand keys looks at one of them and, together, at 1% of
+// the others (as much as there is, where that one's value is zero).  So m is held 10
+// below the largest score, in powers of two: P up to 2^10 then, and 2^-24 of it a normal
+// number.  That leaves 2^6 for later tiles, which scores far apart would often
+// pass; the first that does lifts every row of the wave by 6.  (8 x 1024 x 2048, 16 heads
+// of 128, fp16, without and with this: 149 / 150 us, of queries three times as
+// large 154 / 154, of six times 161 / 161.)
+template <typename T> constexpr bool kHalf = sizeof(T) == 2 && !std::is_same_v<T, __bf16>;
+template <typename T> constexpr float kMostSum = kHalf<T> ? 65504.0f : 4096.0f;
+template <typename T> constexpr float kBelow = kHalf<T> ? 10.0f : 0.0f;
+template <typename T> constexpr float kLift = kHalf<T> ? 6.0f : 0.0f;
 
 template <typename T, int D, int KT, int NQ, int NK> struct AttnForward {
   using M = Mma32<T>;
@@ -105,6 +116,7 @@ __device__ inline void AttnForward<T, D, KT, NQ, NK>::run(const AttnArgs& a, cha
   f32x16 o[kDims];
 #pragma unroll
   for (int i = 0; i < kDims; i++) o[i] = zero16();
+  float below = kBelow<T>;
   float top = -INFINITY, sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};      // of this lane's half of the keys
 
   // The products of a turn, one matrix instruction after the other: P v of the
@@ -145,8 +157,8 @@ __device__ inline void AttnForward<T, D, KT, NQ, NK>::run(const AttnArgs& a, cha
     // (converted here, not where it is used: half the registers)
     if (i % kEach == kEach - 1) asm volatile("" : "+v"(p[i / kEach]));
   };
-  // a tile taken with a look for its maximum; `left` of its keys exist
-  auto raise = [&](f32x16* s, Frag* p, int left) {
+  // a tile taken with a look for its maximum, m raised by `lift` at least; `left` of its keys exist
+  auto raise = [&](f32x16* s, Frag* p, int left, float lift = 0.0f) {
     if (left < KT) {
 #pragma unroll
       for (int b = 0; b < kBlocks; b++)
@@ -157,8 +169,8 @@ __device__ inline void AttnForward<T, D, KT, NQ, NK>::run(const AttnArgs& a, cha
     float most = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kValues; i++) most = fmaxf(most, s[i / 16][i % 16]);
-    most = fmaxf(most, __shfl_xor(most, 32)) * a.scale2;
-    const float raised = fmaxf(top, most), by = raised == -INFINITY ? 1.0f : fast_exp2(top - raised);
+    most = fmaxf(most, __shfl_xor(most, 32)) * a.scale2 - below;
+    const float raised = fmaxf(top + lift, most), by = raised == -INFINITY ? 1.0f : fast_exp2(top - raised);
     top = raised == -INFINITY ? -3e38f : raised;      // (no finite score yet: the first one passes any m of use)
 #pragma unroll
     for (int i = 0; i < 4; i++) sums[i] *= by;
@@ -227,14 +239,16 @@ __device__ inline void AttnForward<T, D, KT, NQ, NK>::run(const AttnArgs& a, cha
                  });
 #pragma unroll
         for (int f = 0; f < kFrags; f++) p[f] = p_next[f];
-        over = __any((part[0] + part[1]) + (part[2] + part[3]) > kMostSum);
+        over = __any((part[0] + part[1]) + (part[2] + part[3]) > kMostSum<T>);
         if (over) break;
 #pragma unroll
         for (int i = 0; i < 4; i++) sums[i] += part[i];
         end_scores(s);
       }
       if (!over) break;
-      raise(s, p, KT);
+      const float lift = below > kBelow<T> - kLift<T> ? kLift<T> : 0.0f;
+      below -= lift;
+      raise(s, p, KT, lift);
       end_scores(s);
     }
     if (mine > 1 && whole < mine) {           // the last tile, with keys that do not exist
