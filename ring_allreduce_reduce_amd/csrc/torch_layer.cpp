@@ -204,12 +204,12 @@ PyObject* dropout(PyObject* const* v) {
   ringar_dropout_t a = {};
   if (!number(v[1], &a.p)) return nullptr;
   a.seed = word(v[2], "seed");
+  const at::Tensor* more = THPVariable_Check(v[3]) ? tensor(v[3], "offset") : nullptr;
   Call call(x, "x");
-  if (THPVariable_Check(v[3])) {
-    const at::Tensor& t = THPVariable_Unpack(v[3]);
-    if (t.scalar_type() != at::kLong || t.numel() != 1 || !t.is_cuda() || t.get_device() != x.get_device())
+  if (more) {
+    if (more->scalar_type() != at::kLong || more->numel() != 1 || !more->is_cuda() || more->get_device() != x.get_device())
       bad("an offset in memory must be one int64 value on x's GPU");
-    a.more_offset = (const int64_t*)t.data_ptr();
+    a.more_offset = (const int64_t*)more->data_ptr();
   } else {
     a.offset = word(v[3], "offset");
   }
