@@ -43,7 +43,7 @@ __device__ inline float powers_of_two(float lse) { return lse == -INFINITY ? INF
 // keys; each kernel says how it is found.  fp16 operands bound dP and delta by 2^39,
 // so dS 2^60 is finite in fp32, and where all dS are 0 the power is that.
 // (8 x 1024 x 2048, 16 heads, fp16, dq and dk with dv, without the powers and with
-// them: head_dim 128 212 / 214 and 327 / 331 us, 64 124 / 124 and 181 / 188.)
+// them: head_dim 128 212 / 214 and 327 / 331 us, 64 124 / 125 and 182 / 186.)
 template <typename T> constexpr bool kScaledSlopes = sizeof(T) == 2 && !std::is_same_v<T, __bf16>;
 constexpr int kMostUp = 60;
 __device__ inline float power_of_two(int n) { return __builtin_ldexpf(1.0f, n); }
@@ -316,7 +316,9 @@ template <typename T, int D> struct AttnDq {
 // fp16's power of two: a tile with a dS beyond 2^15 (the first one with any, then)
 // lowers it so that the wave's largest finite one lies below 2^10, and scales what
 // has been added up.  A dS is off by half a step of its own, or by 2^-34 of the largest
-// one that the wave has met.
+// one that the wave has met.  (The rows' bounds |dy| |v| + |delta| in place of a look at
+// each dS are no faster, 339 and 188 us where this takes 332 and 186, and a key with
+// large values lowers them for keys that hardly look at it.)
 constexpr float kMostSlope = 32768.0f;
 
 // VLDS: the block's values lie in LDS, not in fragments (head_dim 128 of 16-bit
@@ -401,7 +403,7 @@ template <typename T, int D, int QT, bool VLDS> struct AttnDkv {
 #pragma unroll
     for (int i = 0; i < kDims; i++) dk[i] = dv[i] = zero16();
     int up = kMostUp;                                   // fp16 holds dS times 2^up
-    float times = power_of_two(up) * Shift<T>::kBack;
+    float times = exists ? power_of_two(up) * Shift<T>::kBack : 0.0f;      // (keys that do not exist: dS is 0 or NaN)
     FragReader<T, QT> read(smem, lane);
     if (first < last) issue(0);
     int buf = 0;
@@ -440,16 +442,13 @@ template <typename T, int D, int QT, bool VLDS> struct AttnDkv {
             if (b * 32 + result_row(j, lane) >= rows_left) p[j] = ds[j] = 0.0f;
         }
         if constexpr (kScaledSlopes<T>) {
-          // (a key that does not exist may hold anything)
-          float four[4];
+          float most = fmaxf(fabsf(ds[0]), fabsf(ds[1]));
 #pragma unroll
-          for (int j = 0; j < 4; j++) four[j] = fmaxf(fmaxf(fabsf(ds[j]), fabsf(ds[j + 4])), fmaxf(fabsf(ds[j + 8]), fabsf(ds[j + 12])));
-          float most = fmaxf(fmaxf(four[0], four[1]), fmaxf(four[2], four[3]));
-          if (__any(exists && most > kMostSlope)) {
+          for (int j = 2; j < 16; j++) most = fmaxf(most, fabsf(ds[j]));
+          if (__any(most > kMostSlope)) {
             most = 0.0f;
 #pragma unroll
             for (int j = 0; j < 16; j++) most = fabsf(ds[j]) < INFINITY ? fmaxf(most, fabsf(ds[j])) : most;
-            most = exists ? most : 0.0f;
 #pragma unroll
             for (int o = 32; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor(most, o));
             const int less = __builtin_amdgcn_readfirstlane(most > 1024.0f ? exponent_of(most) - 10 : 0);
