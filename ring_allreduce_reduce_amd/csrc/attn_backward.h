@@ -440,6 +440,11 @@ template <typename T, int D, int QT, bool VLDS> struct AttnDkv {
 #pragma unroll
           for (int j = 0; j < 16; j++)
             if (b * 32 + result_row(j, lane) >= rows_left) p[j] = ds[j] = 0.0f;
+          if (b == 0 && a.dy.row < a.dim) {   // (what a wave has read of them so far it has just put away)
+            Tile::clear(smem + buf * kStage + Tile::kPlace, rows_left, wave, lane);
+            wait_lds();
+            block_barrier();
+          }
         }
         if constexpr (kScaledSlopes<T>) {
           float most = fmaxf(fabsf(ds[0]), fabsf(ds[1]));

@@ -260,6 +260,10 @@ __device__ inline void AttnForward<T, D, KT, NQ, NK>::run(const AttnArgs& a, cha
     if (NQ > 1 && NK > 1 && mine > 0 && mine < turns) arrive();
     arrive();
     read.other(Tile::kPlace);
+    if (pitch_v < row_bytes) {
+      if (mine > 0 && left < KT) Tile::clear(buffers + (2 + ((mine - 1) & 1)) * Tile::kPlace, left, wq, lane);
+      arrive();
+    }
     if (mine > 0) products(0, kMmaV, p, kBefore, kNothing);
   }
   float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);

@@ -166,6 +166,16 @@ template <typename T, int D, int R, int NW> struct RowTile {
     for (int i = 0; i + 1 < kLoads; i += 2) load_lds2<NW * 1024>(off[i], off[i + 1], buffer, to + i * NW * 1024);
     if constexpr (kLoads % 2) load_lds(off[kLoads - 1], buffer, to + (kLoads - 1) * NW * 1024);
   }
+  // Zeros from row `from` on, once everything has landed.  Rows that lie over each other
+  // (a stride below the row's length, 0 say) do not end where the buffer does: past
+  // the last row there are values again, and an infinity there, times a weight
+  // of 0, would be NaN.
+  static __device__ inline void clear(char* lds, int from, int wave, int lane) {
+    for (int row = from + wave; row < R; row += NW)
+#pragma unroll
+      for (int i = 0; i < kLines; i++)
+        if (lane < 32) ((uint32_t*)(lds + (i * R + row) * 128))[lane] = 0;
+  }
 };
 
 // The lanes' part of the addresses in LDS at which fragments of a RowTile are
