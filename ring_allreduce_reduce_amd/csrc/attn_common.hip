@@ -60,9 +60,12 @@ static int padded(int dtype, int dim) { return dim <= 64 ? 64 : dtype == kF32 &&
 //   took 19 us in that form, which was chosen without this term, and 12 as
 //   planned now; a second launch 3.5 and 0.3 a part, and the parts' bytes;
 //   keys and values from memory once at 5 TB/s, and to every block at 18.
+// Lengths, which are not known here, count as all keys.  (As three fourths of the
+// bytes, in 40 shapes that this changes: with all keys 0.7% and with three fourths of
+// them 2.8% less time, with a fourth 10% more; .66 .. 1.45 times the time of single ones.)
 void plan_attn_forward(int dtype, AttnArgs& a) {
   const bool wide = dtype == kF32, far = a.dim > 64;
-  const double bytes = (a.lengths ? 1.5 : 2.0) * a.keys * a.kv_heads * a.batch * a.dim * (wide ? 4 : 2);
+  const double bytes = 2.0 * a.keys * a.kv_heads * a.batch * a.dim * (wide ? 4 : 2);
   const double turn = wide ? 0.034 * padded(dtype, a.dim) : far ? 0.46 : 0.33;
   double best = 0;
   for (int form = a.rows <= 32 ? kFewRows : kManyRows; form <= kFewRows; form++) {
