@@ -716,7 +716,8 @@ ringar_result_t ringar_cross_attention(const ringar_cross_attention_t* args, rin
  *   dq = scale dS k,  dk = scale dS^T q,  dv = P^T dy,
  * summed over the query heads that share a key head; keys past a sequence's
  * length get zeros.  dq (like q), dk and dv (like k) are contiguous; any of
- * them may be NULL (not wanted). */
+ * them may be NULL (not wanted; dk and dv are computed together, so one of them
+ * alone takes as long as both). */
 typedef struct {
   ringar_dtype_t dtype;
   int64_t batch, queries, keys, heads, kv_heads, head_dim;

@@ -46,9 +46,10 @@ def cross_attention(q, k, v, *, key_lengths=None, scale=None, stats=False, out=N
 
 
 def cross_attention_backward(dy, q, k, v, y, lse, *, key_lengths=None, scale=None, dq=True, dk=True, dv=True, stream=None):
-    """``(dq, dk, dv)`` of ``cross_attention``; one whose flag is False is not
-    computed and None.  ``y``, ``lse``: the forward pass's; ``key_lengths`` and
-    ``scale`` as there.  Keys past a sequence's length get zeros."""
+    """``(dq, dk, dv)`` of ``cross_attention``; one whose flag is False is None.
+    (dk and dv are computed together: one of them alone takes as long as both.)
+    ``y``, ``lse``: the forward pass's; ``key_lengths`` and ``scale`` as there.
+    Keys past a sequence's length get zeros."""
     ext = block._ext or block._load()
     if stream is None:
         return ext.cross_attention_backward(dy, q, k, v, y, lse, key_lengths, scale, dq, dk, dv)

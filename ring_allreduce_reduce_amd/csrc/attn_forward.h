@@ -25,9 +25,9 @@
 // room, joined by a second launch.
 //
 // Times are medians, ranges two GPUs.  8 x 1024 x 2048, 16 heads of 128, bf16: 138
-// .. 142 us (967 .. 995 TFLOP/s; a large library product reaches 1629).  Counters at 8192 x 16384, 8
-// heads: matrix units busy 68% of the cycles at head_dim 128, vector units 66%
-// at 64; the 68% and the time together make a clock of about 1.5 GHz.  32 tokens
+// .. 142 us (967 .. 995 TFLOP/s; a large library product reaches 1617): matrix units
+// busy 59% of the cycles, vector units 49%, a clock of 1.7 .. 1.9 GHz; of 8192 x 16384, 8
+// heads, 68% at head_dim 128 and 46% (vector units 66%) at 64.  32 tokens
 // on up to 2048 keys each, 32 heads of 128 over 8: 47 us (4.1 TB/s; a large copy
 // 5.1): memory.
 #pragma once

@@ -9,9 +9,9 @@
 // 128 bits, ten rounds of two 32 x 32 bit products, keyed by the seed and
 // counted by (column / 8, row, offset).  A block's 128 bits are the eight
 // 16-bit numbers of eight columns; a value is kept where its number is not
-// below p 2^16.  16 bits, not 32, a value: p is rounded to 2^-17 (and the scale
-// is that rounded p's, so the mean is exact), and the ten rounds then cost
-// less than the memory's time.  Rows count on their own, so a value's number
+// below p 2^16.  16 bits, not 32, a value: p is a multiple of 2^-16, off by 2^-17 at
+// most (and the scale is that p's, so the mean is exact), and the ten rounds then
+// cost less than the memory's time.  Rows count on their own, so a value's number
 // depends on its row and column alone, not on the width, strides or launch.
 // Memory bound: with the residual 16384 x 8192 bf16 157 us (5.1 TB/s).
 #include "layer_types.h"
